@@ -9,6 +9,10 @@ built, importing the binding's entry points raises.
     plan = mfr.Plan(T, H, k, R)
     plan.run(expert_out, permuted_row_of, topk_weights, residual_in,
              residual_out, gamma, eps, out)          # current torch stream
+
+The operators that stand around it in a MoE block (expert sorting, dispatch,
+residual RMSNorm in 8 bits, the gradients) are in layer_ops.py
+(include/moe_layer_ops.h) and under the same names here.
 """
 from __future__ import annotations
 
@@ -25,6 +29,18 @@ __all__ = [
     "run_noalloc", "validate_fused_args", "SF_ROW_MAJOR", "SF_TILED_128x4", "VARIANT_AUTO", "VARIANT_CLUSTER", "VARIANT_ROWS", "VARIANT_STREAM", "STATUS_BAD_INDEX",
     "ERROR_CODES",
 ]
+# the operators around the finalize (layer_ops.py), loaded when first named
+_LAYER_OPS = ("RoutePlan", "DispatchPlan", "FinalizeGradPlan", "ResidualNormPlan", "ResidualNormGradPlan",
+              "QUANT_NONE", "QUANT_TOKEN", "QUANT_GROUP128", "QUANT_MX32", "ROW_PADDING", "ROW_UNUSED")
+__all__ += _LAYER_OPS
+
+
+def __getattr__(name: str):
+    if name in _LAYER_OPS:
+        from . import layer_ops
+        return getattr(layer_ops, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 MFR_OK = 0
 ERROR_CODES = {
@@ -63,7 +79,7 @@ class PlanInfo(ctypes.Structure):
         return d
 
 
-# (name, restype, argtypes) of every symbol the header declares
+# (name, restype, argtypes) of every symbol the headers declare
 _VP, _I64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
     "moe_finalize_rmsnorm_supports": (_I, [_I64, _I]),
@@ -92,6 +108,22 @@ SIGNATURES = {
     "moe_finalize_rmsnorm_destroy": (None, [_VP]),
     "moe_finalize_rmsnorm_strerror": (ctypes.c_char_p, [_I]),
     "moe_finalize_rmsnorm_last_error": (ctypes.c_char_p, []),
+    "moe_op_destroy": (None, [_VP]),
+    "moe_op_get_status": (_I, [_VP, _VP, ctypes.POINTER(_I)]),
+    "moe_op_workspace_bytes": (_I64, [_VP]),
+    "moe_route_plan": (_I, [ctypes.POINTER(_VP), _I64, _I, _I, _I, ctypes.POINTER(Options)]),
+    "moe_route_rows": (_I64, [_VP]),
+    "moe_route_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP]),
+    "moe_dispatch_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, _I, _I64, _I, _I, ctypes.POINTER(Options)]),
+    "moe_dispatch_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_dispatch_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP]),
+    "moe_finalize_grad_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, _I, _I64, _I, ctypes.POINTER(Options)]),
+    "moe_finalize_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_residual_rmsnorm_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, _I, _I, ctypes.POINTER(Options)]),
+    "moe_residual_rmsnorm_sf_bytes": (_I64, [_VP]),
+    "moe_residual_rmsnorm_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP]),
+    "moe_residual_rmsnorm_grad_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, ctypes.POINTER(Options)]),
+    "moe_residual_rmsnorm_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP, _I64, _VP]),
 }
 
 _lib = None

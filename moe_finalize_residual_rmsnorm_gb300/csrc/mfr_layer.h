@@ -1,0 +1,151 @@
+// Declarations shared by the host side of moe_layer_ops.h (mfr_layer_api.cu)
+// and its kernel files.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "mfr_policy.h"
+
+namespace mfr {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxAlign = 4096;
+
+// ---- route (mfr_route.cu) -----------------------------------------------------
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteMaxItems = 16;     // pairs per thread
+constexpr int64_t kRouteBlockPairs = int64_t(kRouteThreads) * kRouteMaxItems;
+
+struct RouteParams {
+    const int32_t* ids;      // [N]
+    int32_t* row_of;         // [N]
+    int32_t* slot_of;        // [R]
+    int32_t* offsets;        // [E + 1]
+    int32_t* counts;         // [E]
+    int32_t* block_counts;   // [blocks, E]: the three-launch form's workspace
+    int* status;
+    int64_t N;
+    int64_t R;
+    int E;
+    int align;
+    int sentinel;
+};
+
+struct RouteLaunch {
+    int cluster;   // CTAs of the one-launch form; 0: the three-launch form
+    int threads;   // per CTA
+    int items;     // pairs per thread
+    int blocks;    // three-launch form: CTAs of the first and last launch
+    int pdl;
+};
+
+cudaError_t route_prepare(const RouteLaunch& l, int E);
+cudaError_t route_launch(const RouteParams& p, const RouteLaunch& l, cudaStream_t s);
+// The outputs of a call without pairs.
+cudaError_t route_empty_launch(const RouteParams& p, int pdl, cudaStream_t s);
+
+// ---- dispatch and the finalize's gradient (mfr_dispatch.cu, mfr_finalize_grad.cu) ----
+struct MapParams {
+    const int32_t* row_of;    // [T, k]
+    const int32_t* slot_of;   // [R]
+    int* status;
+    int64_t T;
+    int64_t R;
+    int k;
+    int sentinel;
+};
+
+struct DispatchParams {
+    MapParams m;
+    const uint8_t* x;         // [T, row_bytes]
+    const uint8_t* sf;        // [T, sf_bytes]
+    uint8_t* out;             // [R, row_bytes]
+    uint8_t* sf_out;          // [R, sf_bytes]
+    int row_bytes;            // a multiple of 16
+    int sf_bytes;
+};
+
+// w[i] = 1 on the default stream: the weights of the dispatch's gradient.
+cudaError_t fill_ones_launch(float* w, int64_t n);
+
+cudaError_t dispatch_launch(const DispatchParams& p, int sms, int pdl, cudaStream_t s);
+
+struct FinalizeGradParams {
+    MapParams m;
+    const void* d_out;          // [T, H] bf16 or fp32
+    const uint16_t* expert_out; // [R, H]
+    const float* w;             // [T, k]
+    uint16_t* d_expert_out;     // [R, H]
+    float* d_w;                 // [T, k]
+    int H;
+    int fp32;
+};
+
+cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, cudaStream_t s);
+
+// ---- residual addition + RMSNorm (mfr_resnorm.cu) --------------------------------
+struct ResNormParams {
+    const uint16_t* x;
+    const float* residual_in;
+    float* residual_out;
+    const uint16_t* gamma;
+    uint16_t* out;       // NULL: none
+    uint8_t* q;
+    void* sf;            // FP32, or E8M0 bytes
+    int64_t T;
+    int H;
+    float eps;
+    int quant;           // MFR_QUANT_*
+    int sf_tiled;
+};
+
+cudaError_t resnorm_launch(const ResNormParams& p, int pdl, cudaStream_t s);
+
+struct ResNormGradParams {
+    const uint16_t* d_out;
+    const float* d_res;   // NULL: zeros
+    const float* r;
+    const uint16_t* gamma;
+    float* d_in;
+    uint16_t* d_x;        // NULL: none
+    float* d_gamma;
+    float* partial;       // [resnorm_grad_partials, H]
+    int64_t T;
+    int H;
+    float eps;
+};
+
+// Rows of the workspace of partial gamma gradients.
+int resnorm_grad_partials(int64_t T, int H, int sms);
+cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s);
+
+// A kernel launch with programmatic stream serialization and a cluster along x, where asked for.
+template <typename... Params, typename... Args>
+cudaError_t layer_launch(void (*kernel)(Params...), int64_t grid, int block, int smem, int cluster, int pdl,
+                         cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(block), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = static_cast<unsigned>(n);
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+}  // namespace mfr
