@@ -91,7 +91,7 @@ int64_t moe_op_workspace_bytes(moe_op_t op);
  * negative and sentinel_skip is 1.
  * The outputs are written whole.  All pointers 4-byte aligned; no two overlap.
  * cluster_size (0 = automatic, else 1, 2, 4, 8 or 16): CTAs of the one-launch
- * form, for up to 16384 pairs a CTA; larger calls take three launches and a
+ * form, for up to 4096 pairs a CTA; larger calls take two launches and a
  * workspace (16-byte aligned).  T == 0 writes expert_offsets and expert_counts
  * (zeros). */
 int moe_route_plan(moe_op_t* op, int64_t T, int k, int E, int align, const mfr_options* opt);

@@ -1,11 +1,16 @@
 // Gradient of the finalize's weighted sum.
 #include "mfr_maps.cuh"
 
+
 namespace mfr {
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kRowsPerWarp = 32;
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void st_row(void* ptr, uint4 v) {
+    asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};"
+                 :: "l"(ptr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 
 template <bool F32>
 __device__ __forceinline__ void load_grad(const void* d_out, int64_t at, float (&g)[8]) {
@@ -19,48 +24,49 @@ __device__ __forceinline__ void load_grad(const void* d_out, int64_t at, float (
     }
 }
 
-// CTA b < T: token b.  CTAs behind: the rows' side of the maps.
+// A token has `wpt` warps of its CTA; thread i of them owns the chunks i, i +
+// 32 wpt, ...  The CTAs before the tokens' look after the rows' side of
+// the maps.
 template <bool F32>
-__global__ void __launch_bounds__(kMaxThreads) finalize_grad_kernel(const FinalizeGradParams p) {
-    __shared__ int s_row[kMaxK];
-    __shared__ float s_w[kMaxK];
-    __shared__ float s_part[kMaxThreads / 32][8];
+__global__ void __launch_bounds__(kThreads, 3) finalize_grad_kernel(const FinalizeGradParams p, const int wpt,
+                                                                    const int row_ctas, const int rpw) {
+    constexpr int kMaxTokens = kThreads / 32;
+    __shared__ int s_row[kMaxTokens][kMaxK];      // -1: the pair has no row
+    __shared__ float s_part[kThreads / 32][8];
     const MapParams& m = p.m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int nck = p.H >> 3;
     pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x >= m.T) {
-        const int64_t r0 = ((blockIdx.x - m.T) * warps + warp) * kRowsPerWarp;
-        if (r0 >= m.R) return;
-        const bool pad = r0 + lane < m.R && row_is_padding(m, r0 + lane);
+    if (blockIdx.x < row_ctas) {
+        const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * warps + warp) * rpw;
+        const bool pad = lane < rpw && r0 + lane < m.R && row_is_padding(m, r0 + lane);
         for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, pad); todo; todo &= todo - 1) {
             uint16_t* row = p.d_expert_out + (r0 + __ffs(todo) - 1) * p.H;
-            for (int c = lane; c < nck; c += 32) st_u4(row + c * 8, make_uint4(0, 0, 0, 0));
+            for (int c = lane; c < nck; c += 32) st_row(row + c * 8, make_uint4(0, 0, 0, 0));
         }
         return;
     }
-    const int64_t t = blockIdx.x;
-    if (tid < m.k) {
-        s_row[tid] = pair_row(m, t, tid, true);
-        s_w[tid] = p.w[t * m.k + tid];
-    }
+    const int mine = warp / wpt, i0 = tid - mine * wpt * 32, nt = wpt * 32;   // this thread's token of the CTA; its place there
+    const int64_t t = static_cast<int64_t>(blockIdx.x - row_ctas) * (warps / wpt) + mine;
+    const bool live = t < m.T;
+    if (live && i0 < m.k) s_row[mine][i0] = pair_row(m, t, i0, true);
     __syncthreads();
     for (int j0 = 0; j0 < m.k; j0 += 8) {
         int row[8];
         float w[8], dot[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            row[j] = j0 + j < m.k ? s_row[j0 + j] : -1;
-            w[j] = j0 + j < m.k ? s_w[j0 + j] : 0.f;
+            row[j] = live && j0 + j < m.k ? s_row[mine][j0 + j] : -1;
+            w[j] = live && j0 + j < m.k ? p.w[t * m.k + j0 + j] : 0.f;
             dot[j] = 0.f;
         }
-        for (int c = tid; c < nck; c += blockDim.x) {
+        for (int c = i0; live && c < nck; c += nt) {
             uint4 v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = row[j] >= 0 ? ld_stream_u4(p.expert_out + static_cast<int64_t>(row[j]) * p.H + c * 8)
-                                   : make_uint4(0, 0, 0, 0);
+                                         : make_uint4(0, 0, 0, 0);
             float g[8];
             load_grad<F32>(p.d_out, t * p.H + c * 8, g);
 #pragma unroll
@@ -70,18 +76,18 @@ __global__ void __launch_bounds__(kMaxThreads) finalize_grad_kernel(const Finali
                 unpack8(v[j], e);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) dot[j] = fmaf(g[q], e[q], dot[j]);
-                const uint4 o = make_uint4(pack_bf16x2(w[j] * g[0], w[j] * g[1]), pack_bf16x2(w[j] * g[2], w[j] * g[3]),
-                                           pack_bf16x2(w[j] * g[4], w[j] * g[5]), pack_bf16x2(w[j] * g[6], w[j] * g[7]));
-                st_u4(p.d_expert_out + static_cast<int64_t>(row[j]) * p.H + c * 8, o);
+                st_row(p.d_expert_out + static_cast<int64_t>(row[j]) * p.H + c * 8,
+                       make_uint4(pack_bf16x2(w[j] * g[0], w[j] * g[1]), pack_bf16x2(w[j] * g[2], w[j] * g[3]),
+                                  pack_bf16x2(w[j] * g[4], w[j] * g[5]), pack_bf16x2(w[j] * g[6], w[j] * g[7])));
             }
         }
         const float sum = warp_reduce_scatter8(dot, lane);
         if ((lane & 3) == 0) s_part[warp][lane >> 2] = sum;
         __syncthreads();
-        if (tid < 8 && j0 + tid < m.k) {
+        if (live && i0 < 8 && j0 + i0 < m.k) {
             float total = 0.f;
-            for (int i = 0; i < warps; ++i) total += s_part[i][tid];
-            p.d_w[t * m.k + j0 + tid] = total;
+            for (int i = 0; i < wpt; ++i) total += s_part[mine * wpt + i][i0];
+            p.d_w[t * m.k + j0 + i0] = total;
         }
         __syncthreads();
     }
@@ -90,14 +96,21 @@ __global__ void __launch_bounds__(kMaxThreads) finalize_grad_kernel(const Finali
 }  // namespace
 
 cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, cudaStream_t s) {
-    (void)sms;
     const int nck = p.H / 8;
-    int block = (nck + 31) / 32 * 32;
-    if (block > 256) block = 256;
-    const int64_t per = static_cast<int64_t>(block / 32) * kRowsPerWarp;
-    const int64_t grid = p.m.T + (p.m.R + per - 1) / per;
-    return p.fp32 ? layer_launch(finalize_grad_kernel<true>, grid, block, 0, 1, pdl, s, p)
-                  : layer_launch(finalize_grad_kernel<false>, grid, block, 0, 1, pdl, s, p);
+    const int rpw = rows_per_warp(p.m.T * nck, sms);
+    int block = kThreads, wpt = 1;
+    if (nck > 64) {
+        const int turns = (nck + kThreads - 1) / kThreads;
+        block = ((nck + turns - 1) / turns + 31) / 32 * 32;
+        wpt = block / 32;
+    } else if (nck > 32) {
+        wpt = 2;
+    }
+    const int64_t tokens = block / 32 / wpt, per = static_cast<int64_t>(block / 32) * rpw;
+    const int row_ctas = static_cast<int>((p.m.R + per - 1) / per);
+    const int64_t grid = row_ctas + (p.m.T + tokens - 1) / tokens;
+    return p.fp32 ? layer_launch(finalize_grad_kernel<true>, grid, block, 0, 1, pdl, s, p, wpt, row_ctas, rpw)
+                  : layer_launch(finalize_grad_kernel<false>, grid, block, 0, 1, pdl, s, p, wpt, row_ctas, rpw);
 }
 
 }  // namespace mfr

@@ -14,8 +14,8 @@ constexpr int kMaxAlign = 4096;
 
 // ---- route (mfr_route.cu) -----------------------------------------------------
 constexpr int kRouteThreads = 1024;
-constexpr int kRouteMaxItems = 16;     // pairs per thread
-constexpr int64_t kRouteBlockPairs = int64_t(kRouteThreads) * kRouteMaxItems;
+constexpr int kRouteMaxItems = 4;                      // one launch: pairs per thread
+constexpr int64_t kRouteOneLaunchPairs = 16 * 1024;    // calls up to here are one launch
 
 struct RouteParams {
     const int32_t* ids;      // [N]
@@ -23,7 +23,7 @@ struct RouteParams {
     int32_t* slot_of;        // [R]
     int32_t* offsets;        // [E + 1]
     int32_t* counts;         // [E]
-    int32_t* block_counts;   // [blocks, E]: the three-launch form's workspace
+    int32_t* block_counts;   // [blocks, E]: the two-launch form's workspace
     int* status;
     int64_t N;
     int64_t R;
@@ -33,15 +33,18 @@ struct RouteParams {
 };
 
 struct RouteLaunch {
-    int cluster;   // CTAs of the one-launch form; 0: the three-launch form
-    int threads;   // per CTA
+    int cluster;   // CTAs of the one-launch form; 0: the two-launch form
+    int threads;   // per CTA, at least E
     int items;     // pairs per thread
-    int blocks;    // three-launch form: CTAs of the first and last launch
-    int pdl;
+    int blocks;    // two-launch form: CTAs of each launch
+    int rounds;    // two-launch form: turns of a CTA
 };
 
-cudaError_t route_prepare(const RouteLaunch& l, int E);
-cudaError_t route_launch(const RouteParams& p, const RouteLaunch& l, cudaStream_t s);
+// Launch geometry for N pairs; forced: CTAs of the one-launch form, or 0.
+RouteLaunch route_choose(int64_t N, int E, int forced, int sms);
+int64_t route_workspace(const RouteLaunch& l, int E);
+cudaError_t route_prepare(const RouteLaunch& l);
+cudaError_t route_launch(const RouteParams& p, const RouteLaunch& l, int pdl, cudaStream_t s);
 // The outputs of a call without pairs.
 cudaError_t route_empty_launch(const RouteParams& p, int pdl, cudaStream_t s);
 
@@ -55,6 +58,19 @@ struct MapParams {
     int k;
     int sentinel;
 };
+
+// Whether `chunks` 16-byte pieces of tokens are 2048 an SM or more: enough for
+// several waves of work, so that bytes count and latency does not.
+inline bool fills_gpu(int64_t chunks, int sms) { return chunks > int64_t(2048) * sms; }
+
+// Rows whose padding one warp looks after.  The warps that do come first in
+// the grid, so that the zeros they write, up to this many rows one after
+// another, are not the call's tail (measured, dispatch of 16384 x 4096 to 8
+// slots, blocks of 128: 209 us with them last, 192 first).  Few rows a warp
+// where that time is most of the call (1024 x 2048, blocks of 16: 12.7 us
+// with 32 rows, 7.4 with 8, 6.7 with 4), more where it hides (16384 x 4096:
+// 192, 193, 196 us).
+inline int rows_per_warp(int64_t chunks, int sms) { return fills_gpu(chunks, sms) ? 32 : 4; }
 
 struct DispatchParams {
     MapParams m;
@@ -111,12 +127,14 @@ struct ResNormGradParams {
     uint16_t* d_x;        // NULL: none
     float* d_gamma;
     float* partial;       // [resnorm_grad_partials, H]
+    int* status;
     int64_t T;
     int H;
     float eps;
 };
 
-// Rows of the workspace of partial gamma gradients.
+// mfr_resnorm_grad.cu: kernel attributes; rows of the workspace of partial gamma gradients.
+cudaError_t resnorm_grad_prepare(int H);
 int resnorm_grad_partials(int64_t T, int H, int sms);
 cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s);
 

@@ -166,6 +166,8 @@ int finish(moe_op_t op, cudaError_t e, void* stream) {
         int st = 0;
         const int rc = moe_op_get_status(op, stream, &st);
         if (rc != MFR_OK) return rc;
+        if (st & MFR_STATUS_TIMEOUT)
+            return MFR_FAIL(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
         if (st & MFR_STATUS_BAD_INDEX) return MFR_FAIL(MFR_ERR_BAD_INDEX, "an expert id or an index map entry was out of range");
     }
     return MFR_OK;
@@ -233,27 +235,9 @@ int moe_route_plan(moe_op_t* op, int64_t T, int k, int E, int align, const mfr_o
     p->E = E;
     p->align = align;
     p->R = R;
-    mfr::RouteLaunch& l = p->route;
-    l.pdl = p->opt.enable_pdl ? 1 : 0;
-    const int forced = p->opt.cluster_size;
-    if (N > mfr::kRouteBlockPairs * 16 || (forced && N > mfr::kRouteBlockPairs * forced)) {
-        l.cluster = 0;
-        l.blocks = static_cast<int>((N + mfr::kRouteBlockPairs - 1) / mfr::kRouteBlockPairs);
-        p->workspace = static_cast<int64_t>(l.blocks) * E * 4;
-    } else {
-        int c = forced ? forced : 1;
-        if (!forced)
-            while (c < 16 && N > static_cast<int64_t>(c) * mfr::kRouteThreads) c *= 2;
-        const int64_t per_cta = (N + c - 1) / c;
-        int threads = static_cast<int>(per_cta < mfr::kRouteThreads ? (per_cta + 31) / 32 * 32 : mfr::kRouteThreads);
-        if (threads < 128) threads = 128;
-        l.cluster = c;
-        l.threads = threads;
-        int items = 1;
-        while (static_cast<int64_t>(items) * threads * c < N) items *= 2;
-        l.items = items;
-    }
-    const cudaError_t e = mfr::route_prepare(l, E);
+    p->route = mfr::route_choose(N, E, p->opt.cluster_size, p->sms);
+    p->workspace = N > 0 ? mfr::route_workspace(p->route, E) : 0;
+    const cudaError_t e = mfr::route_prepare(p->route);
     if (e != cudaSuccess) {
         moe_op_destroy(p);
         *op = nullptr;
@@ -295,7 +279,8 @@ int moe_route_run(moe_op_t op, const int32_t* expert_ids, int32_t* permuted_row_
     p.align = op->align;
     p.sentinel = op->opt.sentinel_skip ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return finish(op, N > 0 ? mfr::route_launch(p, op->route, s) : mfr::route_empty_launch(p, op->route.pdl, s), stream);
+    const int pdl = op->opt.enable_pdl ? 1 : 0;
+    return finish(op, N > 0 ? mfr::route_launch(p, op->route, pdl, s) : mfr::route_empty_launch(p, pdl, s), stream);
 }
 
 // ---- dispatch ------------------------------------------------------------------------
@@ -511,6 +496,12 @@ int moe_residual_rmsnorm_grad_plan(moe_op_t* op, int64_t T, int64_t H, const mfr
     moe_op_s* p = *op;
     p->H = H;
     p->workspace = mfr::resnorm_grad_partials(T, static_cast<int>(H), p->sms) * H * 4;
+    const cudaError_t e = mfr::resnorm_grad_prepare(static_cast<int>(H));
+    if (e != cudaSuccess) {
+        moe_op_destroy(p);
+        *op = nullptr;
+        return fail_cuda(MFR_ERR_CUDA, "kernel attribute setup", e);
+    }
     return MFR_OK;
 }
 
@@ -541,6 +532,7 @@ int moe_residual_rmsnorm_grad_run(moe_op_t op, const void* d_out, const float* d
     p.d_x = static_cast<uint16_t*>(d_x);
     p.d_gamma = d_gamma;
     p.partial = static_cast<float*>(workspace);
+    p.status = op->d_status;
     p.T = op->T;
     p.H = static_cast<int>(op->H);
     p.eps = eps;

@@ -1,4 +1,4 @@
-// Residual addition + RMSNorm with an 8-bit output, and its gradient.
+// Residual addition + RMSNorm with an 8-bit output.
 #include <cfloat>
 
 #include "moe_layer_ops.h"
@@ -10,6 +10,7 @@ namespace {
 
 constexpr float kAmaxFloor = 0x1p-100f;
 constexpr float kE4m3Max = 448.f;
+constexpr int kWarpTokens = 8;
 
 // Two E4M3 codes (nearest even, saturating at 448): lo in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2_rn_sat(float lo, float hi) {
@@ -48,15 +49,18 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     return sum;
 }
 
-// One CTA per token; chunk c (8 columns) belongs to thread c % blockDim.x.
-template <int CPT, int QUANT>
-__global__ void __launch_bounds__(1024) resnorm_kernel(const ResNormParams p) {
+// A token belongs to one CTA, or (WARP) to one warp of a CTA of kWarpTokens
+// warps; chunk c (8 columns) to thread c % nt of its nt threads.
+template <int CPT, int QUANT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpTokens : 1024) resnorm_kernel(const ResNormParams p) {
     __shared__ float s_sum[32];
     __shared__ float s_max[32];
-    const int tid = threadIdx.x, nt = blockDim.x, nck = p.H >> 3;
-    const int64_t t = blockIdx.x, base = t * p.H;
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x, nck = p.H >> 3;
+    const int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpTokens + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t base = t * p.H;
     pdl_wait();
     pdl_launch_dependents();
+    if (WARP && t >= p.T) return;
     float r[CPT][8];
     uint4 g[CPT];
     float ss = 0.f;
@@ -80,7 +84,8 @@ __global__ void __launch_bounds__(1024) resnorm_kernel(const ResNormParams p) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) ss = fmaf(r[i][q], r[i][q], ss);
     }
-    const float inv = rsqrtf(block_sum(ss, s_sum) / static_cast<float>(p.H) + p.eps);
+    ss = WARP ? warp_allreduce_sum(ss) : block_sum(ss, s_sum);
+    const float inv = rsqrtf(ss / static_cast<float>(p.H) + p.eps);
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
@@ -117,9 +122,11 @@ __global__ void __launch_bounds__(1024) resnorm_kernel(const ResNormParams p) {
     }
     if constexpr (QUANT == MFR_QUANT_TOKEN) {
         top = max_over(top, 32);
-        if ((tid & 31) == 0) s_max[tid >> 5] = top;
-        __syncthreads();
-        for (int i = 0; i < nt / 32; ++i) top = fmaxf(top, s_max[i]);
+        if constexpr (!WARP) {
+            if ((tid & 31) == 0) s_max[tid >> 5] = top;
+            __syncthreads();
+            for (int i = 0; i < nt / 32; ++i) top = fmaxf(top, s_max[i]);
+        }
         top = fminf(fmaxf(top, kAmaxFloor), FLT_MAX);
         const float enc = kE4m3Max / top;
 #pragma unroll
@@ -131,154 +138,30 @@ __global__ void __launch_bounds__(1024) resnorm_kernel(const ResNormParams p) {
     }
 }
 
-template <int CPT>
-cudaError_t launch_quant(const ResNormParams& p, int block, int pdl, cudaStream_t s) {
+template <int CPT, bool WARP>
+cudaError_t launch_quant(const ResNormParams& p, int pdl, cudaStream_t s) {
+    const int64_t grid = WARP ? (p.T + kWarpTokens - 1) / kWarpTokens : p.T;
+    const int threads = ((p.H / 8 + CPT - 1) / CPT + 31) / 32 * 32;
+    const int block = WARP ? 32 * kWarpTokens : threads;
     switch (p.quant) {
-        case MFR_QUANT_TOKEN: return layer_launch(resnorm_kernel<CPT, MFR_QUANT_TOKEN>, p.T, block, 0, 1, pdl, s, p);
-        case MFR_QUANT_GROUP128: return layer_launch(resnorm_kernel<CPT, MFR_QUANT_GROUP128>, p.T, block, 0, 1, pdl, s, p);
-        case MFR_QUANT_MX32: return layer_launch(resnorm_kernel<CPT, MFR_QUANT_MX32>, p.T, block, 0, 1, pdl, s, p);
-        default: return layer_launch(resnorm_kernel<CPT, MFR_QUANT_NONE>, p.T, block, 0, 1, pdl, s, p);
+        case MFR_QUANT_TOKEN: return layer_launch(resnorm_kernel<CPT, MFR_QUANT_TOKEN, WARP>, grid, block, 0, 1, pdl, s, p);
+        case MFR_QUANT_GROUP128:
+            return layer_launch(resnorm_kernel<CPT, MFR_QUANT_GROUP128, WARP>, grid, block, 0, 1, pdl, s, p);
+        case MFR_QUANT_MX32: return layer_launch(resnorm_kernel<CPT, MFR_QUANT_MX32, WARP>, grid, block, 0, 1, pdl, s, p);
+        default: return layer_launch(resnorm_kernel<CPT, MFR_QUANT_NONE, WARP>, grid, block, 0, 1, pdl, s, p);
     }
-}
-
-// ---- gradient ------------------------------------------------------------------------
-// Persistent CTAs; a thread owns the same columns of every token, so the
-// gamma gradient is a running sum in its registers, written once per CTA.
-template <int CPT>
-__global__ void __launch_bounds__(1024) resnorm_grad_kernel(const ResNormGradParams p) {
-    __shared__ float2 s_sum[2][32];
-    const int tid = threadIdx.x, nt = blockDim.x, nck = p.H >> 3;
-    const int lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
-    float dg[CPT][8];
-#pragma unroll
-    for (int i = 0; i < CPT; ++i)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) dg[i][q] = 0.f;
-    pdl_wait();
-    pdl_launch_dependents();
-    int turn = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-        const int64_t base = t * p.H;
-        float r[CPT][8], dy[CPT][8], dres[CPT][8];
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int c = tid + i * nt;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) r[i][q] = dy[i][q] = dres[i][q] = 0.f;
-            if (c < nck) {
-                const float4 a = ld_once_f4(p.r + base + c * 8), b = ld_once_f4(p.r + base + c * 8 + 4);
-                unpack8(ld_stream_u4(p.d_out + base + c * 8), dy[i]);
-                if (p.d_res) {
-                    const float4 u = ld_once_f4(p.d_res + base + c * 8), v = ld_once_f4(p.d_res + base + c * 8 + 4);
-                    dres[i][0] = u.x; dres[i][1] = u.y; dres[i][2] = u.z; dres[i][3] = u.w;
-                    dres[i][4] = v.x; dres[i][5] = v.y; dres[i][6] = v.z; dres[i][7] = v.w;
-                }
-                float g[8];
-                unpack8(*reinterpret_cast<const uint4*>(p.gamma + c * 8), g);
-                r[i][0] = a.x; r[i][1] = a.y; r[i][2] = a.z; r[i][3] = a.w;
-                r[i][4] = b.x; r[i][5] = b.y; r[i][6] = b.z; r[i][7] = b.w;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    ss = fmaf(r[i][q], r[i][q], ss);
-                    dot = fmaf(g[q] * dy[i][q], r[i][q], dot);
-                }
-            }
-        }
-        ss = warp_allreduce_sum(ss);
-        dot = warp_allreduce_sum(dot);
-        if (lane == 0) s_sum[turn][warp] = make_float2(ss, dot);
-        __syncthreads();
-        ss = dot = 0.f;
-        for (int i = 0; i < warps; ++i) {
-            ss += s_sum[turn][i].x;
-            dot += s_sum[turn][i].y;
-        }
-        const float n = static_cast<float>(p.H);
-        const float inv = rsqrtf(ss / n + p.eps);
-        const float back = inv * (dot * inv / n);     // times r * inv: no power of inv that could underflow
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int c = tid + i * nt;
-            if (c < nck) {
-                float g[8];
-                unpack8(*reinterpret_cast<const uint4*>(p.gamma + c * 8), g);
-                float d[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float unit = r[i][q] * inv;
-                    d[q] = dres[i][q] + (inv * (g[q] * dy[i][q]) - unit * back);
-                    dg[i][q] = fmaf(dy[i][q], unit, dg[i][q]);
-                }
-                st_f4(p.d_in + base + c * 8, make_float4(d[0], d[1], d[2], d[3]));
-                st_f4(p.d_in + base + c * 8 + 4, make_float4(d[4], d[5], d[6], d[7]));
-                if (p.d_x)
-                    st_u4(p.d_x + base + c * 8, make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]),
-                                                           pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7])));
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-        const int c = tid + i * nt;
-        if (c < nck) {
-            float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.H + c * 8;
-            st_f4(out, make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]));
-            st_f4(out + 4, make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]));
-        }
-    }
-}
-
-// Sum of the partial gamma gradients: a CTA owns 32 columns, warp w the rows w, w + 8, ...
-constexpr int kSumWarps = 8;
-__global__ void __launch_bounds__(32 * kSumWarps) gamma_sum_kernel(const float* partial, int rows, int H, float* d_gamma) {
-    __shared__ float s[kSumWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
-    pdl_wait();
-    pdl_launch_dependents();
-    float sum = 0.f;
-    if (col < H) {
-#pragma unroll 8
-        for (int i = warp; i < rows; i += kSumWarps) sum += partial[static_cast<int64_t>(i) * H + col];
-    }
-    s[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && col < H) {
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kSumWarps; ++i) sum += s[i][lane];
-        d_gamma[col] = sum;
-    }
-}
-
-int chunk_threads(int H, int cpt, int most) {
-    const int nck = H / 8;
-    const int want = ((nck + cpt - 1) / cpt + 31) / 32 * 32;
-    return want < most ? want : most;
 }
 
 }  // namespace
 
 cudaError_t resnorm_launch(const ResNormParams& p, int pdl, cudaStream_t s) {
-    if (p.H <= 8192) return launch_quant<1>(p, chunk_threads(p.H, 1, 1024), pdl, s);
-    return launch_quant<2>(p, chunk_threads(p.H, 2, 1024), pdl, s);
-}
-
-int resnorm_grad_partials(int64_t T, int H, int sms) {
-    const int64_t most = static_cast<int64_t>(sms) * (H <= 4096 ? 2 : 1);
-    return static_cast<int>(T < most ? T : most);
-}
-
-cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s) {
-    const int grid = resnorm_grad_partials(p.T, p.H, sms);
-    cudaError_t e = cudaSuccess;
-    if (grid > 0)
-        e = p.H <= 8192 ? layer_launch(resnorm_grad_kernel<1>, grid, chunk_threads(p.H, 1, 1024), 0, 1, pdl, s, p)
-                        : layer_launch(resnorm_grad_kernel<2>, grid, chunk_threads(p.H, 2, 1024), 0, 1, pdl, s, p);
-    if (e == cudaSuccess)
-        e = layer_launch(gamma_sum_kernel, (p.H + 31) / 32, 32 * kSumWarps, 0, 1, pdl, s, p.partial, grid, p.H, p.d_gamma);
-    return e;
+    if (p.H <= 256) return launch_quant<1, true>(p, pdl, s);
+    if (p.H <= 512) return launch_quant<2, true>(p, pdl, s);
+#ifdef RN2
+    if (p.H > 2048) return launch_quant<2, false>(p, pdl, s);
+#endif
+    if (p.H <= 8192) return launch_quant<1, false>(p, pdl, s);
+    return launch_quant<2, false>(p, pdl, s);
 }
 
 }  // namespace mfr

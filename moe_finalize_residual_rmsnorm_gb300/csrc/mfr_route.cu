@@ -7,17 +7,16 @@
 //   row(s) = offset_{id_s} + #{s' < s : id_s' = id_s},   slot_of[row(s)] = s
 //
 // A pair's rank among its expert's pairs is the sum of four counts, each in
-// pair order, so the result is the stable one whatever the schedule, and no
-// atomic is used: the lanes before it in its warp's round (a match over the
-// warp), the rounds before in its warp (a 16-bit counter per warp and expert
-// in shared memory), the warps before in its CTA (a scan over the warps'
-// counters), and the CTAs before.
+// pair order, so the result is the stable one whatever the schedule: the
+// lanes before it in its warp's round, the rounds before in its warp (a 16-bit
+// counter per warp and expert in shared memory), the warps before in its CTA
+// (a scan over the warps' counters), and the CTAs before.
 //
 // The bytes (12 a pair) are few: 262144 pairs are 3 MB, 0.5 us at the copy
-// rate, so the time is latency, and the one-launch form is one cluster of up
-// to 16 CTAs that exchange their E totals through distributed shared memory
-// instead of three launches.  Past 16384 pairs a CTA three launches count,
-// scan and write.
+// rate, so the time is latency and the counting.  Few pairs are one cluster
+// of CTAs that exchange their E totals through distributed shared memory, in
+// one launch; more are two launches over all SMs, the first of which counts
+// each CTA's pairs and the second sums the counts before its own and writes.
 #include <cooperative_groups.h>
 
 #include "moe_layer_ops.h"
@@ -29,117 +28,137 @@ namespace cg = cooperative_groups;
 namespace mfr {
 namespace {
 
-// Counters of one warp: 16 bits per expert (a CTA holds at most 16384 pairs).
-// The pitch is 2 mod 4 counters, so that the 32 warps' counters of one expert
-// lie in 32 banks.
-__host__ __device__ constexpr int count_pitch(int E) { return (E + 1) / 4 * 4 + 2; }
+// Counters of one warp: 16 bits per expert (a CTA ranks at most 4096 pairs at
+// a time).
+__host__ __device__ constexpr int count_pitch(int E) { return (E + 1) / 2 * 2; }
 
-// Dynamic shared memory: int tot[E], start[E + 1], before[E]; uint16 cnt[warps][pitch].
-int route_smem(int threads, int E) { return (3 * E + 1) * 4 + threads / 32 * count_pitch(E) * 2; }
+// Dynamic shared memory: int tot[E], before[E], all[E], start[E + 1]; uint16 cnt[warps][pitch].
+int route_smem(int threads, int E) { return (4 * E + 1) * 4 + threads / 32 * count_pitch(E) * 2; }
 
 struct RouteShared {
-    int* tot;       // pairs of each expert in this CTA
-    int* start;     // [E + 1] first row of each expert
+    int* tot;       // pairs of each expert among those this CTA ranks
     int* before;    // first row of this CTA's pairs of each expert
+    int* all;       // pairs of each expert in the call
+    int* start;     // [E + 1] first row of each expert
     uint16_t* cnt;  // [warps][pitch]
 };
 
 __device__ __forceinline__ RouteShared route_shared(unsigned char* smem, int E) {
     RouteShared s;
     s.tot = reinterpret_cast<int*>(smem);
-    s.start = s.tot + E;
-    s.before = s.start + E + 1;
-    s.cnt = reinterpret_cast<uint16_t*>(s.before + E);
+    s.before = s.tot + E;
+    s.all = s.before + E;
+    s.start = s.all + E;
+    s.cnt = reinterpret_cast<uint16_t*>(s.start + E + 1);
     return s;
+}
+
+// The expert of pair s, or E: none.
+__device__ __forceinline__ int expert_of(const RouteParams& p, int64_t s, bool& bad) {
+    if (s >= p.N) return p.E;
+    const int32_t e = p.ids[s];
+    if (e >= 0 && e < p.E) return e;
+    bad |= !(p.sentinel && e < 0);
+    return p.E;
 }
 
 // Ranks this CTA's pairs [first, first + threads * I) within the CTA.  Thread
 // order is pair order: warp w holds 32 * I consecutive pairs, lane l the pairs
-// l, 32 + l, ...  On return id[i] is the pair's expert (-1: none), rank[i] its
+// l, 32 + l, ...  On return id[i] is the pair's expert (E: none), rank[i] its
 // rank within its warp, sh.cnt[warp][e] the CTA's pairs of e in earlier warps
 // and sh.tot[e] the CTA's pairs of e; the CTA is synchronised.
+// The lanes of a round with the same expert are found from one ballot per
+// bit of the id: measured on GB300, a match instruction takes 60 cycles of
+// its SM and the 9 ballots of 256 experts 30.
 template <int I>
 __device__ __forceinline__ void rank_pairs(const RouteParams& p, const RouteShared& sh, int64_t first, int (&id)[I],
                                            int (&rank)[I]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int pitch = count_pitch(p.E);
+    const int bits = 32 - __clz(p.E);          // ids are 0 .. E
     const int64_t s0 = first + static_cast<int64_t>(warp) * 32 * I + lane;
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-        const int64_t s = s0 + 32 * i;
-        id[i] = -1;
-        if (s < p.N) {
-            const int32_t e = p.ids[s];
-            const bool ok = e >= 0 && e < p.E;
-            id[i] = ok ? e : -1;
-            bad |= !ok && !(p.sentinel && e < 0);
+    for (int i = 0; i < I; ++i) id[i] = expert_of(p, s0 + 32 * i, bad);
+    uint16_t* mine = sh.cnt + warp * pitch;
+    for (int e = lane; e < pitch / 2; e += 32) reinterpret_cast<uint32_t*>(mine)[e] = 0;
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
+    uint32_t same[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) same[i] = 0xFFFFFFFFu;
+    for (int b = 0; b < bits; ++b) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const bool on = (id[i] >> b) & 1;
+            const uint32_t with = __ballot_sync(0xFFFFFFFFu, on);
+            same[i] &= on ? with : ~with;
         }
     }
-    uint16_t* mine = sh.cnt + warp * pitch;
-    for (int e = lane; e < p.E; e += 32) mine[e] = 0;
-    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[i]);
-        const uint32_t lower = same & ((1u << lane) - 1u);
-        const int base = id[i] >= 0 ? mine[id[i]] : 0;
+        const uint32_t lower = same[i] & ((1u << lane) - 1u);
+        const bool has = id[i] < p.E;
+        const int base = has ? mine[id[i]] : 0;
         rank[i] = base + __popc(lower);
         __syncwarp();
-        if (id[i] >= 0 && lower == 0) mine[id[i]] = static_cast<uint16_t>(base + __popc(same));
+        if (has && lower == 0) mine[id[i]] = static_cast<uint16_t>(base + __popc(same[i]));
         __syncwarp();
     }
     __syncthreads();
-    // exclusive scan over the warps, one expert per warp step, lane = warp
-    for (int e = warp; e < p.E; e += warps) {
-        const int v = lane < warps ? sh.cnt[lane * pitch + e] : 0;
-        int incl = v;
+    // exclusive scan over the warps, a thread per expert, eight loads at a time
+    for (int e = tid; e < p.E; e += blockDim.x) {
+        int run = 0;
+        for (int w0 = 0; w0 < warps; w0 += 8) {
+            int v[8];
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-            if (lane >= off) incl += o;
+            for (int w = 0; w < 8; ++w) v[w] = w0 + w < warps ? sh.cnt[(w0 + w) * pitch + e] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w0 + w < warps) sh.cnt[(w0 + w) * pitch + e] = static_cast<uint16_t>(run);
+                run += v[w];
+            }
         }
-        if (lane < warps) sh.cnt[lane * pitch + e] = static_cast<uint16_t>(incl - v);
-        if (lane == 31) sh.tot[e] = incl;
+        sh.tot[e] = run;
     }
     __syncthreads();
 }
 
-// Exclusive scan by warp 0 of the E padded totals: start[e], and start[E] the
-// rows in all.  total(e) gives an expert's pairs.
-template <typename Total>
-__device__ __forceinline__ void scan_experts(int* start, int E, int align, Total total) {
-    const int lane = threadIdx.x & 31;
-    const int per = (E + 31) / 32;
-    const int e0 = lane * per;
-    int sum = 0;
-    for (int i = 0; i < per; ++i)
-        if (e0 + i < E) sum += (total(e0 + i) + align - 1) / align * align;
-    int incl = sum;
+// start[] from all[], a thread per expert (blockDim.x >= E); the CTA is
+// synchronised on return.
+__device__ __forceinline__ void scan_experts(const RouteParams& p, const RouteShared& sh) {
+    __shared__ int s_warp[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    int v = 0;
+    if (tid < p.E) {
+        v = sh.all[tid];
+        if (p.align > 1) v = (v + p.align - 1) / p.align * p.align;
+    }
+    int incl = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
         if (lane >= off) incl += o;
     }
-    int run = incl - sum;
-    for (int i = 0; i < per; ++i)
-        if (e0 + i < E) {
-            start[e0 + i] = run;
-            run += (total(e0 + i) + align - 1) / align * align;
-        }
-    if (lane == 31) start[E] = incl;
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int base = lane < warp && lane < warps ? s_warp[lane] : 0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) base += __shfl_xor_sync(0xFFFFFFFFu, base, off);
+    if (tid < p.E) sh.start[tid] = base + incl - v;
+    if (tid == p.E - 1) sh.start[p.E] = base + incl;
+    __syncthreads();
 }
 
 // Marks the rows that carry no pair: the padding of each expert's block and
 // the rows behind the last block.  Shared among `n` threads, this one `i`
 // (both in whole warps).
-__device__ __forceinline__ void mark_empty_rows(int32_t* slot_of, int64_t R, int E, const int* start,
-                                                const int32_t* counts, int64_t i, int64_t n) {
+__device__ __forceinline__ void mark_empty_rows(const RouteParams& p, const RouteShared& sh, int64_t i, int64_t n) {
     const int lane = static_cast<int>(i & 31);
-    for (int64_t e = i >> 5; e < E; e += n >> 5)
-        for (int r = start[e] + counts[e] + lane; r < start[e + 1]; r += 32) slot_of[r] = MFR_ROW_PADDING;
-    for (int64_t r = start[E] + i; r < R; r += n) slot_of[r] = MFR_ROW_UNUSED;
+    if (p.align > 1)
+        for (int64_t e = i >> 5; e < p.E; e += n >> 5)
+            for (int r = sh.start[e] + sh.all[e] + lane; r < sh.start[e + 1]; r += 32) p.slot_of[r] = MFR_ROW_PADDING;
+    for (int64_t r = sh.start[p.E] + i; r < p.R; r += n) p.slot_of[r] = MFR_ROW_UNUSED;
 }
 
 template <int I>
@@ -153,7 +172,7 @@ __device__ __forceinline__ void write_maps(const RouteParams& p, const RouteShar
         const int64_t s = s0 + 32 * i;
         if (s >= p.N) continue;
         const int e = id[i];
-        const int row = e >= 0 ? sh.before[e] + mine[e] + rank[i] : -1;
+        const int row = e < p.E ? sh.before[e] + mine[e] + rank[i] : -1;
         p.row_of[s] = row;
         if (row >= 0) p.slot_of[row] = static_cast<int32_t>(s);
     }
@@ -164,111 +183,126 @@ template <int I>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p, const int csize) {
     extern __shared__ __align__(16) unsigned char smem[];
     const RouteShared sh = route_shared(smem, p.E);
-    const int rank_in_cluster = static_cast<int>(blockIdx.x);   // the grid is one cluster
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x * I;
+    const int cta = static_cast<int>(blockIdx.x);   // the grid is one cluster
+    const int64_t first = static_cast<int64_t>(cta) * blockDim.x * I;
     int id[I], rank[I];
     // No early trigger: the maps written here are inputs that a finalize with
     // dependent launch reads before its own wait.
     pdl_wait();
     rank_pairs<I>(p, sh, first, id, rank);
-    int* total = sh.tot;          // pairs of each expert in all CTAs
     if (csize > 1) {
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();                // every CTA's totals are written
-        total = sh.start;         // E + 1 ints; start[] is made from it below, in place
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
             int sum = 0, mine = 0;
             for (int c = 0; c < csize; ++c) {
-                if (c == rank_in_cluster) mine = sum;
+                if (c == cta) mine = sum;
                 sum += cl.map_shared_rank(sh.tot, c)[e];
             }
             sh.before[e] = mine;
-            total[e] = sum;
+            sh.all[e] = sum;
         }
         cl.barrier_arrive();      // this CTA has read the others' totals
-        __syncthreads();
     } else {
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.before[e] = 0;
-        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+            sh.before[e] = 0;
+            sh.all[e] = sh.tot[e];
+        }
     }
-    if (rank_in_cluster == 0)
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.counts[e] = total[e];
-    if (csize > 1) cg::this_cluster().barrier_wait();   // before tot is reused
-    if (total != sh.tot) {
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.tot[e] = total[e];
-        __syncthreads();
+    // scan_experts: thread e reads only its own all[e] before it synchronises
+    scan_experts(p, sh);
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        sh.before[e] += sh.start[e];
+        if (cta == 0) {
+            p.counts[e] = sh.all[e];
+            p.offsets[e] = sh.start[e];
+        }
     }
-    if (threadIdx.x < 32) scan_experts(sh.start, p.E, p.align, [&](int e) { return sh.tot[e]; });
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.before[e] += sh.start[e];
-    if (rank_in_cluster == 0)
-        for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = sh.start[e];
+    if (cta == 0 && threadIdx.x == 0) p.offsets[p.E] = sh.start[p.E];
     __syncthreads();
     write_maps<I>(p, sh, first, id, rank);
-    mark_empty_rows(p.slot_of, p.R, p.E, sh.start, sh.tot,
-                    static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
-                    static_cast<int64_t>(csize) * blockDim.x);
+    mark_empty_rows(p, sh, static_cast<int64_t>(cta) * blockDim.x + threadIdx.x, static_cast<int64_t>(csize) * blockDim.x);
+    if (csize > 1) cg::this_cluster().barrier_wait();   // no CTA leaves while its totals may be read
 }
 
-// ---- three launches --------------------------------------------------------------
-__global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const RouteParams p) {
+// ---- two launches -------------------------------------------------------------------
+// CTA b's pairs are [b, b + 1) * rounds * kRoundPairs.
+constexpr int kRoundItems = 2;
+constexpr int64_t kRoundPairs = int64_t(kRouteThreads) * kRoundItems;
+
+__global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const RouteParams p, const int rounds) {
+    __shared__ int s_count[kMaxExperts];
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) s_count[e] = 0;
+    pdl_wait();
+    // The second launch may start: it reads the ids, which are complete, and
+    // waits for this one before it reads or writes anything else.
+    pdl_launch_dependents();
+    __syncthreads();
+    const int64_t first = blockIdx.x * kRoundPairs * rounds;
+    for (int64_t i = threadIdx.x; i < kRoundPairs * rounds; i += blockDim.x) {
+        bool bad = false;
+        const int e = expert_of(p, first + i, bad);
+        if (e < p.E) atomicAdd(&s_count[e], 1);      // whole numbers: any order gives the same
+        if (bad) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x)
+        p.block_counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = s_count[e];
+}
+
+__global__ void __launch_bounds__(kRouteThreads) route_write_kernel(const RouteParams p, const int rounds) {
     extern __shared__ __align__(16) unsigned char smem[];
     const RouteShared sh = route_shared(smem, p.E);
-    int id[kRouteMaxItems], rank[kRouteMaxItems];
+    const int tid = threadIdx.x;
+    int id[kRoundItems], rank[kRoundItems];
+    int64_t first = blockIdx.x * kRoundPairs * rounds;
+    rank_pairs<kRoundItems>(p, sh, first, id, rank);
     pdl_wait();
-    rank_pairs<kRouteMaxItems>(p, sh, blockIdx.x * kRouteBlockPairs, id, rank);
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-        p.block_counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = sh.tot[e];
-}
-
-// One CTA: block_counts[b][e] becomes the pairs of e before block b; counts and offsets.
-__global__ void __launch_bounds__(kRouteThreads) route_scan_kernel(const RouteParams p, const int blocks) {
-    __shared__ int s_total[kMaxExperts];
-    __shared__ int s_start[kMaxExperts + 1];
-    pdl_wait();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        int run = 0;
-        int b = 0;
-        for (; b + 8 <= blocks; b += 8) {      // eight loads in flight
+    // pairs of each expert in the blocks before, and in all: the blocks'
+    // counts shared among groups of E threads, eight loads at a time
+    const int groups = blockDim.x / p.E, group = tid / p.E, e0 = tid - group * p.E;
+    for (int e = tid; e < p.E; e += blockDim.x) sh.before[e] = sh.all[e] = 0;
+    __syncthreads();
+    if (group < groups) {
+        int before = 0, all = 0;
+        const int blocks = static_cast<int>(gridDim.x), mine = static_cast<int>(blockIdx.x);
+        for (int b0 = group; b0 < blocks; b0 += 8 * groups) {
             int v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = p.block_counts[static_cast<int64_t>(b + i) * p.E + e];
+            for (int i = 0; i < 8; ++i) {
+                const int b = b0 + i * groups;
+                v[i] = b < blocks ? p.block_counts[static_cast<int64_t>(b) * p.E + e0] : 0;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p.block_counts[static_cast<int64_t>(b + i) * p.E + e] = run;
-                run += v[i];
+                all += v[i];
+                if (b0 + i * groups < mine) before += v[i];
             }
         }
-        for (; b < blocks; ++b) {
-            const int v = p.block_counts[static_cast<int64_t>(b) * p.E + e];
-            p.block_counts[static_cast<int64_t>(b) * p.E + e] = run;
-            run += v;
+        atomicAdd(&sh.before[e0], before);
+        atomicAdd(&sh.all[e0], all);
+    }
+    __syncthreads();
+    scan_experts(p, sh);
+    for (int e = tid; e < p.E; e += blockDim.x) {
+        sh.before[e] += sh.start[e];
+        if (blockIdx.x == 0) {
+            p.counts[e] = sh.all[e];
+            p.offsets[e] = sh.start[e];
         }
-        s_total[e] = run;
-        p.counts[e] = run;
     }
+    if (blockIdx.x == 0 && tid == 0) p.offsets[p.E] = sh.start[p.E];
     __syncthreads();
-    if (threadIdx.x < 32) scan_experts(s_start, p.E, p.align, [&](int e) { return s_total[e]; });
-    __syncthreads();
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = s_start[e];
-}
-
-__global__ void __launch_bounds__(kRouteThreads) route_write_kernel(const RouteParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    const RouteShared sh = route_shared(smem, p.E);
-    int id[kRouteMaxItems], rank[kRouteMaxItems];
-    pdl_wait();
-    rank_pairs<kRouteMaxItems>(p, sh, blockIdx.x * kRouteBlockPairs, id, rank);
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) sh.start[e] = p.offsets[e];
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        sh.before[e] = p.offsets[e] + p.block_counts[static_cast<int64_t>(blockIdx.x) * p.E + e];
-        sh.tot[e] = p.counts[e];
+    for (int r = 0;;) {
+        write_maps<kRoundItems>(p, sh, first, id, rank);
+        if (++r == rounds) break;
+        __syncthreads();
+        for (int e = tid; e < p.E; e += blockDim.x) sh.before[e] += sh.tot[e];
+        __syncthreads();
+        first += kRoundPairs;
+        rank_pairs<kRoundItems>(p, sh, first, id, rank);
     }
-    __syncthreads();
-    write_maps<kRouteMaxItems>(p, sh, blockIdx.x * kRouteBlockPairs, id, rank);
-    mark_empty_rows(p.slot_of, p.R, p.E, sh.start, sh.tot,
-                    static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
-                    static_cast<int64_t>(gridDim.x) * blockDim.x);
+    mark_empty_rows(p, sh, static_cast<int64_t>(blockIdx.x) * blockDim.x + tid, static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 __global__ void route_empty_kernel(const RouteParams p) {
@@ -281,8 +315,7 @@ __global__ void route_empty_kernel(const RouteParams p) {
 
 using RouteKernel = void (*)(const RouteParams, int);
 RouteKernel route_kernel_for(int items) {
-    return items <= 1 ? route_kernel<1> : items <= 2 ? route_kernel<2> : items <= 4 ? route_kernel<4>
-         : items <= 8 ? route_kernel<8> : route_kernel<16>;
+    return items <= 1 ? route_kernel<1> : items <= 2 ? route_kernel<2> : route_kernel<4>;
 }
 
 cudaError_t allow_smem(const void* f, int bytes) {
@@ -291,13 +324,36 @@ cudaError_t allow_smem(const void* f, int bytes) {
 
 }  // namespace
 
-cudaError_t route_prepare(const RouteLaunch& l, int) {
+int64_t route_workspace(const RouteLaunch& l, int E) { return l.cluster ? 0 : static_cast<int64_t>(l.blocks) * E * 4; }
+
+RouteLaunch route_choose(int64_t N, int E, int forced, int sms) {
+    RouteLaunch l{};
+    const int c_most = forced ? forced : 16;
+    const bool one = forced ? N <= int64_t(forced) * kRouteThreads * kRouteMaxItems : N <= kRouteOneLaunchPairs;
+    if (!one) {
+        const int64_t want = (N + kRoundPairs - 1) / kRoundPairs, most = 2 * static_cast<int64_t>(sms);
+        const int64_t rounds = (want + most - 1) / most;
+        l.rounds = static_cast<int>(rounds);
+        l.blocks = static_cast<int>((want + rounds - 1) / rounds);
+        return l;
+    }
+    int c = forced ? forced : 1;
+    while (!forced && c < c_most && N > int64_t(c) * kRouteThreads) c *= 2;
+    // a thread per pair and per expert
+    const int64_t pairs = (N + c - 1) / c;
+    int64_t threads = pairs > E ? pairs : E;
+    threads = threads < 128 ? 128 : threads > kRouteThreads ? kRouteThreads : (threads + 31) / 32 * 32;
+    l.cluster = c;
+    l.threads = static_cast<int>(threads);
+    l.items = 1;
+    while (int64_t(l.items) * threads * c < N) l.items *= 2;
+    return l;
+}
+
+cudaError_t route_prepare(const RouteLaunch& l) {
     // the attribute is per kernel, shared by every plan: always the most any plan needs
     const int most = route_smem(kRouteThreads, kMaxExperts);
-    if (l.cluster == 0) {
-        cudaError_t e = allow_smem(reinterpret_cast<const void*>(route_count_kernel), most);
-        return e != cudaSuccess ? e : allow_smem(reinterpret_cast<const void*>(route_write_kernel), most);
-    }
+    if (l.cluster == 0) return allow_smem(reinterpret_cast<const void*>(route_write_kernel), most);
     const void* f = reinterpret_cast<const void*>(route_kernel_for(l.items));
     cudaError_t e = allow_smem(f, most);
     if (e == cudaSuccess && l.cluster > 8)
@@ -305,14 +361,13 @@ cudaError_t route_prepare(const RouteLaunch& l, int) {
     return e;
 }
 
-cudaError_t route_launch(const RouteParams& p, const RouteLaunch& l, cudaStream_t s) {
+cudaError_t route_launch(const RouteParams& p, const RouteLaunch& l, int pdl, cudaStream_t s) {
     if (l.cluster > 0)
-        return layer_launch(route_kernel_for(l.items), l.cluster, l.threads, route_smem(l.threads, p.E), l.cluster, l.pdl,
+        return layer_launch(route_kernel_for(l.items), l.cluster, l.threads, route_smem(l.threads, p.E), l.cluster, pdl,
                             s, p, l.cluster);
-    const int smem = route_smem(kRouteThreads, p.E);
-    cudaError_t e = layer_launch(route_count_kernel, l.blocks, kRouteThreads, smem, 1, l.pdl, s, p);
-    if (e == cudaSuccess) e = layer_launch(route_scan_kernel, 1, kRouteThreads, 0, 1, l.pdl, s, p, l.blocks);
-    if (e == cudaSuccess) e = layer_launch(route_write_kernel, l.blocks, kRouteThreads, smem, 1, l.pdl, s, p);
+    cudaError_t e = layer_launch(route_count_kernel, l.blocks, kRouteThreads, 0, 1, pdl, s, p, l.rounds);
+    if (e == cudaSuccess)
+        e = layer_launch(route_write_kernel, l.blocks, kRouteThreads, route_smem(kRouteThreads, p.E), 1, pdl, s, p, l.rounds);
     return e;
 }
 

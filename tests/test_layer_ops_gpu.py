@@ -88,7 +88,7 @@ def test_route_large(T, k, E, align, kw):
     rng = np.random.default_rng(T)
     ids = rng.integers(-1, E, size=(T, k)).astype(np.int32)
     plan, got = run_route(ids, E, align, sentinel_skip=True, **kw)
-    assert (plan.workspace_bytes() > 0) == (T * k > 262144 or bool(kw))
+    assert plan.workspace_bytes() > 0
     # the reference by a stable argsort: one pair at a time takes too long here
     flat = ids.reshape(-1)
     counts = np.bincount(flat[flat >= 0], minlength=E)
