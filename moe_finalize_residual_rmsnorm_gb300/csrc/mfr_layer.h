@@ -15,7 +15,7 @@ constexpr int kMaxAlign = 4096;
 // ---- route (mfr_route.cu) -----------------------------------------------------
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteMaxItems = 4;                      // one launch: pairs per thread
-constexpr int64_t kRouteOneLaunchPairs = 16 * 1024;    // calls up to here are one launch
+constexpr int64_t kRouteOneLaunchPairs = 32 * 1024;    // calls up to here are one launch
 
 struct RouteParams {
     const int32_t* ids;      // [N]
@@ -40,8 +40,8 @@ struct RouteLaunch {
     int rounds;    // two-launch form: turns of a CTA
 };
 
-// Launch geometry for N pairs; forced: CTAs of the one-launch form, or 0.
-RouteLaunch route_choose(int64_t N, int E, int forced, int sms);
+// Launch geometry for N pairs and R rows; forced: CTAs of the one-launch form, or 0.
+RouteLaunch route_choose(int64_t N, int64_t R, int E, int forced, int sms);
 int64_t route_workspace(const RouteLaunch& l, int E);
 cudaError_t route_prepare(const RouteLaunch& l);
 cudaError_t route_launch(const RouteParams& p, const RouteLaunch& l, int pdl, cudaStream_t s);
@@ -116,7 +116,8 @@ struct ResNormParams {
     int sf_tiled;
 };
 
-cudaError_t resnorm_launch(const ResNormParams& p, int pdl, cudaStream_t s);
+cudaError_t resnorm_prepare(int H, int quant);   // kernel attributes
+cudaError_t resnorm_launch(const ResNormParams& p, int sms, int pdl, cudaStream_t s);
 
 struct ResNormGradParams {
     const uint16_t* d_out;

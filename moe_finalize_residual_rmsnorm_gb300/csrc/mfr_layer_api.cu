@@ -235,7 +235,7 @@ int moe_route_plan(moe_op_t* op, int64_t T, int k, int E, int align, const mfr_o
     p->E = E;
     p->align = align;
     p->R = R;
-    p->route = mfr::route_choose(N, E, p->opt.cluster_size, p->sms);
+    p->route = mfr::route_choose(N, R, E, p->opt.cluster_size, p->sms);
     p->workspace = N > 0 ? mfr::route_workspace(p->route, E) : 0;
     const cudaError_t e = mfr::route_prepare(p->route);
     if (e != cudaSuccess) {
@@ -436,6 +436,12 @@ int moe_residual_rmsnorm_plan(moe_op_t* op, int64_t T, int64_t H, int quant, int
     p->H = H;
     p->quant = quant;
     p->sf_tiled = sf_layout == MFR_SF_TILED_128x4 ? 1 : 0;
+    const cudaError_t e = mfr::resnorm_prepare(static_cast<int>(H), quant);
+    if (e != cudaSuccess) {
+        moe_op_destroy(p);
+        *op = nullptr;
+        return fail_cuda(MFR_ERR_CUDA, "kernel attribute setup", e);
+    }
     return MFR_OK;
 }
 
@@ -483,7 +489,7 @@ int moe_residual_rmsnorm_run(moe_op_t op, const void* x, const float* residual_i
     p.eps = eps;
     p.quant = op->quant;
     p.sf_tiled = op->sf_tiled;
-    return finish(op, mfr::resnorm_launch(p, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
+    return finish(op, mfr::resnorm_launch(p, op->sms, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
 int moe_residual_rmsnorm_grad_plan(moe_op_t* op, int64_t T, int64_t H, const mfr_options* opt) {

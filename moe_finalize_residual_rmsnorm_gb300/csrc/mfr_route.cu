@@ -326,7 +326,7 @@ cudaError_t allow_smem(const void* f, int bytes) {
 
 int64_t route_workspace(const RouteLaunch& l, int E) { return l.cluster ? 0 : static_cast<int64_t>(l.blocks) * E * 4; }
 
-RouteLaunch route_choose(int64_t N, int E, int forced, int sms) {
+RouteLaunch route_choose(int64_t N, int64_t R, int E, int forced, int sms) {
     RouteLaunch l{};
     const int c_most = forced ? forced : 16;
     const bool one = forced ? N <= int64_t(forced) * kRouteThreads * kRouteMaxItems : N <= kRouteOneLaunchPairs;
@@ -338,7 +338,12 @@ RouteLaunch route_choose(int64_t N, int E, int forced, int sms) {
         return l;
     }
     int c = forced ? forced : 1;
-    while (!forced && c < c_most && N > int64_t(c) * kRouteThreads) c *= 2;
+    // Up to 512 pairs one CTA, then 256 a CTA; where blocks are padded, also
+    // enough CTAs to mark 1024 padding rows each.  Measured, us by CTAs:
+    //   512 pairs   1: 2.34   2: 2.85         1024 pairs  2: 3.23   4: 2.87
+    //   8192 pairs  4: 5.5  8: 4.6  16: 3.7   32768 pairs  16: 5.7  two launches: 6.6
+    //   64 pairs, 512 experts, 128-row blocks  1: 5.06   8: 4.63   16: 5.08
+    while (!forced && c < c_most && ((N > 512 && N > c * int64_t(256)) || R - N > c * int64_t(1024))) c *= 2;
     // a thread per pair and per expert
     const int64_t pairs = (N + c - 1) / c;
     int64_t threads = pairs > E ? pairs : E;
