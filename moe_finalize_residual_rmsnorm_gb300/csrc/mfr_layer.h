@@ -23,7 +23,7 @@ struct RouteParams {
     int32_t* slot_of;        // [R]
     int32_t* offsets;        // [E + 1]
     int32_t* counts;         // [E]
-    int32_t* block_counts;   // [blocks, E]: the two-launch form's workspace
+    int32_t* block_counts;   // [blocks, block_pitch(E)]: the two-launch form's workspace
     int* status;
     int64_t N;
     int64_t R;
@@ -40,10 +40,13 @@ struct RouteLaunch {
     int rounds;    // two-launch form: turns of a CTA
 };
 
-// Launch geometry for N pairs and R rows; forced: CTAs of the one-launch form, or 0.
+// Launch geometry for N pairs and R rows; forced: CTAs of the one-launch form,
+// 0: automatic, -1: the two-launch form.
 RouteLaunch route_choose(int64_t N, int64_t R, int E, int forced, int sms);
 int64_t route_workspace(const RouteLaunch& l, int E);
 cudaError_t route_prepare(const RouteLaunch& l);
+// Whether the device holds the one-launch form's cluster.
+bool route_resident(const RouteLaunch& l, int E);
 cudaError_t route_launch(const RouteParams& p, const RouteLaunch& l, int pdl, cudaStream_t s);
 // The outputs of a call without pairs.
 cudaError_t route_empty_launch(const RouteParams& p, int pdl, cudaStream_t s);

@@ -236,8 +236,17 @@ int moe_route_plan(moe_op_t* op, int64_t T, int k, int E, int align, const mfr_o
     p->align = align;
     p->R = R;
     p->route = mfr::route_choose(N, R, E, p->opt.cluster_size, p->sms);
+    cudaError_t e = mfr::route_prepare(p->route);
+    if (e == cudaSuccess && !mfr::route_resident(p->route, E)) {
+        if (p->opt.cluster_size) {
+            moe_op_destroy(p);
+            *op = nullptr;
+            return MFR_FAIL(MFR_ERR_UNSUPPORTED_SHAPE, "a cluster of %d CTAs cannot be resident", opt->cluster_size);
+        }
+        p->route = mfr::route_choose(N, R, E, -1, p->sms);
+        e = mfr::route_prepare(p->route);
+    }
     p->workspace = N > 0 ? mfr::route_workspace(p->route, E) : 0;
-    const cudaError_t e = mfr::route_prepare(p->route);
     if (e != cudaSuccess) {
         moe_op_destroy(p);
         *op = nullptr;
