@@ -20,7 +20,9 @@
  * function returns MFR_OK or an MFR_ERR_* code with its reason in
  * moe_finalize_rmsnorm_last_error(), no run allocates), and:
  *  - Plans (moe_op_t) are made for the current device and belong to one
- *    operator; each run function refuses another operator's plan.
+ *    operator; each run function refuses another operator's plan.  A plan holds
+ *    a 4-byte status word on the device; a dispatch plan that has a gradient
+ *    holds T * k unit weights too.
  *  - mfr_options: enable_pdl, debug_checks and sentinel_skip have the meaning
  *    they have for the finalize, except that these kernels read EVERY input
  *    after waiting on the preceding kernel in the stream, so any input may
@@ -45,9 +47,9 @@
  * moe_dispatch_run and moe_finalize_grad_run read both and write row r for
  * pair s only where permuted_row_of[s] == r and slot_of_row[r] == s.  Any
  * disagreement (an index out of range, two pairs with the same row, a row
- * whose pair points elsewhere) sets MFR_STATUS_BAD_INDEX; nothing is written
- * for it, and its pair's other outputs are 0.  Padding rows are written with zeros, unused rows
- * are left as they were.
+ * whose pair points elsewhere) sets MFR_STATUS_BAD_INDEX; the row is left as it
+ * was, and the pair's weight gradient is 0.  Padding rows are written with
+ * zeros, unused rows are left as they were.
  */
 #ifndef MOE_LAYER_OPS_H
 #define MOE_LAYER_OPS_H

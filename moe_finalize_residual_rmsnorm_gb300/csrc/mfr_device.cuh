@@ -66,6 +66,12 @@ __device__ __forceinline__ void st_u4(void* ptr, uint4 v) {
                  :: "l"(ptr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// A store that leaves L1 alone, for rows that this kernel does not read again.
+__device__ __forceinline__ void st_stream_u4(void* ptr, uint4 v) {
+    asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};"
+                 :: "l"(ptr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // ---- shared-memory barriers and cluster stores ---------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

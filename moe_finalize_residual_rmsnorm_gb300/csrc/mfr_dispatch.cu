@@ -11,23 +11,16 @@
 // behind the segment's own loads.
 //
 // Measured on GB300 at 16384 x 4096 bf16 rows, k = 8, blocks padded to 128
-// rows (1.27 GB): 206 us, 6.2 TB/s, 0.91 of the copy rate of half reads and
-// half writes; a plain fill of as many bytes runs at 4.1 TB/s.  Copies
-// through shared memory (a bulk load and k bulk stores a segment, 4 or 8
-// warps with 2 or 3 stages) took 217 to 221 us.
+// rows (1.27 GB): 189 us, the copy rate of half reads and half writes (a plain
+// fill of as many bytes runs at 0.6 of it).  Copies through shared memory (a
+// bulk load and k bulk stores a segment, 4 or 8 warps with 2 or 3 stages)
+// took 6 % longer.  Stores past L1: 4096 x 8192 bytes 43.8 -> 40.7 us.
 #include "mfr_maps.cuh"
 
 namespace mfr {
 namespace {
 
 constexpr int kThreads = 256;
-// A store that leaves L1 alone: nothing here is read again.  Measured at 4096
-// x 8192 bytes: 40.7 us, 43.8 us with the default policy.
-__device__ __forceinline__ void st_row(void* ptr, uint4 v) {
-    asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};"
-                 :: "l"(ptr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // A row of scales, by one warp.
 __device__ __forceinline__ void copy_scales(const uint8_t* src, uint8_t* dst, int bytes, int lane) {
     if (bytes % 4 == 0) {
@@ -56,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchParams
         const bool pad = lane < rpw && r0 + lane < m.R && row_is_padding(m, r0 + lane);
         for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, pad); todo; todo &= todo - 1) {
             const int64_t r = r0 + __ffs(todo) - 1;
-            for (int c = lane; c < nck; c += 32) st_row(p.out + r * p.row_bytes + c * 16, make_uint4(0, 0, 0, 0));
+            for (int c = lane; c < nck; c += 32) st_stream_u4(p.out + r * p.row_bytes + c * 16, make_uint4(0, 0, 0, 0));
             for (int c = lane; c < p.sf_bytes; c += 32) p.sf_out[r * p.sf_bytes + c] = 0;
         }
         return;
@@ -78,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchParams
         uint8_t* dst = p.out + static_cast<int64_t>(r) * p.row_bytes;
 #pragma unroll
         for (int i = 0; i < C; ++i)
-            if (c0 + 32 * i < nck) st_row(dst + (c0 + 32 * i) * 16, v[i]);
+            if (c0 + 32 * i < nck) st_stream_u4(dst + (c0 + 32 * i) * 16, v[i]);
         if (p.sf_bytes > 0 && seg == segs - 1)
             copy_scales(p.sf + t * p.sf_bytes, p.sf_out + static_cast<int64_t>(r) * p.sf_bytes, p.sf_bytes, lane);
     }

@@ -1,16 +1,26 @@
-// Gradient of the finalize's weighted sum.
+// Gradient of the finalize's weighted sum, for the pairs (t, j) that have a row r:
+//
+//   d_expert_out[r, h]   = bf16( w[t, j] * d_out[t, h] )
+//   d_topk_weights[t, j] = sum_h d_out[t, h] * expert_out[r, h]
+//
+// Both come from one pass: a token's gradient is read once and, chunk by chunk
+// in registers, multiplied into its k rows, while the k rows' dot products
+// run beside.  It reads a row and writes a row per pair (2.35 GB at 16384 x
+// 4096, k = 8), so bytes bound it, and what counts is that enough of them are
+// in flight: eight 16-byte row loads a thread, three CTAs of 256 threads an SM
+// (measured at that size: 345 us, 1.01 of the copy rate; two CTAs with more
+// registers 430 to 630 us, four with fewer 380 us; 512 threads a CTA 432 us).
+// Rows are written past L1.  The dot products are summed per thread in column
+// order, over the lanes by a reduce-scatter butterfly and over the warps in
+// order, all in FP32, so a call gives the same bits every time; a row's
+// gradient is rounded once, from the FP32 product to bf16, the type of the rows
+// that the experts' GEMMs take their gradients in.
 #include "mfr_maps.cuh"
-
 
 namespace mfr {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ void st_row(void* ptr, uint4 v) {
-    asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};"
-                 :: "l"(ptr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
 
 template <bool F32>
 __device__ __forceinline__ void load_grad(const void* d_out, int64_t at, float (&g)[8]) {
@@ -43,7 +53,7 @@ __global__ void __launch_bounds__(kThreads, 3) finalize_grad_kernel(const Finali
         const bool pad = lane < rpw && r0 + lane < m.R && row_is_padding(m, r0 + lane);
         for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, pad); todo; todo &= todo - 1) {
             uint16_t* row = p.d_expert_out + (r0 + __ffs(todo) - 1) * p.H;
-            for (int c = lane; c < nck; c += 32) st_row(row + c * 8, make_uint4(0, 0, 0, 0));
+            for (int c = lane; c < nck; c += 32) st_stream_u4(row + c * 8, make_uint4(0, 0, 0, 0));
         }
         return;
     }
@@ -76,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 3) finalize_grad_kernel(const Finali
                 unpack8(v[j], e);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) dot[j] = fmaf(g[q], e[q], dot[j]);
-                st_row(p.d_expert_out + static_cast<int64_t>(row[j]) * p.H + c * 8,
+                st_stream_u4(p.d_expert_out + static_cast<int64_t>(row[j]) * p.H + c * 8,
                        make_uint4(pack_bf16x2(w[j] * g[0], w[j] * g[1]), pack_bf16x2(w[j] * g[2], w[j] * g[3]),
                                   pack_bf16x2(w[j] * g[4], w[j] * g[5]), pack_bf16x2(w[j] * g[6], w[j] * g[7])));
             }
@@ -97,6 +107,9 @@ __global__ void __launch_bounds__(kThreads, 3) finalize_grad_kernel(const Finali
 
 cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, cudaStream_t s) {
     const int nck = p.H / 8;
+    // One token a CTA, whose threads divide its chunks evenly (333 x 2056,
+    // 257 chunks: 160 threads twice, 5.2 us; 256 threads, of which one has a
+    // second chunk, 6.3 us); narrow rows share a CTA.
     const int rpw = rows_per_warp(p.m.T * nck, sms);
     int block = kThreads, wpt = 1;
     if (nck > 64) {

@@ -3,6 +3,9 @@
 //   r = residual + x,  y = r * rsqrt(mean(r^2) + eps) * gamma,
 //   a group's scale from its largest |y|,  q = E4M3(y / scale)
 //
+// y is quantised from its FP32 value, not from its bf16 rounding, so that each
+// code carries one rounding.
+//
 // One pass over DRAM: a token's r stays on the chip from its sum to its
 // output, so bytes bound it (2 + 4 read, 4 + 1 (+ 2) written an element) and
 // one CTA per token is enough, as long as several are resident on an SM, each
@@ -54,8 +57,9 @@ __device__ __forceinline__ float max_over(float v, int lanes) {
     return v;
 }
 
-// E8M0 byte of the smallest power of two 2^(byte - 127) with amax / 2^.. <= 448 = 1.75 * 2^8,
-// for amax in [2^-100, FLT_MAX]: from amax = m * 2^x, 1 <= m < 2, the exponent x - 8, one more where m > 1.75.
+// E8M0 byte of the smallest power of two 2^(byte - 127) that brings amax, in
+// [2^-100, FLT_MAX], to 448 = 1.75 * 2^8 or below: from amax = m * 2^x, 1 <= m <
+// 2, the exponent x - 8, one more where m > 1.75.
 __device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
     const uint32_t u = __float_as_uint(amax);
     return (u >> 23) - 8u + ((u & 0x7FFFFFu) > 0x600000u ? 1u : 0u);
@@ -77,7 +81,8 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
 // c % nt of its nt threads (SPLIT: of CTA c / nt).  A group of columns lies in
 // consecutive lanes of one warp, 16 or 4 of them.
 template <int CPT, int QUANT, bool WARP, bool SPLIT = false>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpTokens : 512, WARP ? 1 : CPT == 1 ? 4 : 3) resnorm_kernel(const ResNormParams p, const int csize) {
+__global__ void __launch_bounds__(WARP ? 32 * kWarpTokens : 512, WARP ? 1 : CPT == 1 ? 4 : 3)
+resnorm_kernel(const ResNormParams p, const int csize) {
     __shared__ float s_sum[32];
     __shared__ float s_max[32];
     __shared__ float s_split[2][16];      // SPLIT: every CTA's sum and largest magnitude

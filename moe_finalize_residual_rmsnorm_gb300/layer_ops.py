@@ -224,7 +224,7 @@ class ResidualNormPlan(_OpPlan):
                    debug_checks=debug_checks)
 
     def sf_shape(self) -> tuple:
-        """Shape of out_sf: FP32 [T], FP32 [T, ceil(H/128)], uint8 [T, ceil(H/32)], or the bytes of the tiled layout."""
+        """Shape of out_sf: FP32 [T, 1], FP32 [T, ceil(H/128)], uint8 [T, ceil(H/32)], or the bytes of the tiled layout."""
         T, S = self.T, -(-self.H // 32)
         if self.quant == QUANT_MX32 and self.sf_layout == SF_TILED_128x4:
             return (-(-T // 128) * 128 * (-(-S // 4) * 4),)
