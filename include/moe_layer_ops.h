@@ -21,8 +21,7 @@
  * moe_finalize_rmsnorm_last_error(), no run allocates), and:
  *  - Plans (moe_op_t) are made for the current device and belong to one
  *    operator; each run function refuses another operator's plan.  A plan holds
- *    a 4-byte status word on the device; a dispatch plan that has a gradient
- *    holds T * k unit weights too.
+ *    a 4-byte status word on the device and nothing else there.
  *  - mfr_options: enable_pdl, debug_checks and sentinel_skip have the meaning
  *    they have for the finalize, except that these kernels read EVERY input
  *    after waiting on the preceding kernel in the stream, so any input may
@@ -119,9 +118,12 @@ int moe_dispatch_plan(moe_op_t* op, int64_t T, int64_t H, int k, int64_t R, int 
 int moe_dispatch_run(moe_op_t op, const void* x, const void* sf, const int32_t* permuted_row_of,
                      const int32_t* slot_of_row, void* rows_out, void* sf_out, void* stream);
 
-/* Its gradient, for bf16 plans (elem_bytes = 2 and sf_bytes = 0) with H % 8 == 0:
+/* Its gradient, for bf16 rows (plans with elem_bytes = 2 and sf_bytes = 0):
  *   d_x[t, :] = bf16( sum_j d_rows[permuted_row_of[t, j], :] )
- * summed in FP32 in slot order.  Rows outside [0, R) as in moe_finalize_run. */
+ * summed in FP32 in slot order.  A pair whose entry lies outside [0, R) adds
+ * nothing and sets MFR_STATUS_BAD_INDEX, unless it is negative and
+ * sentinel_skip is 1.  d_rows and d_x bf16, 16-byte aligned; d_x overlaps no
+ * input. */
 int moe_dispatch_grad_run(moe_op_t op, const void* d_rows, const int32_t* permuted_row_of, void* d_x, void* stream);
 
 /* ---- gradient of the finalize's weighted sum --------------------------------

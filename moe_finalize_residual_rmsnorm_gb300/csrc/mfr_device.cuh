@@ -43,6 +43,18 @@ __device__ __forceinline__ uint4 ld_stream_u4(const void* ptr) {
     return v;
 }
 
+// The same where `take`, else zeros: a predicated load, so that several of them
+// stay in flight where branches would take them one by one.
+__device__ __forceinline__ uint4 ld_stream_u4_if(const void* ptr, bool take) {
+    uint4 v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                 "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                 "@p ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+                 : "l"(ptr), "r"(static_cast<uint32_t>(take)));
+    return v;
+}
+
 // 16 bytes of data this kernel may also write (the residual, in place).
 __device__ __forceinline__ float4 ld_once_f4(const float* ptr) {
     float4 v;

@@ -7,9 +7,12 @@
 // in registers, multiplied into its k rows, while the k rows' dot products
 // run beside.  It reads a row and writes a row per pair (2.35 GB at 16384 x
 // 4096, k = 8), so bytes bound it, and what counts is that enough of them are
-// in flight: eight 16-byte row loads a thread, three CTAs of 256 threads an SM
-// (measured at that size: 345 us, 1.01 of the copy rate; two CTAs with more
-// registers 430 to 630 us, four with fewer 380 us; 512 threads a CTA 432 us).
+// in flight: eight 16-byte row loads a thread (with few slots from two chunks,
+// k = 2 at 16384 x 4096: 126 us with one, 99 with two; with more than eight
+// slots sixteen loads and two CTAs of 256 threads an SM, k = 16: 653 us, 820 in
+// two groups of eight), and 768 threads an SM (measured at k = 8: 344 us, 1.01
+// of the copy rate; with 512 threads and more registers 430 us and more, with
+// 1024 and fewer 380).
 // Rows are written past L1.  The dot products are summed per thread in column
 // order, over the lanes by a reduce-scatter butterfly and over the warps in
 // order, all in FP32, so a call gives the same bits every time; a row's
@@ -34,15 +37,15 @@ __device__ __forceinline__ void load_grad(const void* d_out, int64_t at, float (
     }
 }
 
-// A token has `wpt` warps of its CTA; thread i of them owns the chunks i, i +
-// 32 wpt, ...  The CTAs before the tokens' look after the rows' side of
-// the maps.
-template <bool F32>
-__global__ void __launch_bounds__(kThreads, 3) finalize_grad_kernel(const FinalizeGradParams p, const int wpt,
-                                                                    const int row_ctas, const int rpw) {
-    constexpr int kMaxTokens = kThreads / 32;
-    __shared__ int s_row[kMaxTokens][kMaxK];      // -1: the pair has no row
-    __shared__ float s_part[kThreads / 32][8];
+// One token a CTA, thread i of it the chunks i, i + blockDim.x, ... of the
+// token's rows, U of them at a time; SG: slots at most.  The row_ctas CTAs
+// before the tokens' look after the rows' side of the maps, `rpw` rows a warp.
+template <bool F32, int SG, int U>
+__global__ void __launch_bounds__(kThreads, SG > 8 ? 2 : 3) finalize_grad_kernel(const FinalizeGradParams p, const int row_ctas,
+                                                                                   const int rpw) {
+    __shared__ int s_row[kMaxK];      // -1: the pair has no row
+    __shared__ float s_w[kMaxK];
+    __shared__ float s_part[kThreads / 32][SG > 8 ? 16 : 8];
     const MapParams& m = p.m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int nck = p.H >> 3;
@@ -57,73 +60,94 @@ __global__ void __launch_bounds__(kThreads, 3) finalize_grad_kernel(const Finali
         }
         return;
     }
-    const int mine = warp / wpt, i0 = tid - mine * wpt * 32, nt = wpt * 32;   // this thread's token of the CTA; its place there
-    const int64_t t = static_cast<int64_t>(blockIdx.x - row_ctas) * (warps / wpt) + mine;
-    const bool live = t < m.T;
-    if (live && i0 < m.k) s_row[mine][i0] = pair_row(m, t, i0, true);
+    const int64_t t = blockIdx.x - row_ctas;
+    if (tid < m.k) {
+        s_row[tid] = pair_row(m, t, tid, true);
+        s_w[tid] = p.w[t * m.k + tid];
+    }
+    float dot[SG > 8 ? 16 : 8];
+#pragma unroll
+    for (int j = 0; j < (SG > 8 ? 16 : 8); ++j) dot[j] = 0.f;
     __syncthreads();
-    for (int j0 = 0; j0 < m.k; j0 += 8) {
-        int row[8];
-        float w[8], dot[8];
+    for (int c0 = tid; c0 - tid < nck; c0 += U * blockDim.x) {     // as many turns for every thread
+        uint4 v[SG][U];
+        float g[U][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            row[j] = live && j0 + j < m.k ? s_row[mine][j0 + j] : -1;
-            w[j] = live && j0 + j < m.k ? p.w[t * m.k + j0 + j] : 0.f;
-            dot[j] = 0.f;
-        }
-        for (int c = i0; live && c < nck; c += nt) {
-            uint4 v[8];
+        for (int j = 0; j < SG; ++j) {
+            const int row = j < m.k ? s_row[j] : -1;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = row[j] >= 0 ? ld_stream_u4(p.expert_out + static_cast<int64_t>(row[j]) * p.H + c * 8)
-                                         : make_uint4(0, 0, 0, 0);
-            float g[8];
-            load_grad<F32>(p.d_out, t * p.H + c * 8, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (row[j] < 0) continue;
-                float e[8];
-                unpack8(v[j], e);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) dot[j] = fmaf(g[q], e[q], dot[j]);
-                st_stream_u4(p.d_expert_out + static_cast<int64_t>(row[j]) * p.H + c * 8,
-                       make_uint4(pack_bf16x2(w[j] * g[0], w[j] * g[1]), pack_bf16x2(w[j] * g[2], w[j] * g[3]),
-                                  pack_bf16x2(w[j] * g[4], w[j] * g[5]), pack_bf16x2(w[j] * g[6], w[j] * g[7])));
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * blockDim.x;
+                if (row >= 0 && c < nck) v[j][u] = ld_stream_u4(p.expert_out + static_cast<int64_t>(row) * p.H + c * 8);
             }
         }
-        const float sum = warp_reduce_scatter8(dot, lane);
-        if ((lane & 3) == 0) s_part[warp][lane >> 2] = sum;
-        __syncthreads();
-        if (live && i0 < 8 && j0 + i0 < m.k) {
-            float total = 0.f;
-            for (int i = 0; i < wpt; ++i) total += s_part[mine * wpt + i][i0];
-            p.d_w[t * m.k + j0 + i0] = total;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * blockDim.x < nck) load_grad<F32>(p.d_out, t * p.H + (c0 + u * blockDim.x) * 8, g[u]);
+#pragma unroll
+        for (int j = 0; j < SG; ++j) {
+            const int row = j < m.k ? s_row[j] : -1;
+            if (row < 0) continue;
+            const float w = s_w[j];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * blockDim.x;
+                if (c >= nck) continue;
+                float e[8];
+                unpack8(v[j][u], e);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) dot[j] = fmaf(g[u][q], e[q], dot[j]);
+                st_stream_u4(p.d_expert_out + static_cast<int64_t>(row) * p.H + c * 8,
+                             make_uint4(pack_bf16x2(w * g[u][0], w * g[u][1]), pack_bf16x2(w * g[u][2], w * g[u][3]),
+                                        pack_bf16x2(w * g[u][4], w * g[u][5]), pack_bf16x2(w * g[u][6], w * g[u][7])));
+            }
         }
-        __syncthreads();
     }
+#pragma unroll
+    for (int a = 0; a < (SG > 8 ? 2 : 1); ++a) {
+        float d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = dot[a * 8 + j];
+        const float sum = warp_reduce_scatter8(d, lane);
+        if ((lane & 3) == 0) s_part[warp][a * 8 + (lane >> 2)] = sum;
+    }
+    __syncthreads();
+    if (tid < m.k) {
+        float total = 0.f;
+        for (int i = 0; i < warps; ++i) total += s_part[i][tid];
+        p.d_w[t * m.k + tid] = total;
+    }
+}
+
+using GradKernel = void (*)(const FinalizeGradParams, int, int);
+
+template <bool F32>
+GradKernel kernel_for(int k) {
+    return k <= 2 ? finalize_grad_kernel<F32, 2, 2> : k <= 4 ? finalize_grad_kernel<F32, 4, 2>
+         : k <= 8 ? finalize_grad_kernel<F32, 8, 1> : finalize_grad_kernel<F32, 16, 1>;
 }
 
 }  // namespace
 
 cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, cudaStream_t s) {
     const int nck = p.H / 8;
-    // One token a CTA, whose threads divide its chunks evenly (333 x 2056,
-    // 257 chunks: 160 threads twice, 5.2 us; 256 threads, of which one has a
-    // second chunk, 6.3 us); narrow rows share a CTA.
-    const int rpw = rows_per_warp(p.m.T * nck, sms);
-    int block = kThreads, wpt = 1;
-    if (nck > 64) {
-        const int turns = (nck + kThreads - 1) / kThreads;
-        block = ((nck + turns - 1) / turns + 31) / 32 * 32;
-        wpt = block / 32;
-    } else if (nck > 32) {
-        wpt = 2;
-    }
-    const int64_t tokens = block / 32 / wpt, per = static_cast<int64_t>(block / 32) * rpw;
+    // A CTA's threads divide a token's chunks evenly: no turn in which a few
+    // have one (333 x 2056, 257 chunks: 160 threads twice, 5.2 us; 256 threads,
+    // of which one has a second, 6.3).  Where tokens are plenty, smaller CTAs of more
+    // turns: the more CTAs an SM holds, the less the phases of each show
+    // (16384 x 4096, us by turns: k = 8 2: 340, 4: 335; k = 3 4: 152, 8: 145; k =
+    // 16 2: 677, 4: 653), but two warps at least for five rows or more (32768 x
+    // 1024, k = 8: one warp 177, two 172).
+    int turns = (nck + kThreads - 1) / kThreads;
+    const int least = p.m.k <= 4 ? 8 : 4;
+    if (p.m.T > 12 * static_cast<int64_t>(sms) && turns < least) turns = least;
+    int block = ((nck + turns - 1) / turns + 31) / 32 * 32;
+    if (p.m.k > 4 && block < 64 && nck > 32) block = 64;
+    const int rpw = rows_per_warp(p.m.T, sms);
+    const int64_t per = static_cast<int64_t>(block / 32) * rpw;
     const int row_ctas = static_cast<int>((p.m.R + per - 1) / per);
-    const int64_t grid = row_ctas + (p.m.T + tokens - 1) / tokens;
-    return p.fp32 ? layer_launch(finalize_grad_kernel<true>, grid, block, 0, 1, pdl, s, p, wpt, row_ctas, rpw)
-                  : layer_launch(finalize_grad_kernel<false>, grid, block, 0, 1, pdl, s, p, wpt, row_ctas, rpw);
+    return layer_launch(p.fp32 ? kernel_for<true>(p.m.k) : kernel_for<false>(p.m.k), row_ctas + p.m.T, block, 0, 1, pdl, s, p,
+                        row_ctas, rpw);
 }
 
 }  // namespace mfr

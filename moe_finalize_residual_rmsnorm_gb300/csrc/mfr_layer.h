@@ -66,14 +66,16 @@ struct MapParams {
 // several waves of work, so that bytes count and latency does not.
 inline bool fills_gpu(int64_t chunks, int sms) { return chunks > int64_t(2048) * sms; }
 
-// Rows whose padding one warp looks after.  The warps that do come first in
-// the grid, so that the zeros they write, up to this many rows one after
-// another, are not the call's tail (measured, dispatch of 16384 x 4096 to 8
-// slots, blocks of 128: 209 us with them last, 192 first).  Few rows a warp
-// where that time is most of the call (1024 x 2048, blocks of 16: 12.7 us
-// with 32 rows, 7.4 with 8, 6.7 with 4), more where it hides (16384 x 4096:
-// 192, 193, 196 us).
-inline int rows_per_warp(int64_t chunks, int sms) { return fills_gpu(chunks, sms) ? 32 : 4; }
+// Rows whose padding one warp looks after: half as many as there are tokens an
+// SM, 1 to 32.  The warps that do come first in the grid, so that the zeros they write, row after row, are not the
+// call's tail (measured, dispatch of 16384 x 4096 to 8 slots, blocks of 128:
+// 209 us with them last, 192 first), and a small call has many of them (1024 x
+// 2048, blocks of 16: 12.7 us with 32 rows, 7.4 with 8, 6.7 with 4; 16384 x
+// 4096: 192, 193, 196 us).
+inline int rows_per_warp(int64_t T, int sms) {
+    const int64_t rows = T / (2 * static_cast<int64_t>(sms));
+    return rows < 1 ? 1 : rows > 32 ? 32 : static_cast<int>(rows);
+}
 
 struct DispatchParams {
     MapParams m;
@@ -85,10 +87,15 @@ struct DispatchParams {
     int sf_bytes;
 };
 
-// w[i] = 1 on the default stream: the weights of the dispatch's gradient.
-cudaError_t fill_ones_launch(float* w, int64_t n);
+struct DispatchGradParams {
+    MapParams m;              // slot_of: not read
+    const uint16_t* d_rows;   // [R, H]
+    uint16_t* d_x;            // [T, H]
+    int H;
+};
 
 cudaError_t dispatch_launch(const DispatchParams& p, int sms, int pdl, cudaStream_t s);
+cudaError_t dispatch_grad_launch(const DispatchGradParams& p, int pdl, cudaStream_t s);
 
 struct FinalizeGradParams {
     MapParams m;

@@ -45,9 +45,6 @@ struct moe_op_s {
     mfr_options opt;
     mfr::RouteLaunch route;
     int* d_status;
-    // dispatch: the gradient is a plain finalize whose weights are all 1
-    mfr_plan_t sum_plan;
-    float* d_ones;
 };
 
 namespace {
@@ -192,9 +189,7 @@ extern "C" {
 void moe_op_destroy(moe_op_t op) {
     if (!op) return;
     if (op->d_status) cudaFree(op->d_status);
-    if (op->d_ones) cudaFree(op->d_ones);
     cudaGetLastError();
-    moe_finalize_rmsnorm_destroy(op->sum_plan);
     delete op;
 }
 
@@ -202,16 +197,12 @@ int moe_op_get_status(moe_op_t op, void* stream, int* device_status) {
     mfr::set_last_error("%s", "");
     if (!op || !device_status) return MFR_FAIL(MFR_ERR_INVALID_ARG, "the plan and device_status must not be NULL");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int h = 0, sum = 0;
+    int h = 0;
     cudaError_t e = cudaMemcpyAsync(&h, op->d_status, sizeof(int), cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e == cudaSuccess) e = cudaMemsetAsync(op->d_status, 0, sizeof(int), s);
     if (e != cudaSuccess) return fail_cuda(MFR_ERR_CUDA, "reading the status word", e);
-    if (op->sum_plan) {
-        const int rc = moe_finalize_rmsnorm_get_status(op->sum_plan, stream, &sum);
-        if (rc != MFR_OK) return rc;
-    }
-    *device_status = h | sum;
+    *device_status = h;
     return MFR_OK;
 }
 
@@ -314,26 +305,6 @@ int moe_dispatch_plan(moe_op_t* op, int64_t T, int64_t H, int k, int64_t R, int 
     p->R = R;
     p->elem_bytes = elem_bytes;
     p->sf_bytes = sf_bytes;
-    if (elem_bytes == 2 && sf_bytes == 0) {
-        // plain stream order: a finalize with dependent launch reads its map
-        // before its wait, and this one's may come from the kernel before it
-        mfr_options o;
-        moe_finalize_rmsnorm_default_options(&o);
-        o.enable_pdl = 0;
-        o.sentinel_skip = p->opt.sentinel_skip;
-        int src = moe_finalize_plan(&p->sum_plan, T, H, k, R, &o);
-        if (src == MFR_OK && T > 0) {
-            cudaError_t e = cudaMalloc(&p->d_ones, static_cast<size_t>(T * k) * sizeof(float));
-            if (e == cudaSuccess) e = mfr::fill_ones_launch(p->d_ones, T * k);
-            if (e == cudaSuccess) e = cudaDeviceSynchronize();
-            if (e != cudaSuccess) src = fail_cuda(MFR_ERR_CUDA, "the gradient's unit weights", e);
-        }
-        if (src != MFR_OK) {
-            moe_op_destroy(p);
-            *op = nullptr;
-            return src;
-        }
-    }
     return MFR_OK;
 }
 
@@ -367,14 +338,25 @@ int moe_dispatch_run(moe_op_t op, const void* x, const void* sf, const int32_t* 
 }
 
 int moe_dispatch_grad_run(moe_op_t op, const void* d_rows, const int32_t* permuted_row_of, void* d_x, void* stream) {
-    const int rc = check_op(op, kDispatch);
+    int rc = check_op(op, kDispatch);
     if (rc != MFR_OK) return rc;
-    if (!op->sum_plan)
+    if (op->elem_bytes != 2 || op->sf_bytes != 0)
         return MFR_FAIL(MFR_ERR_INVALID_ARG, "the gradient needs a plan for 16-bit rows without scales");
     if (op->T == 0) return MFR_OK;
-    const int src = moe_finalize_run(op->sum_plan, d_rows, permuted_row_of, op->d_ones, d_x, stream);
-    if (src != MFR_OK) return src;
-    return finish(op, cudaSuccess, stream);
+    const int64_t T = op->T, H = op->H, R = op->R, N = T * op->k;
+    if (!permuted_row_of || !d_x || (R > 0 && !d_rows)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(d_rows, 16) || !aligned(d_x, 16)) return MFR_FAIL(MFR_ERR_MISALIGNED, "d_rows and d_x must be 16-byte aligned");
+    if (!aligned(permuted_row_of, 4)) return MFR_FAIL(MFR_ERR_MISALIGNED, "permuted_row_of must be 4-byte aligned");
+    const Span in[] = {{d_rows, R * H * 2}, {permuted_row_of, N * 4}};
+    const Span out[] = {{d_x, T * H * 2}};
+    if (outputs_meet(out, in)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "d_x overlaps an input");
+    if ((rc = check_device(op)) != MFR_OK) return rc;
+    mfr::DispatchGradParams p{};
+    p.m = map_params(op, permuted_row_of, nullptr);
+    p.d_rows = static_cast<const uint16_t*>(d_rows);
+    p.d_x = static_cast<uint16_t*>(d_x);
+    p.H = static_cast<int>(H);
+    return finish(op, mfr::dispatch_grad_launch(p, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
 // ---- gradient of the weighted sum -------------------------------------------------------

@@ -9,7 +9,7 @@
 // Bytes bound it: 4 + 4 + 2 read and 4 (+ 2) written an element.  Measured on
 // GB300, of the copy rate: 8192 x 8192 166 us (0.96; 224 us a token at a time
 // without the ring below), 16384 x 4096 160 us (0.99), 32768 x 2048 164 us
-// (0.96), 4096 x 16384 166 us (0.96), 32768 x 1024 91 us (0.88); 511 x 4104
+// (0.96), 4096 x 16384 166 us (0.96), 32768 x 1024 85 us (0.93); 511 x 4104
 // 11.5 us, of which the second launch is 2.3.
 //
 // Wide rows: persistent CTAs, whose GT consumer threads own the same columns
@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const Res
 
 // ---- narrow rows ------------------------------------------------------------------------------
 // A warp per token, lane l owning the chunks (8 columns) l, l + 32, ...
+// Measured: 32768 x 512 51 us (0.77 of the copy rate), 32768 x 256 25 us (0.78);
+// above, the ring is faster (32768 x 1024 85 us, 92 with a warp per token).
 constexpr int kNarrowWarps = 8;
-constexpr int kNarrowMaxH = 1024;
+constexpr int kNarrowMaxH = 512;
 
 template <int CPT>
 __global__ void __launch_bounds__(32 * kNarrowWarps) resnorm_grad_narrow(const ResNormGradParams p) {
@@ -334,9 +336,8 @@ Form ring_form(int H) {
 }
 
 Form form_for(int H) {
-    if (H <= 256) return {resnorm_grad_narrow<1>, 32 * kNarrowWarps, 0, 3, kNarrowWarps};
-    if (H <= 512) return {resnorm_grad_narrow<2>, 32 * kNarrowWarps, 0, 2, kNarrowWarps};
-    if (H <= kNarrowMaxH) return {resnorm_grad_narrow<4>, 32 * kNarrowWarps, 0, 1, kNarrowWarps};
+    if (H <= 256) return {resnorm_grad_narrow<1>, 32 * kNarrowWarps, 0, 4, kNarrowWarps};
+    if (H <= kNarrowMaxH) return {resnorm_grad_narrow<2>, 32 * kNarrowWarps, 0, 2, kNarrowWarps};
     if (H <= 2048) return ring_form<128, 4>(H);
     if (H <= 4096) return ring_form<256, 4>(H);
     if (H <= 8192) return ring_form<512, 4>(H);
