@@ -21,13 +21,19 @@ namespace mfr {
 namespace {
 
 constexpr int kThreads = 256;
-// A row of scales, by one warp.
-__device__ __forceinline__ void copy_scales(const uint8_t* src, uint8_t* dst, int bytes, int lane) {
-    if (bytes % 4 == 0) {
-        for (int c = lane; c < bytes / 4; c += 32)
-            reinterpret_cast<uint32_t*>(dst)[c] = reinterpret_cast<const uint32_t*>(src)[c];
-    } else {
-        for (int c = lane; c < bytes; c += 32) dst[c] = src[c];
+// A token's row of scales to the rows of its pairs, by one warp: lane j < k
+// holds the row of pair j.  Word is the unit the row divides into.
+template <typename Word>
+__device__ __forceinline__ void copy_scales(const DispatchParams& p, int64_t t, int row, int lane) {
+    const int words = p.sf_bytes / static_cast<int>(sizeof(Word));
+    const Word* src = reinterpret_cast<const Word*>(p.sf) + t * words;
+    for (int c0 = 0; c0 < words; c0 += 32) {
+        const int c = c0 + lane;
+        const Word v = c < words ? src[c] : Word(0);
+        for (int j = 0; j < p.m.k; ++j) {
+            const int r = __shfl_sync(0xFFFFFFFFu, row, j);
+            if (r >= 0 && c < words) reinterpret_cast<Word*>(p.sf_out)[static_cast<int64_t>(r) * words + c] = v;
+        }
     }
 }
 
@@ -72,8 +78,10 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchParams
 #pragma unroll
         for (int i = 0; i < C; ++i)
             if (c0 + 32 * i < nck) st_stream_u4(dst + (c0 + 32 * i) * 16, v[i]);
-        if (p.sf_bytes > 0 && seg == segs - 1)
-            copy_scales(p.sf + t * p.sf_bytes, p.sf_out + static_cast<int64_t>(r) * p.sf_bytes, p.sf_bytes, lane);
+    }
+    if (p.sf_bytes > 0 && seg == segs - 1) {
+        if (p.sf_bytes % 4 == 0) copy_scales<uint32_t>(p, t, row, lane);
+        else copy_scales<uint8_t>(p, t, row, lane);
     }
 }
 

@@ -18,7 +18,11 @@
 // order, all in FP32, so a call gives the same bits every time; a row's
 // gradient is rounded once, from the FP32 product to bf16, the type of the rows
 // that the experts' GEMMs take their gradients in.
+#include <cooperative_groups.h>
+
 #include "mfr_maps.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace mfr {
 namespace {
@@ -38,17 +42,20 @@ __device__ __forceinline__ void load_grad(const void* d_out, int64_t at, float (
 }
 
 // One token a CTA, thread i of it the chunks i, i + blockDim.x, ... of the
-// token's rows, U of them at a time; SG: slots at most.  The row_ctas CTAs
-// before the tokens' look after the rows' side of the maps, `rpw` rows a warp.
-template <bool F32, int SG, int U>
+// token's rows, U of them at a time; SG: slots at most.  SPLIT: a token has a
+// cluster of csize CTAs, each a share of the chunks, whose dot products meet in
+// the first one's shared memory.  The row_ctas CTAs (whole clusters) before the
+// tokens' look after the rows' side of the maps, `rpw` rows a warp.
+template <bool F32, int SG, int U, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, SG > 8 ? 2 : 3) finalize_grad_kernel(const FinalizeGradParams p, const int row_ctas,
-                                                                                   const int rpw) {
+                                                                                   const int rpw, const int csize) {
     __shared__ int s_row[kMaxK];      // -1: the pair has no row
     __shared__ float s_w[kMaxK];
     __shared__ float s_part[kThreads / 32][SG > 8 ? 16 : 8];
+    __shared__ float s_split[8][SPLIT ? kMaxK : 1];
     const MapParams& m = p.m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int nck = p.H >> 3;
+    const int chunks = p.H >> 3;
     pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x < row_ctas) {
@@ -56,20 +63,23 @@ __global__ void __launch_bounds__(kThreads, SG > 8 ? 2 : 3) finalize_grad_kernel
         const bool pad = lane < rpw && r0 + lane < m.R && row_is_padding(m, r0 + lane);
         for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, pad); todo; todo &= todo - 1) {
             uint16_t* row = p.d_expert_out + (r0 + __ffs(todo) - 1) * p.H;
-            for (int c = lane; c < nck; c += 32) st_stream_u4(row + c * 8, make_uint4(0, 0, 0, 0));
+            for (int c = lane; c < chunks; c += 32) st_stream_u4(row + c * 8, make_uint4(0, 0, 0, 0));
         }
         return;
     }
-    const int64_t t = blockIdx.x - row_ctas;
+    const int64_t t = (blockIdx.x - row_ctas) / csize;
+    const int rank = SPLIT ? static_cast<int>(blockIdx.x - row_ctas) % csize : 0;
+    if constexpr (SPLIT) cg::this_cluster().barrier_arrive();
     if (tid < m.k) {
-        s_row[tid] = pair_row(m, t, tid, true);
+        s_row[tid] = pair_row(m, t, tid, rank == 0);
         s_w[tid] = p.w[t * m.k + tid];
     }
     float dot[SG > 8 ? 16 : 8];
 #pragma unroll
     for (int j = 0; j < (SG > 8 ? 16 : 8); ++j) dot[j] = 0.f;
     __syncthreads();
-    for (int c0 = tid; c0 - tid < nck; c0 += U * blockDim.x) {     // as many turns for every thread
+    const int first = SPLIT ? chunks * rank / csize : 0, nck = SPLIT ? chunks * (rank + 1) / csize : chunks;   // this CTA's
+    for (int c0 = first + tid; c0 - tid < nck; c0 += U * blockDim.x) {     // as many turns for every thread
         uint4 v[SG][U];
         float g[U][8];
 #pragma unroll
@@ -112,19 +122,27 @@ __global__ void __launch_bounds__(kThreads, SG > 8 ? 2 : 3) finalize_grad_kernel
         if ((lane & 3) == 0) s_part[warp][a * 8 + (lane >> 2)] = sum;
     }
     __syncthreads();
-    if (tid < m.k) {
-        float total = 0.f;
+    float total = 0.f;
+    if (tid < m.k)
         for (int i = 0; i < warps; ++i) total += s_part[i][tid];
-        p.d_w[t * m.k + tid] = total;
+    if constexpr (SPLIT) {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.barrier_wait();          // the first CTA runs
+        if (tid < m.k) cl.map_shared_rank(&s_split[0][0], 0)[rank * kMaxK + tid] = total;
+        cl.sync();
+        total = 0.f;
+        if (rank == 0 && tid < m.k)
+            for (int i = 0; i < csize; ++i) total += s_split[i][tid];
     }
+    if (rank == 0 && tid < m.k) p.d_w[t * m.k + tid] = total;
 }
 
-using GradKernel = void (*)(const FinalizeGradParams, int, int);
+using GradKernel = void (*)(const FinalizeGradParams, int, int, int);
 
-template <bool F32>
+template <bool F32, bool SPLIT>
 GradKernel kernel_for(int k) {
-    return k <= 2 ? finalize_grad_kernel<F32, 2, 2> : k <= 4 ? finalize_grad_kernel<F32, 4, 2>
-         : k <= 8 ? finalize_grad_kernel<F32, 8, 1> : finalize_grad_kernel<F32, 16, 1>;
+    return k <= 2 ? finalize_grad_kernel<F32, 2, 2, SPLIT> : k <= 4 ? finalize_grad_kernel<F32, 4, 2, SPLIT>
+         : k <= 8 ? finalize_grad_kernel<F32, 8, 1, SPLIT> : finalize_grad_kernel<F32, 16, 1, SPLIT>;
 }
 
 }  // namespace
@@ -143,11 +161,23 @@ cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, 
     if (p.m.T > 12 * static_cast<int64_t>(sms) && turns < least) turns = least;
     int block = ((nck + turns - 1) / turns + 31) / 32 * 32;
     if (p.m.k > 4 && block < 64 && nck > 32) block = 64;
+    // Few tokens of more than two turns: a cluster per token, while its CTAs find
+    // an SM each (us with one CTA a token and with the cluster: T = 1, H = 4096
+    // 3.4, 3.4; 8192 5.3, 3.4; 16384 9.0, 3.6; T = 38, H = 8192 5.6, 4.3).
+    int csize = 1;
+    if (nck > 2 * kThreads)
+        while (csize < 8 && p.m.T * 2 * csize <= sms) csize *= 2;
+    if (csize > 1) {
+        const int share = (nck + csize - 1) / csize;
+        turns = (share + kThreads - 1) / kThreads;
+        block = ((share + turns - 1) / turns + 31) / 32 * 32;
+    }
     const int rpw = rows_per_warp(p.m.T, sms);
     const int64_t per = static_cast<int64_t>(block / 32) * rpw;
-    const int row_ctas = static_cast<int>((p.m.R + per - 1) / per);
-    return layer_launch(p.fp32 ? kernel_for<true>(p.m.k) : kernel_for<false>(p.m.k), row_ctas + p.m.T, block, 0, 1, pdl, s, p,
-                        row_ctas, rpw);
+    const int row_ctas = static_cast<int>((p.m.R + per * csize - 1) / (per * csize)) * csize;
+    const GradKernel kernel = csize > 1 ? (p.fp32 ? kernel_for<true, true>(p.m.k) : kernel_for<false, true>(p.m.k))
+                                        : (p.fp32 ? kernel_for<true, false>(p.m.k) : kernel_for<false, false>(p.m.k));
+    return layer_launch(kernel, row_ctas + p.m.T * csize, block, 0, csize, pdl, s, p, row_ctas, rpw, csize);
 }
 
 }  // namespace mfr
