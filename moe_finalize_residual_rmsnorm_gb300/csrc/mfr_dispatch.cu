@@ -12,15 +12,17 @@
 //
 // Measured on GB300 at 16384 x 4096 bf16 rows, k = 8, blocks padded to 128
 // rows (1.27 GB): 189 us, the copy rate of half reads and half writes (a plain
-// fill of as many bytes runs at 0.6 of it).  Copies through shared memory (a
-// bulk load and k bulk stores a segment, 4 or 8 warps with 2 or 3 stages)
-// took 6 % longer.  Stores past L1: 4096 x 8192 bytes 43.8 -> 40.7 us.
+// fill of as many bytes runs at 0.6 of it); 4096 x 8192 8-bit rows with scales
+// 44.7 us (0.92).  Copies through shared memory (a bulk load and k bulk stores a
+// segment, 4 or 8 warps with 2 or 3 stages) took 6 % longer; stores that keep
+// L1 lines 7 % longer at 4096 x 8192 bytes.
 #include "mfr_maps.cuh"
 
 namespace mfr {
 namespace {
 
 constexpr int kThreads = 256;
+
 // A token's row of scales to the rows of its pairs, by one warp: lane j < k
 // holds the row of pair j.  Word is the unit the row divides into.
 template <typename Word>
@@ -43,7 +45,8 @@ __device__ __forceinline__ void copy_scales(const DispatchParams& p, int64_t t, 
 // (measured at 16384 x 4096, rows' warps last: 213 us with 512-byte segments,
 // 207 with 1 KB, 206 with 2 KB, 208 with 4 KB).
 template <int C>
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchParams p, const int segs, const int64_t row_warps, const int rpw) {
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchParams p, const int segs, const int64_t row_warps,
+                                                            const int rpw) {
     const int lane = threadIdx.x & 31;
     int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const MapParams& m = p.m;
