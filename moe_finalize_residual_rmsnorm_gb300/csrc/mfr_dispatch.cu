@@ -164,7 +164,7 @@ cudaError_t dispatch_grad_launch(const DispatchGradParams& p, int pdl, cudaStrea
 cudaError_t dispatch_launch(const DispatchParams& p, int sms, int pdl, cudaStream_t s) {
     const int nck = p.row_bytes / 16;
     const bool wide = fills_gpu(p.m.T * nck, sms);
-    const int rpw = rows_per_warp(p.m.T, sms);
+    const int rpw = rows_per_warp(p.m.T, p.m.R, sms);
     const int chunks = wide ? 128 : 32;
     const int segs = (nck + chunks - 1) / chunks;
     const int64_t row_warps = (p.m.R + rpw - 1) / rpw;

@@ -172,7 +172,7 @@ cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, 
         turns = (share + kThreads - 1) / kThreads;
         block = ((share + turns - 1) / turns + 31) / 32 * 32;
     }
-    const int rpw = rows_per_warp(p.m.T, sms);
+    const int rpw = rows_per_warp(p.m.T, p.m.R, sms);
     const int64_t per = static_cast<int64_t>(block / 32) * rpw;
     const int row_ctas = static_cast<int>((p.m.R + per * csize - 1) / (per * csize)) * csize;
     const GradKernel kernel = csize > 1 ? (p.fp32 ? kernel_for<true, true>(p.m.k) : kernel_for<false, true>(p.m.k))

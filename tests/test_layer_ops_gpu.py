@@ -83,7 +83,9 @@ def test_route_gives_the_same_for_every_cluster(cluster, T, k, E):
 
 
 @pytest.mark.parametrize("T,k,E,align,kw", [(32769, 8, 64, 1, {}), (40000, 8, 1024, 128, {}), (70001, 5, 3, 1, {}),
-                                            (17000, 1, 16, 16, dict(cluster_size=1)), (32768, 8, 256, 128, {})])
+                                            (17000, 1, 16, 16, dict(cluster_size=1)), (32768, 8, 256, 128, {}),
+                                            # several rounds a CTA: from 4096 pairs an SM up
+                                            (90001, 7, 130, 16, {}), (262147, 8, 1023, 128, {}), (2000003, 1, 2, 1, {})])
 def test_route_large(T, k, E, align, kw):
     rng = np.random.default_rng(T)
     ids = rng.integers(-1, E, size=(T, k)).astype(np.int32)
@@ -311,6 +313,66 @@ def test_rows_past_32_bit_offsets():
     sq = (x.double() ** 2).sum(1)                # every row of a token is the token's own
     assert ((dw.double() - sq[:, None]).abs() <= ref.CHAIN * ref.U * sq[:, None]).all()
     assert p.get_status() == 0 and q.get_status() == 0
+
+
+def test_many_unused_rows():
+    """A matrix of far more rows than the tokens have: the rest is left as it was."""
+    T, H, k, R = 2, 8, 3, 3000000
+    row = torch.tensor([[5, R - 1, 70000], [1234567, 0, 2999998]], dtype=I32, device="cuda")
+    slot = torch.full((R,), -2, dtype=I32, device="cuda")
+    slot[row.view(-1).long()] = torch.arange(6, dtype=I32, device="cuda")
+    slot[17], slot[R - 3] = -1, -1
+    x, w = randn((T, H), 1, B16), randn((T, k), 2, F32)
+    out, dE, dw = Guarded((R, H), B16), Guarded((R, H), B16), Guarded((T, k), F32)
+    p, q = mfr.DispatchPlan(T, H, k, R), mfr.FinalizeGradPlan(T, H, k, R)
+    p.run(x, row, slot, out.t)
+    E = out.t.clone()
+    q.run(x, E, row, slot, w, dE.t, dw.t)
+    torch.cuda.synchronize()
+    for buf, want in ((out, x[:, None, :].expand(T, k, H)), (dE, (w[..., None] * x[:, None, :].float()).to(B16))):
+        t = buf.check()
+        assert torch.equal(t[row.view(-1).long()], want.reshape(-1, H)) and not t[17].any() and not t[R - 3].any()
+        rest = torch.ones(R, dtype=torch.bool, device="cuda")
+        rest[row.view(-1).long()] = rest[17] = rest[R - 3] = False
+        assert (t.view(torch.uint8)[rest] == 0x5A).all()
+    sq = (ref.f64(x) ** 2).sum(1)[:, None] * np.ones((1, k))
+    ref.assert_within(ref.f64(dw.check()), sq, ref.CHAIN * ref.U * sq, "d_w")
+    assert p.get_status() == 0 and q.get_status() == 0
+
+
+def test_norms_past_32_bit_offsets():
+    """Residual norm and its gradient over more than 2^31 elements, the last
+    rows and d_gamma against 64 bits."""
+    T, H = 135000, 16384
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty((T, H), dtype=B16, device="cuda")
+    res = torch.empty((T, H), device="cuda")
+    for a in range(0, T, 9000):
+        x[a:a + 9000] = torch.randn((min(9000, T - a), H), generator=g, device="cuda")
+        res[a:a + 9000] = torch.randn((min(9000, T - a), H), generator=g, device="cuda")
+    gamma = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).to(B16)
+    p = mfr.ResidualNormPlan(T, H, quant=mfr.QUANT_MX32)
+    q, sf = torch.empty((T, H), dtype=FP8, device="cuda"), torch.empty(p.sf_shape(), dtype=torch.uint8, device="cuda")
+    last = slice(T - 40, T)
+    before = res[last].clone()
+    p.run(x, res, res, gamma, 1e-6, None, q, sf)
+    check_norm(x[last], before, gamma, 1e-6, mfr.QUANT_MX32, False, [res[last], None, q[last], sf[last]])
+    del q
+    n = mfr.ResidualNormGradPlan(T, H)
+    d_in, d_x, d_g = torch.empty_like(res), torch.empty_like(x), torch.empty(H, device="cuda")
+    n.run(x, None, res, gamma, 1e-6, d_in, d_g, torch.empty(n.workspace_bytes(), dtype=torch.uint8, device="cuda"), d_x)
+    want, size, _, _ = ref.residual_norm_grad(ref.f64(x[last]), None, ref.f64(res[last]), ref.f64(gamma), 1e-6)
+    ref.assert_within(ref.f64(d_in[last]), want, ref.GRAD_REL * size + ref.TINY, "d_residual_in")
+    assert torch.equal(d_x[last], d_in[last].to(B16))
+    dg, dg_size = torch.zeros(H, dtype=torch.float64, device="cuda"), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for a in range(0, T, 9000):
+        r = res[a:a + 9000].double()
+        term = x[a:a + 9000].double() * r * torch.rsqrt((r * r).mean(1, keepdim=True) + 1e-6)
+        dg += term.sum(0)
+        dg_size += term.abs().sum(0)
+    chain = T / 152 + 1 + 152 * 8 / 8 + 8
+    ref.assert_within(ref.f64(d_g), dg.cpu().numpy(), ((chain + 4) * ref.U + ref.Y_REL) * dg_size.cpu().numpy(), "d_gamma")
+    assert p.get_status() == 0 and n.get_status() == 0
 
 
 # ---- residual norm ------------------------------------------------------------------------
