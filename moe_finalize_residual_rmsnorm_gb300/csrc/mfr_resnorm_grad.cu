@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const Res
 
 // ---- narrow rows ------------------------------------------------------------------------------
 // A warp per token, lane l owning the chunks (8 columns) l, l + 32, ...
-// Measured: 32768 x 512 51 us (0.77 of the copy rate), 32768 x 256 25 us (0.78);
+// Measured: 32768 x 512 46 us (0.85 of the copy rate), 32768 x 256 25 us (0.78);
 // above, the ring is faster (32768 x 1024 85 us, 92 with a warp per token).
 constexpr int kNarrowWarps = 8;
 constexpr int kNarrowMaxH = 512;
@@ -222,29 +222,43 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) resnorm_grad_narrow(const R
     pdl_wait();
     pdl_launch_dependents();
     const int64_t step = static_cast<int64_t>(gridDim.x) * kNarrowWarps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kNarrowWarps + warp; t < p.T; t += step) {
+    // the next token's values are loaded while this one's sums and stores are under way
+    float4 nr[CPT][2], na[CPT][2];
+    uint4 nd[CPT];
+    auto load = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const int c = lane + 32 * i;
+            const int64_t at = t * p.H + c * 8;
+            nr[i][0] = nr[i][1] = na[i][0] = na[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            nd[i] = make_uint4(0, 0, 0, 0);
+            if (t < p.T && c < nck) {
+                nr[i][0] = ld_once_f4(p.r + at);
+                nr[i][1] = ld_once_f4(p.r + at + 4);
+                nd[i] = ld_stream_u4(p.d_out + at);
+                if (p.d_res) {
+                    na[i][0] = ld_once_f4(p.d_res + at);
+                    na[i][1] = ld_once_f4(p.d_res + at + 4);
+                }
+            }
+        }
+    };
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kNarrowWarps + warp;
+    load(t);
+    for (; t < p.T; t += step) {
         float r[CPT][8], a[CPT][8];
         uint4 d[CPT];
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
-            const int c = lane + 32 * i;
-            const int64_t at = t * p.H + c * 8;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) r[i][q] = a[i][q] = 0.f;
-            d[i] = make_uint4(0, 0, 0, 0);
-            if (c < nck) {
-                const float4 u = ld_once_f4(p.r + at), v = ld_once_f4(p.r + at + 4);
-                d[i] = ld_stream_u4(p.d_out + at);
-                r[i][0] = u.x; r[i][1] = u.y; r[i][2] = u.z; r[i][3] = u.w;
-                r[i][4] = v.x; r[i][5] = v.y; r[i][6] = v.z; r[i][7] = v.w;
-                if (p.d_res) {
-                    const float4 x = ld_once_f4(p.d_res + at), y = ld_once_f4(p.d_res + at + 4);
-                    a[i][0] = x.x; a[i][1] = x.y; a[i][2] = x.z; a[i][3] = x.w;
-                    a[i][4] = y.x; a[i][5] = y.y; a[i][6] = y.z; a[i][7] = y.w;
-                }
-            }
+            const float4 u = nr[i][0], v = nr[i][1], x = na[i][0], w = na[i][1];
+            r[i][0] = u.x; r[i][1] = u.y; r[i][2] = u.z; r[i][3] = u.w;
+            r[i][4] = v.x; r[i][5] = v.y; r[i][6] = v.z; r[i][7] = v.w;
+            a[i][0] = x.x; a[i][1] = x.y; a[i][2] = x.z; a[i][3] = x.w;
+            a[i][4] = w.x; a[i][5] = w.y; a[i][6] = w.z; a[i][7] = w.w;
+            d[i] = nd[i];
         }
+        load(t + step);
         float g[8], y[8];
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
@@ -297,7 +311,10 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) resnorm_grad_narrow(const R
 }
 
 // ---- the partial sums of d_gamma ------------------------------------------------------------
-// A CTA owns 32 columns, warp w the rows w, w + 32, ..., then the warps in order.
+// A CTA owns 32 columns, warp w the rows w, w + 32, ..., then a butterfly over the
+// warps.  It costs 2.5 to 3 us of a call; small CTAs of 8 columns that wait beside
+// the first kernel's took longer (511 x 4104 12.5 us instead of 11.7, 32768 x
+// 2048 181 instead of 164).
 __global__ void __launch_bounds__(1024) gamma_sum_kernel(const float* partial, int rows, int H, float* d_gamma) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -336,7 +353,7 @@ Form ring_form(int H) {
 }
 
 Form form_for(int H) {
-    if (H <= 256) return {resnorm_grad_narrow<1>, 32 * kNarrowWarps, 0, 4, kNarrowWarps};
+    if (H <= 256) return {resnorm_grad_narrow<1>, 32 * kNarrowWarps, 0, 3, kNarrowWarps};
     if (H <= kNarrowMaxH) return {resnorm_grad_narrow<2>, 32 * kNarrowWarps, 0, 2, kNarrowWarps};
     if (H <= 2048) return ring_form<128, 4>(H);
     if (H <= 4096) return ring_form<256, 4>(H);
@@ -358,8 +375,10 @@ cudaError_t resnorm_grad_prepare(int H) {
 
 int resnorm_grad_partials(int64_t T, int H, int sms) {
     const Form f = form_for(H);
-    const int64_t want = (T + f.tokens - 1) / f.tokens, most = static_cast<int64_t>(sms) * f.per_sm;
-    return static_cast<int>(want < most ? want : most);
+    // the turns spread evenly: no CTA has one fewer than it could take over from another
+    const int64_t turns = (T + f.tokens - 1) / f.tokens, most = static_cast<int64_t>(sms) * f.per_sm;
+    const int64_t each = (turns + most - 1) / most;
+    return each > 0 ? static_cast<int>((turns + each - 1) / each) : 0;
 }
 
 cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s) {
