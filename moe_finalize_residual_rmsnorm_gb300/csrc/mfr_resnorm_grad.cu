@@ -375,10 +375,8 @@ cudaError_t resnorm_grad_prepare(int H) {
 
 int resnorm_grad_partials(int64_t T, int H, int sms) {
     const Form f = form_for(H);
-    // the turns spread evenly: no CTA has one fewer than it could take over from another
-    const int64_t turns = (T + f.tokens - 1) / f.tokens, most = static_cast<int64_t>(sms) * f.per_sm;
-    const int64_t each = (turns + most - 1) / most;
-    return each > 0 ? static_cast<int>((turns + each - 1) / each) : 0;
+    const int64_t want = (T + f.tokens - 1) / f.tokens, most = static_cast<int64_t>(sms) * f.per_sm;
+    return static_cast<int>(want < most ? want : most);
 }
 
 cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s) {
