@@ -32,7 +32,10 @@
  *    before its own wait: those must not be outputs of the call directly
  *    before it in the stream.
  *  - A plan may be run concurrently on several streams; calls that are given
- *    the same workspace must not overlap.
+ *    the same workspace, graphs that captured it included, must not overlap.
+ *  - Runs may be captured into a graph, which must not outlive its plans.  Make
+ *    plans before the capture; debug_checks waits for the stream and cannot be
+ *    captured.
  *  - T == 0 is a no-op returning MFR_OK unless the function says otherwise.
  *
  * The pair of index maps.  A pair s = t * k + j (token t, slot j) has the row

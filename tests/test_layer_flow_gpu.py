@@ -261,6 +261,41 @@ def test_two_launch_route_of_changing_ids(pdl):
     assert m.plan.get_status() == 0
 
 
+def test_captured_two_launch_route_and_gradient():
+    """The calls of two launches (a large route, the norm's gradient) captured
+    into one graph and replayed on other inputs."""
+    T, k, E, H = 6000, 8, 100, 1032
+    m = Route(T, k, E, 16)
+    n = mfr.ResidualNormGradPlan(T, H)
+    ws, d_in, d_g = new((n.workspace_bytes(),), torch.uint8), new((T, H)), new((H,))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ids = new((T, k), I32)
+    d, r, gamma = randn((T, H), 1, B16), randn((T, H), 2), (1 + 0.1 * randn((H,), 3)).to(B16)
+
+    def calls():
+        n.run(d, None, r, gamma, 1e-6, d_in, d_g, ws)
+        m.run(ids)
+        n.run(d, d_in, r, gamma, 1e-6, d_in, d_g, ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            calls()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        ids.copy_(torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=I32))
+        r.copy_(torch.randn((T, H), generator=g, device="cuda"))
+        graph.replay()
+        order = torch.argsort(ids.view(-1).long(), stable=True)
+        replayed = [t.clone() for t in (m.row_of, m.slot_of, m.offsets, m.counts, d_in, d_g)]
+        slots = m.slot_of[m.slot_of >= 0].long()
+        assert torch.equal(slots, order)
+        calls()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, (m.row_of, m.slot_of, m.offsets, m.counts, d_in, d_g)))
+    assert m.plan.get_status() == n.get_status() == 0
+
+
 def test_the_same_bits_every_time_and_in_a_graph():
     """Eager runs, a replayed graph and a graph replayed on new inputs give the
     same bits as eager runs on those inputs."""

@@ -146,8 +146,10 @@ class Maps:
         self.d_row, self.d_slot = cuda(self.row_of, I32), cuda(self.slot_of, I32)
 
 
+# every form by slots (to 2, 4, 6, 8, 16) and by columns, few tokens of wide rows
+# (a cluster a token) and plenty of tokens
 ROWS = [(1, 8, 1), (1, 4096, 8), (3, 24, 16), (7, 136, 6), (33, 2056, 3), (130, 4096, 8), (20, 8192, 8), (9, 16384, 2),
-        (600, 1032, 5)]
+        (600, 1032, 5), (2, 8200, 9), (30, 5000, 16), (1, 16384, 13), (2000, 264, 1), (2100, 1032, 8), (1900, 136, 4)]
 
 
 @pytest.mark.parametrize("T,H,k", ROWS)
@@ -175,6 +177,18 @@ def test_dispatch(T, H, k, align, share, dtype, sf):
         want[here] = src[m.slot_of[here] // k]
         assert np.array_equal(got, want)
     assert plan.get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bool, torch.float16, torch.int32])
+def test_dispatch_copies_any_type(dtype):
+    T, H, k = 11, 48, 3
+    m = Maps(T, k, 16, 4)
+    x = torch.randint(0, 2, (T, H), device="cuda").to(dtype)
+    out = Guarded((m.R, H), dtype)
+    mfr.DispatchPlan(T, H, k, m.R, dtype=dtype).run(x, m.d_row, m.d_slot, out.t)
+    torch.cuda.synchronize()
+    here = torch.from_numpy(m.slot_of >= 0).cuda()
+    assert torch.equal(out.check()[here], x[torch.from_numpy(m.slot_of[m.slot_of >= 0] // k).cuda()])
 
 
 @pytest.mark.parametrize("T,H,k", ROWS)
