@@ -10,13 +10,15 @@
 // output, so bytes bound it (2 + 4 read, 4 + 1 (+ 2) written an element) and
 // one CTA per token is enough, as long as several are resident on an SM, each
 // in another phase of load, sum and store.  The launch bounds below hold that
-// up; CTAs are at most 512 threads of one chunk (8 columns), two or four.
+// up; CTAs are at most 512 threads of one to four chunks (8 columns).
 // Measured on GB300, of the copy rate: 16384 x 4096 107 us (1.03), with bf16
 // output and MX scales 127 us (1.02); 8192 x 8192 109 us (1.00; 117 with 1024
 // threads of a chunk, 121 with two 512-thread CTAs an SM); 4096 x 16384 119
 // us (0.92).
-//   four chunks (H > 8192): r waits in shared memory, three CTAs an SM (148 us
-//     with r in the registers of 1024 threads)
+//   three or four chunks (H > 8192): r waits in shared memory, three CTAs an SM
+//     (16384 columns: 148 us with r in the registers of 1024 threads, 119 with a
+//     ring of stages as in the gradient; 9000 columns: 127 us with three chunks a
+//     thread, 150 with four, 150 with the ring)
 //   few tokens of wide rows: a cluster of 4 or 8 CTAs per token, which
 //     exchange their sums through distributed shared memory (T = 1: H = 4096
 //     1.96 -> 1.71 us, 8192 2.98 -> 1.86, 16384 5.24 -> 2.03)
@@ -247,22 +249,27 @@ cudaError_t launch_quant(const ResNormParams& p, int pdl, cudaStream_t s) {
     }
 }
 
-template <int QUANT>
+template <int CPT, int QUANT>
 cudaError_t allow_stash() {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(resnorm_kernel<4, QUANT, false>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * 512 * 16);
+    // the attribute is per kernel, shared by every plan: always the most any plan needs
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(resnorm_kernel<CPT, QUANT, false>),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * CPT * 512 * 16);
+}
+
+template <int CPT>
+cudaError_t prepare_stash(int quant) {
+    switch (quant) {
+        case MFR_QUANT_TOKEN: return allow_stash<CPT, MFR_QUANT_TOKEN>();
+        case MFR_QUANT_GROUP128: return allow_stash<CPT, MFR_QUANT_GROUP128>();
+        case MFR_QUANT_MX32: return allow_stash<CPT, MFR_QUANT_MX32>();
+        default: return allow_stash<CPT, MFR_QUANT_NONE>();
+    }
 }
 
 }  // namespace
 
 cudaError_t resnorm_prepare(int H, int quant) {
-    if (H <= 8192) return cudaSuccess;
-    switch (quant) {
-        case MFR_QUANT_TOKEN: return allow_stash<MFR_QUANT_TOKEN>();
-        case MFR_QUANT_GROUP128: return allow_stash<MFR_QUANT_GROUP128>();
-        case MFR_QUANT_MX32: return allow_stash<MFR_QUANT_MX32>();
-        default: return allow_stash<MFR_QUANT_NONE>();
-    }
+    return H <= 8192 ? cudaSuccess : H <= 12288 ? prepare_stash<3>(quant) : prepare_stash<4>(quant);
 }
 
 cudaError_t resnorm_launch(const ResNormParams& p, int sms, int pdl, cudaStream_t s) {
@@ -277,6 +284,7 @@ cudaError_t resnorm_launch(const ResNormParams& p, int sms, int pdl, cudaStream_
     if (p.H <= 512) return launch_quant<2, true>(p, pdl, s);
     if (p.H <= 4096) return launch_quant<1, false>(p, pdl, s);
     if (p.H <= 8192) return launch_quant<2, false>(p, pdl, s);
+    if (p.H <= 12288) return launch_quant<3, false>(p, pdl, s);
     return launch_quant<4, false>(p, pdl, s);
 }
 

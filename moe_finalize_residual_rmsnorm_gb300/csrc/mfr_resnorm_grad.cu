@@ -28,11 +28,6 @@
 namespace mfr {
 namespace {
 
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-
 // ---- wide rows ---------------------------------------------------------------------------
 // GT consumer threads, four columns of a tile each; NT tiles at most.
 template <int GT>
@@ -94,9 +89,9 @@ __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const Res
                 const int64_t at = t * H + c0;
                 if (lane == 0) mbar_arrive_expect_tx(bar, cb * (p.d_res ? 10 : 6));
                 __syncwarp();
-                if (lane == 0) bulk_g2s(st, p.r + at, cb * 4, bar);
-                if (lane == 1 && p.d_res) bulk_g2s(st + CB * 4, p.d_res + at, cb * 4, bar);
-                if (lane == 2) bulk_g2s(st + CB * 8, p.d_out + at, cb * 2, bar);
+                if (lane == 0) bulk_load(st, p.r + at, cb * 4, bar);
+                if (lane == 1 && p.d_res) bulk_load(st + CB * 4, p.d_res + at, cb * 4, bar);
+                if (lane == 2) bulk_load(st + CB * 8, p.d_out + at, cb * 2, bar);
                 ++fill;
                 if (++s == S) { s = 0; phase ^= 1u; }
             }

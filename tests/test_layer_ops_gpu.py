@@ -391,7 +391,7 @@ def test_norms_past_32_bit_offsets():
 
 # ---- residual norm ------------------------------------------------------------------------
 
-NORMS = [(1, 8), (1, 4096), (2, 24), (5, 136), (3, 1000), (7, 2056), (130, 4096), (33, 8192), (17, 8200), (9, 16384),
+NORMS = [(1, 8), (1, 4096), (60, 12288), (50, 12296), (45, 9000), (2, 24), (5, 136), (3, 1000), (7, 2056), (130, 4096), (33, 8192), (17, 8200), (9, 16384),
          (300, 264), (257, 64)]
 
 
