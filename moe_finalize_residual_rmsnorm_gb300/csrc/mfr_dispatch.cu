@@ -148,7 +148,20 @@ __global__ void __launch_bounds__(kThreads) dispatch_grad_kernel(const DispatchG
                              pack_bf16x2(acc[i][4], acc[i][5]), pack_bf16x2(acc[i][6], acc[i][7])));
 }
 
+using DispatchGradKernel = void (*)(const DispatchGradParams, int);
+DispatchGradKernel grad_kernel_for(int k) {
+    return k <= 2 ? dispatch_grad_kernel<2, 2> : k <= 4 ? dispatch_grad_kernel<4, 2>
+         : k <= 6 ? dispatch_grad_kernel<6, 1> : dispatch_grad_kernel<8, 1>;
+}
+
 }  // namespace
+
+cudaError_t dispatch_prepare() {
+    cudaError_t e = preload(dispatch_kernel<4>);
+    if (e == cudaSuccess) e = preload(dispatch_kernel<1>);
+    for (int k = 1; k <= kMaxK && e == cudaSuccess; ++k) e = preload(grad_kernel_for(k));
+    return e;
+}
 
 cudaError_t dispatch_grad_launch(const DispatchGradParams& p, int pdl, cudaStream_t s) {
     const int nck = p.H / 8;
@@ -156,9 +169,7 @@ cudaError_t dispatch_grad_launch(const DispatchGradParams& p, int pdl, cudaStrea
     const int c = p.m.k <= 4 ? 2 : 1;
     const int segs = (nck + 32 * c - 1) / (32 * c);
     const int64_t grid = (p.m.T * segs + kThreads / 32 - 1) / (kThreads / 32);
-    const auto kernel = p.m.k <= 2 ? dispatch_grad_kernel<2, 2> : p.m.k <= 4 ? dispatch_grad_kernel<4, 2>
-                      : p.m.k <= 6 ? dispatch_grad_kernel<6, 1> : dispatch_grad_kernel<8, 1>;
-    return layer_launch(kernel, grid, kThreads, 0, 1, pdl, s, p, segs);
+    return layer_launch(grad_kernel_for(p.m.k), grid, kThreads, 0, 1, pdl, s, p, segs);
 }
 
 cudaError_t dispatch_launch(const DispatchParams& p, int sms, int pdl, cudaStream_t s) {

@@ -147,6 +147,11 @@ GradKernel kernel_for(int k) {
 
 }  // namespace
 
+cudaError_t finalize_grad_prepare(int k, int fp32) {
+    cudaError_t e = preload(fp32 ? kernel_for<true, false>(k) : kernel_for<false, false>(k));
+    return e != cudaSuccess ? e : preload(fp32 ? kernel_for<true, true>(k) : kernel_for<false, true>(k));
+}
+
 cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, cudaStream_t s) {
     const int nck = p.H / 8;
     // A CTA's threads divide a token's chunks evenly: no turn in which a few

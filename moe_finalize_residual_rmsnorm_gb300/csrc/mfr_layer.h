@@ -96,6 +96,8 @@ struct DispatchGradParams {
     int H;
 };
 
+// Each prepare loads the kernels that the plan's calls launch and sets their attributes.
+cudaError_t dispatch_prepare();
 cudaError_t dispatch_launch(const DispatchParams& p, int sms, int pdl, cudaStream_t s);
 cudaError_t dispatch_grad_launch(const DispatchGradParams& p, int pdl, cudaStream_t s);
 
@@ -110,6 +112,7 @@ struct FinalizeGradParams {
     int fp32;
 };
 
+cudaError_t finalize_grad_prepare(int k, int fp32);
 cudaError_t finalize_grad_launch(const FinalizeGradParams& p, int sms, int pdl, cudaStream_t s);
 
 // ---- residual addition + RMSNorm (mfr_resnorm.cu) --------------------------------
@@ -128,7 +131,7 @@ struct ResNormParams {
     int sf_tiled;
 };
 
-cudaError_t resnorm_prepare(int H, int quant);   // kernel attributes
+cudaError_t resnorm_prepare(int64_t T, int H, int quant, int sms);
 cudaError_t resnorm_launch(const ResNormParams& p, int sms, int pdl, cudaStream_t s);
 
 struct ResNormGradParams {
@@ -146,10 +149,17 @@ struct ResNormGradParams {
     float eps;
 };
 
-// mfr_resnorm_grad.cu: kernel attributes; rows of the workspace of partial gamma gradients.
+// Rows of the workspace of partial gamma gradients: resnorm_grad_partials.
 cudaError_t resnorm_grad_prepare(int H);
 int resnorm_grad_partials(int64_t T, int H, int sms);
 cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s);
+
+// Loads a kernel when its plan is made, so that its first launch may be a captured one.
+template <typename Kernel>
+cudaError_t preload(Kernel* kernel) {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kernel));
+}
 
 // A kernel launch with programmatic stream serialization and a cluster along x, where asked for.
 template <typename... Params, typename... Args>

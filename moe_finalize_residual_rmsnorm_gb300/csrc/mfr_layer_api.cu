@@ -131,6 +131,14 @@ int make_op(moe_op_t* op, Kind kind, int64_t T, const mfr_options* opt) {
     return MFR_OK;
 }
 
+// The end of a plan: its kernels are loaded and set up, or there is none.
+int prepared(moe_op_t* op, cudaError_t e) {
+    if (e == cudaSuccess) return MFR_OK;
+    moe_op_destroy(*op);
+    *op = nullptr;
+    return fail_cuda(MFR_ERR_CUDA, "kernel setup", e);
+}
+
 // What every run checks first.
 int check_op(moe_op_t op, Kind kind) {
     mfr::set_last_error("%s", "");
@@ -238,12 +246,7 @@ int moe_route_plan(moe_op_t* op, int64_t T, int k, int E, int align, const mfr_o
         e = mfr::route_prepare(p->route);
     }
     p->workspace = N > 0 ? mfr::route_workspace(p->route, E) : 0;
-    if (e != cudaSuccess) {
-        moe_op_destroy(p);
-        *op = nullptr;
-        return fail_cuda(MFR_ERR_CUDA, "kernel attribute setup", e);
-    }
-    return MFR_OK;
+    return prepared(op, e);
 }
 
 int64_t moe_route_rows(moe_op_t op) { return op && op->kind == kRoute ? op->R : -1; }
@@ -305,7 +308,7 @@ int moe_dispatch_plan(moe_op_t* op, int64_t T, int64_t H, int k, int64_t R, int 
     p->R = R;
     p->elem_bytes = elem_bytes;
     p->sf_bytes = sf_bytes;
-    return MFR_OK;
+    return prepared(op, mfr::dispatch_prepare());
 }
 
 int moe_dispatch_run(moe_op_t op, const void* x, const void* sf, const int32_t* permuted_row_of,
@@ -376,7 +379,7 @@ int moe_finalize_grad_plan(moe_op_t* op, int64_t T, int64_t H, int k, int64_t R,
     p->k = k;
     p->R = R;
     p->grad_fp32 = grad_fp32;
-    return MFR_OK;
+    return prepared(op, mfr::finalize_grad_prepare(k, grad_fp32));
 }
 
 int moe_finalize_grad_run(moe_op_t op, const void* d_out, const void* expert_out, const int32_t* permuted_row_of,
@@ -427,13 +430,7 @@ int moe_residual_rmsnorm_plan(moe_op_t* op, int64_t T, int64_t H, int quant, int
     p->H = H;
     p->quant = quant;
     p->sf_tiled = sf_layout == MFR_SF_TILED_128x4 ? 1 : 0;
-    const cudaError_t e = mfr::resnorm_prepare(static_cast<int>(H), quant);
-    if (e != cudaSuccess) {
-        moe_op_destroy(p);
-        *op = nullptr;
-        return fail_cuda(MFR_ERR_CUDA, "kernel attribute setup", e);
-    }
-    return MFR_OK;
+    return prepared(op, mfr::resnorm_prepare(T, static_cast<int>(H), quant, p->sms));
 }
 
 int64_t moe_residual_rmsnorm_sf_bytes(moe_op_t op) {
@@ -493,13 +490,7 @@ int moe_residual_rmsnorm_grad_plan(moe_op_t* op, int64_t T, int64_t H, const mfr
     moe_op_s* p = *op;
     p->H = H;
     p->workspace = mfr::resnorm_grad_partials(T, static_cast<int>(H), p->sms) * H * 4;
-    const cudaError_t e = mfr::resnorm_grad_prepare(static_cast<int>(H));
-    if (e != cudaSuccess) {
-        moe_op_destroy(p);
-        *op = nullptr;
-        return fail_cuda(MFR_ERR_CUDA, "kernel attribute setup", e);
-    }
-    return MFR_OK;
+    return prepared(op, mfr::resnorm_grad_prepare(static_cast<int>(H)));
 }
 
 int moe_residual_rmsnorm_grad_run(moe_op_t op, const void* d_out, const float* d_residual_out, const float* residual,

@@ -215,15 +215,6 @@ resnorm_kernel(const ResNormParams p, const int csize) {
     }
 }
 
-template <int CPT, int QUANT, bool WARP>
-cudaError_t launch_one(const ResNormParams& p, int pdl, cudaStream_t s) {
-    const int64_t grid = WARP ? (p.T + kWarpTokens - 1) / kWarpTokens : p.T;
-    const int threads = ((p.H / 8 + CPT - 1) / CPT + 31) / 32 * 32;
-    const int block = WARP ? 32 * kWarpTokens : threads;
-    const int smem = !WARP && CPT > 2 ? 2 * CPT * block * 16 : 0;
-    return layer_launch(resnorm_kernel<CPT, QUANT, WARP>, grid, block, smem, 1, pdl, s, p, 1);
-}
-
 // CTAs per token: 8 or 4 where that many find an SM each and the row is wide
 // enough to pay for the exchange (us for T = 1 by CTAs: H = 2048 1: 1.51, 2:
 // 1.83; H = 4096 1: 1.96, 4: 1.73, 8: 1.71; T = 38, H = 8192 1: 3.05, 4: 2.42).
@@ -232,60 +223,55 @@ int split_ctas(int64_t T, int H, int sms) {
     return T * 8 <= sms ? 8 : T * 4 <= sms ? 4 : 1;
 }
 
-// A cluster of `csize` CTAs per token.
-template <int QUANT>
-cudaError_t launch_split(const ResNormParams& p, int csize, int pdl, cudaStream_t s) {
-    const int block = (p.H / 8 + csize - 1) / csize;
-    return layer_launch(resnorm_kernel<1, QUANT, false, true>, p.T * csize, (block + 31) / 32 * 32, 0, csize, pdl, s, p, csize);
-}
+// A call's kernel and launch geometry.
+struct Form {
+    void (*kernel)(const ResNormParams, int);
+    int64_t grid;
+    int block;
+    int smem;
+    int csize;
+};
 
-template <int CPT, bool WARP>
-cudaError_t launch_quant(const ResNormParams& p, int pdl, cudaStream_t s) {
-    switch (p.quant) {
-        case MFR_QUANT_TOKEN: return launch_one<CPT, MFR_QUANT_TOKEN, WARP>(p, pdl, s);
-        case MFR_QUANT_GROUP128: return launch_one<CPT, MFR_QUANT_GROUP128, WARP>(p, pdl, s);
-        case MFR_QUANT_MX32: return launch_one<CPT, MFR_QUANT_MX32, WARP>(p, pdl, s);
-        default: return launch_one<CPT, MFR_QUANT_NONE, WARP>(p, pdl, s);
-    }
-}
-
-template <int CPT, int QUANT>
-cudaError_t allow_stash() {
-    // the attribute is per kernel, shared by every plan: always the most any plan needs
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(resnorm_kernel<CPT, QUANT, false>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * CPT * 512 * 16);
-}
-
-template <int CPT>
-cudaError_t prepare_stash(int quant) {
+template <int CPT, bool WARP, bool SPLIT = false>
+void (*kernel_for(int quant))(const ResNormParams, int) {
     switch (quant) {
-        case MFR_QUANT_TOKEN: return allow_stash<CPT, MFR_QUANT_TOKEN>();
-        case MFR_QUANT_GROUP128: return allow_stash<CPT, MFR_QUANT_GROUP128>();
-        case MFR_QUANT_MX32: return allow_stash<CPT, MFR_QUANT_MX32>();
-        default: return allow_stash<CPT, MFR_QUANT_NONE>();
+        case MFR_QUANT_TOKEN: return resnorm_kernel<CPT, MFR_QUANT_TOKEN, WARP, SPLIT>;
+        case MFR_QUANT_GROUP128: return resnorm_kernel<CPT, MFR_QUANT_GROUP128, WARP, SPLIT>;
+        case MFR_QUANT_MX32: return resnorm_kernel<CPT, MFR_QUANT_MX32, WARP, SPLIT>;
+        default: return resnorm_kernel<CPT, MFR_QUANT_NONE, WARP, SPLIT>;
     }
+}
+
+Form form_for(int64_t T, int H, int quant, int sms) {
+    const int nck = H / 8;
+    auto threads = [&](int n) { return ((nck + n - 1) / n + 31) / 32 * 32; };     // each with at most n chunks
+    const int csize = split_ctas(T, H, sms);
+    if (csize > 1) return {kernel_for<1, false, true>(quant), T * csize, threads(csize), 0, csize};
+    if (H <= 512) {
+        const int64_t grid = (T + kWarpTokens - 1) / kWarpTokens;
+        return {H <= 256 ? kernel_for<1, true>(quant) : kernel_for<2, true>(quant), grid, 32 * kWarpTokens, 0, 1};
+    }
+    if (H <= 4096) return {kernel_for<1, false>(quant), T, threads(1), 0, 1};
+    if (H <= 8192) return {kernel_for<2, false>(quant), T, threads(2), 0, 1};
+    if (H <= 12288) return {kernel_for<3, false>(quant), T, threads(3), 2 * 3 * 16 * threads(3), 1};
+    return {kernel_for<4, false>(quant), T, threads(4), 2 * 4 * 16 * threads(4), 1};
 }
 
 }  // namespace
 
-cudaError_t resnorm_prepare(int H, int quant) {
-    return H <= 8192 ? cudaSuccess : H <= 12288 ? prepare_stash<3>(quant) : prepare_stash<4>(quant);
+cudaError_t resnorm_prepare(int64_t T, int H, int quant, int sms) {
+    const Form f = form_for(T, H, quant, sms);
+    const cudaError_t e = preload(f.kernel);
+    if (e != cudaSuccess || f.smem == 0) return e;
+    // the attribute is per kernel, shared by every plan: always the most any
+    // plan needs, which the widest rows of each form do
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(f.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                2 * (H <= 12288 ? 3 : 4) * 16 * 512);
 }
 
 cudaError_t resnorm_launch(const ResNormParams& p, int sms, int pdl, cudaStream_t s) {
-    const int csize = split_ctas(p.T, p.H, sms);
-    if (csize > 1) switch (p.quant) {
-        case MFR_QUANT_TOKEN: return launch_split<MFR_QUANT_TOKEN>(p, csize, pdl, s);
-        case MFR_QUANT_GROUP128: return launch_split<MFR_QUANT_GROUP128>(p, csize, pdl, s);
-        case MFR_QUANT_MX32: return launch_split<MFR_QUANT_MX32>(p, csize, pdl, s);
-        default: return launch_split<MFR_QUANT_NONE>(p, csize, pdl, s);
-    }
-    if (p.H <= 256) return launch_quant<1, true>(p, pdl, s);
-    if (p.H <= 512) return launch_quant<2, true>(p, pdl, s);
-    if (p.H <= 4096) return launch_quant<1, false>(p, pdl, s);
-    if (p.H <= 8192) return launch_quant<2, false>(p, pdl, s);
-    if (p.H <= 12288) return launch_quant<3, false>(p, pdl, s);
-    return launch_quant<4, false>(p, pdl, s);
+    const Form f = form_for(p.T, p.H, p.quant, sms);
+    return layer_launch(f.kernel, f.grid, f.block, f.smem, f.csize, pdl, s, p, f.csize);
 }
 
 }  // namespace mfr

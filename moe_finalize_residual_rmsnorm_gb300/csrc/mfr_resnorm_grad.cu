@@ -359,10 +359,12 @@ Form form_for(int H) {
 }  // namespace
 
 cudaError_t resnorm_grad_prepare(int H) {
+    const Form f = form_for(H);
+    cudaError_t e = preload(gamma_sum_kernel);
+    if (e == cudaSuccess) e = preload(f.kernel);
+    if (e != cudaSuccess || f.smem == 0) return e;
     // the attribute is per kernel, shared by every plan: always the most any
     // plan needs, which the widest rows of each form do
-    const Form f = form_for(H);
-    if (f.smem == 0) return cudaSuccess;
     const int widest = H <= 2048 ? 2048 : H <= 4096 ? 4096 : H <= 8192 ? 8192 : kMaxH;
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(f.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 form_for(widest).smem);

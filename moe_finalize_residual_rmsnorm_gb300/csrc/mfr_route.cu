@@ -381,9 +381,12 @@ RouteLaunch route_choose(int64_t N, int64_t R, int E, int forced, int sms) {
 cudaError_t route_prepare(const RouteLaunch& l) {
     // the attribute is per kernel, shared by every plan: always the most any plan needs
     const int most = route_smem(kRouteThreads, kMaxExperts);
+    cudaError_t e = preload(route_empty_kernel);
+    if (e == cudaSuccess) e = preload(route_count_kernel);
+    if (e != cudaSuccess) return e;
     if (l.cluster == 0) return allow_smem(reinterpret_cast<const void*>(route_write_for(l.items)), most);
     const void* f = reinterpret_cast<const void*>(route_kernel_for(l.items));
-    cudaError_t e = allow_smem(f, most);
+    e = allow_smem(f, most);
     if (e == cudaSuccess && l.cluster > 8)
         e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e;

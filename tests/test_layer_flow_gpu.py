@@ -1,6 +1,10 @@
 """The operators around the finalize as they are used: a MoE block forwards in
 8 bits, a training step there and back, many calls in a row without a wait,
 captured graphs, several streams."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -384,3 +388,52 @@ def test_parameters_and_slices_are_taken():
     plan.run(big_x[2:2 + T].clone(), big_r[3:3 + T].clone(), again[0], gamma.detach().clone(), 1e-6, again[1])
     torch.cuda.synchronize()
     assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1]) and out[1].any()
+
+
+CAPTURE_FIRST = r"""
+import torch
+import moe_finalize_residual_rmsnorm_gb300 as mfr
+T, H, k, E = 50, {H}, {k}, 16
+I32, F32, B16 = torch.int32, torch.float32, torch.bfloat16
+def new(shape, dtype=F32):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+g = torch.Generator(device="cuda").manual_seed(1)
+ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=I32)
+x, r = torch.randn((T, H), generator=g, device="cuda").to(B16), torch.randn((T, H), generator=g, device="cuda")
+gamma, w = torch.ones(H, dtype=B16, device="cuda"), torch.rand((T, k), generator=g, device="cuda")
+route, norm, back = mfr.RoutePlan(T, k, E), mfr.ResidualNormPlan(T, H, quant=mfr.QUANT_TOKEN), mfr.ResidualNormGradPlan(T, H)
+disp, grad = mfr.DispatchPlan(T, H, k), mfr.FinalizeGradPlan(T, H, k)
+b = dict(row=new((T, k), I32), slot=new((T * k,), I32), off=new((E + 1,), I32), cnt=new((E,), I32), r=new((T, H)),
+         y=new((T, H), B16), q=new((T, H), torch.float8_e4m3fn), sf=new((T, 1)), rows=new((T * k, H), B16),
+         dE=new((T * k, H), B16), dw=new((T, k)), dx=new((T, H), B16), dr=new((T, H)), dg=new((H,)))
+ws = new((back.workspace_bytes(),), torch.uint8)
+def calls():
+    norm.run(x, r, b["r"], gamma, 1e-6, b["y"], b["q"], b["sf"])
+    route.run(ids, b["row"], b["slot"], b["off"], b["cnt"])
+    disp.run(b["y"], b["row"], b["slot"], b["rows"])
+    grad.run(x, b["rows"], b["row"], b["slot"], w, b["dE"], b["dw"])
+    disp.run_grad(b["dE"], b["row"], b["dx"])
+    back.run(b["dx"], r, b["r"], gamma, 1e-6, b["dr"], b["dg"], ws)
+torch.cuda.synchronize()
+graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+first = dict((n, t.clone()) for n, t in b.items())
+calls()
+torch.cuda.synchronize()
+for n, t in b.items():
+    assert torch.equal(first[n].view(torch.uint8), t.view(torch.uint8)), n
+    assert t.view(torch.uint8).any(), n
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("H,k", [(64, 2), (1024, 5), (4096, 8), (9000, 12)])
+def test_the_first_calls_of_a_process_may_be_captured(H, k):
+    """Plans load their kernels: in a new process nothing runs before the capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST.format(H=H, k=k)], cwd=root, capture_output=True, text=True,
+                       timeout=240)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
