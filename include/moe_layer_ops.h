@@ -21,7 +21,7 @@
  * moe_finalize_rmsnorm_last_error(), no run allocates), and:
  *  - Plans (moe_op_t) are made for the current device and belong to one
  *    operator; each run function refuses another operator's plan.  A plan holds
- *    a 4-byte status word on the device and nothing else there.
+ *    its status word on the device (8 bytes) and nothing else there.
  *  - mfr_options: enable_pdl, debug_checks and sentinel_skip have the meaning
  *    they have for the finalize, except that these kernels read EVERY input
  *    after waiting on the preceding kernel in the stream, so any input may
@@ -33,6 +33,10 @@
  *    before it in the stream.
  *  - A plan may be run concurrently on several streams; calls that are given
  *    the same workspace, graphs that captured it included, must not overlap.
+ *    The status word belongs to the plan: its bits are those of all its calls
+ *    since the last reading, whatever their streams.  With debug_checks a
+ *    plan's calls take turns, each from its launch to its check, so that a
+ *    call reports its own bits.
  *  - Runs may be captured into a graph, which must not outlive its plans.  Make
  *    plans before the capture; debug_checks waits for the stream and cannot be
  *    captured.
@@ -72,8 +76,9 @@ typedef struct moe_op_s* moe_op_t;
 /* Frees a plan (NULL is allowed).  No call with it may be in flight. */
 void moe_op_destroy(moe_op_t op);
 
-/* Waits for `stream`, reads the plan's status word (MFR_STATUS_* bits) into
- * *device_status and clears it. */
+/* Waits for `stream`, then reads the plan's status word (MFR_STATUS_* bits) into
+ * *device_status and clears it in one step: a bit that a call on another
+ * stream raises meanwhile is in this reading or in the next. */
 int moe_op_get_status(moe_op_t op, void* stream, int* device_status);
 
 /* Bytes of the device workspace the operator's run function takes (0: none

@@ -9,6 +9,7 @@
 #include "moe_layer_ops.h"
 #include "mfr_internal.h"
 #include "mfr_layer.h"
+#include "mfr_status.h"
 
 namespace {
 
@@ -44,7 +45,7 @@ struct moe_op_s {
     int sms;
     mfr_options opt;
     mfr::RouteLaunch route;
-    int* d_status;
+    mfr::StatusWord status;
 };
 
 namespace {
@@ -121,9 +122,7 @@ int make_op(moe_op_t* op, Kind kind, int64_t T, const mfr_options* opt) {
     p->device = dev;
     p->sms = sms;
     p->opt = o;
-    if ((e = cudaMalloc(&p->d_status, sizeof(int))) == cudaSuccess) e = cudaMemset(p->d_status, 0, sizeof(int));
-    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);   // cleared before a run on any stream
-    if (e != cudaSuccess) {
+    if ((e = mfr::status_make(p->status)) != cudaSuccess) {
         moe_op_destroy(p);
         return fail_cuda(MFR_ERR_CUDA, "the plan's status word", e);
     }
@@ -165,11 +164,17 @@ int check_workspace(moe_op_t op, const void* workspace, int64_t bytes) {
     return MFR_OK;
 }
 
+int take(moe_op_t op, void* stream, int* bits) {
+    const cudaError_t e = mfr::status_take(op->status, static_cast<cudaStream_t>(stream), bits);
+    return e == cudaSuccess ? MFR_OK : fail_cuda(MFR_ERR_CUDA, "reading the status word", e);
+}
+
+// The end of a run, whose DebugTurn the caller holds.
 int finish(moe_op_t op, cudaError_t e, void* stream) {
     if (e != cudaSuccess) return fail_cuda(MFR_ERR_LAUNCH, "kernel launch", e);
     if (op->opt.debug_checks) {
         int st = 0;
-        const int rc = moe_op_get_status(op, stream, &st);
+        const int rc = take(op, stream, &st);
         if (rc != MFR_OK) return rc;
         if (st & MFR_STATUS_TIMEOUT)
             return MFR_FAIL(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
@@ -182,7 +187,7 @@ mfr::MapParams map_params(moe_op_t op, const int32_t* row_of, const int32_t* slo
     mfr::MapParams m{};
     m.row_of = row_of;
     m.slot_of = slot_of;
-    m.status = op->d_status;
+    m.status = op->status.words;
     m.T = op->T;
     m.R = op->R;
     m.k = op->k;
@@ -196,22 +201,15 @@ extern "C" {
 
 void moe_op_destroy(moe_op_t op) {
     if (!op) return;
-    if (op->d_status) cudaFree(op->d_status);
-    cudaGetLastError();
+    mfr::status_free(op->status);
     delete op;
 }
 
 int moe_op_get_status(moe_op_t op, void* stream, int* device_status) {
     mfr::set_last_error("%s", "");
     if (!op || !device_status) return MFR_FAIL(MFR_ERR_INVALID_ARG, "the plan and device_status must not be NULL");
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int h = 0;
-    cudaError_t e = cudaMemcpyAsync(&h, op->d_status, sizeof(int), cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(op->d_status, 0, sizeof(int), s);
-    if (e != cudaSuccess) return fail_cuda(MFR_ERR_CUDA, "reading the status word", e);
-    *device_status = h;
-    return MFR_OK;
+    const std::lock_guard<std::mutex> turn(op->status.turn);
+    return take(op, stream, device_status);
 }
 
 int64_t moe_op_workspace_bytes(moe_op_t op) { return op ? op->workspace : -1; }
@@ -275,7 +273,7 @@ int moe_route_run(moe_op_t op, const int32_t* expert_ids, int32_t* permuted_row_
     p.offsets = expert_offsets;
     p.counts = expert_counts;
     p.block_counts = static_cast<int32_t*>(workspace);
-    p.status = op->d_status;
+    p.status = op->status.words;
     p.N = N;
     p.R = op->R;
     p.E = op->E;
@@ -283,6 +281,7 @@ int moe_route_run(moe_op_t op, const int32_t* expert_ids, int32_t* permuted_row_
     p.sentinel = op->opt.sentinel_skip ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int pdl = op->opt.enable_pdl ? 1 : 0;
+    const mfr::DebugTurn turn(op->status, op->opt.debug_checks != 0);
     return finish(op, N > 0 ? mfr::route_launch(p, op->route, pdl, s) : mfr::route_empty_launch(p, pdl, s), stream);
 }
 
@@ -337,6 +336,7 @@ int moe_dispatch_run(moe_op_t op, const void* x, const void* sf, const int32_t* 
     p.sf_out = static_cast<uint8_t*>(sf_out);
     p.row_bytes = static_cast<int>(row);
     p.sf_bytes = op->sf_bytes;
+    const mfr::DebugTurn turn(op->status, op->opt.debug_checks != 0);
     return finish(op, mfr::dispatch_launch(p, op->sms, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
@@ -359,6 +359,7 @@ int moe_dispatch_grad_run(moe_op_t op, const void* d_rows, const int32_t* permut
     p.d_rows = static_cast<const uint16_t*>(d_rows);
     p.d_x = static_cast<uint16_t*>(d_x);
     p.H = static_cast<int>(H);
+    const mfr::DebugTurn turn(op->status, op->opt.debug_checks != 0);
     return finish(op, mfr::dispatch_grad_launch(p, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
@@ -410,6 +411,7 @@ int moe_finalize_grad_run(moe_op_t op, const void* d_out, const void* expert_out
     p.d_w = d_topk_weights;
     p.H = static_cast<int>(H);
     p.fp32 = op->grad_fp32;
+    const mfr::DebugTurn turn(op->status, op->opt.debug_checks != 0);
     return finish(op, mfr::finalize_grad_launch(p, op->sms, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
@@ -477,6 +479,7 @@ int moe_residual_rmsnorm_run(moe_op_t op, const void* x, const float* residual_i
     p.eps = eps;
     p.quant = op->quant;
     p.sf_tiled = op->sf_tiled;
+    const mfr::DebugTurn turn(op->status, op->opt.debug_checks != 0);
     return finish(op, mfr::resnorm_launch(p, op->sms, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
@@ -520,10 +523,11 @@ int moe_residual_rmsnorm_grad_run(moe_op_t op, const void* d_out, const float* d
     p.d_x = static_cast<uint16_t*>(d_x);
     p.d_gamma = d_gamma;
     p.partial = static_cast<float*>(workspace);
-    p.status = op->d_status;
+    p.status = op->status.words;
     p.T = op->T;
     p.H = static_cast<int>(op->H);
     p.eps = eps;
+    const mfr::DebugTurn turn(op->status, op->opt.debug_checks != 0);
     return finish(op, mfr::resnorm_grad_launch(p, op->sms, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 

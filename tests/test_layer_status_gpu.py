@@ -1,0 +1,87 @@
+"""The status word of the plans: no bit is lost between streams and threads."""
+import threading
+
+import pytest
+import torch
+
+import layer_ref as ref
+import moe_finalize_residual_rmsnorm_gb300 as mfr
+
+pytestmark = pytest.mark.gpu
+
+I32, F32, B16 = torch.int32, torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    mfr.build()
+    mfr.load_library()
+
+
+def new(shape, dtype=F32):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+class Route:
+    """A small route whose ids are all in range, or one of them is not."""
+
+    def __init__(self, plan, bad):
+        T, k, E = plan.T, plan.k, plan.E
+        ids = ref.draw_ids(T, k, E, seed=1)
+        if bad:
+            ids[T // 2, 0] = E
+        self.plan, self.ids = plan, torch.from_numpy(ids).cuda()
+        self.outs = [new((T, k), I32), new((plan.R,), I32), new((E + 1,), I32), new((E,), I32)]
+
+    def run(self, stream=None):
+        self.plan.run(self.ids, *self.outs, None, stream)
+
+
+def test_a_status_read_on_one_stream_keeps_the_bits_of_another():
+    """A call that raises a bit runs on one stream while the word is read and
+    cleared on another, at ever different moments: every call's bit is reported by
+    one of the reads."""
+    plan = mfr.RoutePlan(8, 8, 16)
+    call = Route(plan, bad=True)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    lost = 0
+    for n in range(4000):
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(n % 50 * 1000)               # up to about 25 us
+        call.run(b)
+        got = plan.get_status(a) | plan.get_status(a) | plan.get_status(a)
+        b.synchronize()
+        got |= plan.get_status(b)
+        lost += got != mfr.STATUS_BAD_INDEX
+    assert lost == 0
+
+
+def test_debug_checks_report_each_threads_own_call():
+    """Two threads, each with a stream, share a plan with debug_checks: every
+    call of the one that passes a bad id fails, no call of the other does."""
+    plan = mfr.RoutePlan(8, 8, 16, debug_checks=True)
+    calls = [Route(plan, bad=False), Route(plan, bad=True)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    failures, errors = [0, 0], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            for _ in range(500):
+                try:
+                    calls[i].run(streams[i])
+                except mfr.MFRError as e:
+                    assert e.name == "MFR_ERR_BAD_INDEX"
+                    failures[i] += 1
+        except Exception as e:                             # reported by the test, not by the thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert failures == [0, 500]
