@@ -33,7 +33,7 @@
  * Conventions for every entry point:
  *  - Pointers named "device" are CUDA device (or managed) addresses on the
  *    plan's device; the caller owns all of them.  No entry point allocates on
- *    a run: only the *_plan functions allocate (a 4-byte device status word
+ *    a run: only the *_plan functions allocate (a device status word of 8 bytes
  *    each), and moe_finalize_rmsnorm_destroy frees it.
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream).  Runs are asynchronous on that stream.
@@ -125,9 +125,11 @@ void moe_finalize_rmsnorm_default_options(mfr_options* opt);
  * expert_out of R rows (R >= 0) on the CURRENT device.  opt may be NULL
  * (defaults).  Validates the shape, checks the device is compute capability
  * 10.3, fixes the variant and launch geometry, and allocates the plan's
- * 4-byte device status word (cleared).  On failure *plan is set to NULL.
+ * device status word (8 bytes, cleared).  On failure *plan is set to NULL.
  * A plan is immutable after creation and may be run concurrently on several
- * streams; they share its status word. */
+ * streams; they share its status word, whose bits are those of all the plan's
+ * calls since the last reading.  With debug_checks its calls take turns, each
+ * from its launch to its check, so that a call reports its own bits. */
 int moe_finalize_rmsnorm_plan(mfr_plan_t* plan, int64_t T, int64_t H, int k, int64_t R,
                               const mfr_options* opt);
 
@@ -244,8 +246,10 @@ int moe_finalize_rmsnorm_run_host(mfr_plan_t plan, const void* h_expert_out,
                                   const void* h_gamma, float eps, void* h_out,
                                   void* d_workspace, int64_t workspace_bytes, void* stream);
 
-/* Waits for `stream`, reads the plan's status word into *device_status
- * (MFR_STATUS_* bits) and clears it.  Returns MFR_OK or a CUDA error code. */
+/* Waits for `stream`, then reads the plan's status word into *device_status
+ * (MFR_STATUS_* bits) and clears it in one step: a bit that a call on another
+ * stream raises meanwhile is in this reading or in the next.  Returns MFR_OK or
+ * MFR_ERR_CUDA. */
 int moe_finalize_rmsnorm_get_status(mfr_plan_t plan, void* stream, int* device_status);
 
 /* Enqueues an EMPTY kernel with exactly the plan's launch geometry (grid,

@@ -10,6 +10,7 @@
 
 #include "moe_finalize_rmsnorm.h"
 #include "mfr_internal.h"
+#include "mfr_status.h"
 
 struct mfr_plan_s {
     int64_t T;
@@ -20,7 +21,7 @@ struct mfr_plan_s {
     int sm_count;
     mfr_options opt;
     mfr::Launch launch;
-    int* d_status;
+    mfr::StatusWord status;
     bool fused;        // residual + RMSNorm (false: moe_finalize_plan's plain finalize)
     bool fp4;          // made by moe_finalize_rmsnorm_nvfp4_plan: NVFP4 output
     bool expert_norm;  // made by moe_finalize_expert_rmsnorm_plan
@@ -54,6 +55,13 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// The caller holds the status word's turn.
+int take_status(mfr_plan_t plan, void* stream, int* bits) {
+    const cudaError_t e = mfr::status_take(plan->status, static_cast<cudaStream_t>(stream), bits);
+    if (e == cudaSuccess) return MFR_OK;
+    cudaGetLastError();
+    return fail_cuda(MFR_ERR_CUDA, "reading the status word", e);
+}
 
 }  // namespace
 
@@ -221,20 +229,11 @@ int make_plan(mfr_plan_t* plan, int64_t T, int64_t H, int k, int64_t R, const mf
         }
     }
 
-    int* status = nullptr;
-    if ((e = cudaMalloc(&status, sizeof(int))) != cudaSuccess) {
-        cudaGetLastError();
-        return fail_cuda(MFR_ERR_CUDA, "cudaMalloc(status)", e);
-    }
-    if ((e = cudaMemset(status, 0, sizeof(int))) != cudaSuccess) {
-        cudaFree(status);
-        cudaGetLastError();
-        return fail_cuda(MFR_ERR_CUDA, "cudaMemset(status)", e);
-    }
     mfr_plan_s* p = new (std::nothrow) mfr_plan_s{};
-    if (!p) {
-        cudaFree(status);
-        return fail(MFR_ERR_CUDA, "out of host memory");
+    if (!p) return fail(MFR_ERR_CUDA, "out of host memory");
+    if ((e = mfr::status_make(p->status)) != cudaSuccess) {
+        delete p;
+        return fail_cuda(MFR_ERR_CUDA, "the plan's status word", e);
     }
     p->T = T;
     p->H = H;
@@ -244,7 +243,6 @@ int make_plan(mfr_plan_t* plan, int64_t T, int64_t H, int k, int64_t R, const mf
     p->sm_count = sms;
     p->opt = o;
     p->launch = l;
-    p->d_status = status;
     p->fused = fused;
     p->fp4 = fp4;
     p->expert_norm = expert_norm;
@@ -329,7 +327,7 @@ int moe_finalize_expert_rmsnorm_run(mfr_plan_t plan, const void* expert_out, con
     p.topk_weights = topk_weights;
     p.gamma = static_cast<const uint16_t*>(gamma);
     p.out = static_cast<uint16_t*>(out);
-    p.status = plan->d_status;
+    p.status = plan->status.words;
     p.T = T;
     p.R = R;
     p.H = static_cast<int>(H);
@@ -338,6 +336,7 @@ int moe_finalize_expert_rmsnorm_run(mfr_plan_t plan, const void* expert_out, con
     p.sentinel = plan->opt.sentinel_skip ? 1 : 0;
     p.early_trigger = plan->launch.early_trigger;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
     e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
                                                    : mfr::expert_norm_launch(p, plan->launch, s);
     if (e != cudaSuccess) {
@@ -346,7 +345,7 @@ int moe_finalize_expert_rmsnorm_run(mfr_plan_t plan, const void* expert_out, con
     }
     if (plan->opt.debug_checks) {
         int st = 0;
-        const int rc = moe_finalize_rmsnorm_get_status(plan, stream, &st);
+        const int rc = take_status(plan, stream, &st);
         if (rc != MFR_OK) return rc;
         if (st & MFR_STATUS_BAD_INDEX)
             return fail(MFR_ERR_BAD_INDEX, "a permuted_row_of entry was outside [0, %lld)", (long long)R);
@@ -387,7 +386,7 @@ int moe_finalize_run(mfr_plan_t plan, const void* expert_out, const int32_t* per
     p.permuted_row_of = permuted_row_of;
     p.topk_weights = topk_weights;
     p.out = static_cast<uint16_t*>(out);
-    p.status = plan->d_status;
+    p.status = plan->status.words;
     p.T = T;
     p.R = R;
     p.H = static_cast<int>(H);
@@ -395,6 +394,7 @@ int moe_finalize_run(mfr_plan_t plan, const void* expert_out, const int32_t* per
     p.sentinel = plan->opt.sentinel_skip ? 1 : 0;
     p.early_trigger = plan->launch.early_trigger;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
     e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
                                                    : mfr::rows_launch(p, plan->launch, s);
     if (e != cudaSuccess) {
@@ -403,7 +403,7 @@ int moe_finalize_run(mfr_plan_t plan, const void* expert_out, const int32_t* per
     }
     if (plan->opt.debug_checks) {
         int st = 0;
-        const int rc = moe_finalize_rmsnorm_get_status(plan, stream, &st);
+        const int rc = take_status(plan, stream, &st);
         if (rc != MFR_OK) return rc;
         if (st & MFR_STATUS_TIMEOUT)
             return fail(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
@@ -480,7 +480,7 @@ int fused_run(mfr_plan_t plan, const void* expert_out, const int32_t* permuted_r
     p.out_q = static_cast<uint8_t*>(out_q);
     p.out_sf = static_cast<uint8_t*>(out_sf);
     p.s_enc = s_enc;
-    p.status = plan->d_status;
+    p.status = plan->status.words;
     p.T = T;
     p.R = R;
     p.H = static_cast<int>(H);
@@ -490,6 +490,7 @@ int fused_run(mfr_plan_t plan, const void* expert_out, const int32_t* permuted_r
     p.early_trigger = plan->launch.early_trigger;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
     e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
                                                    : mfr::rows_launch(p, plan->launch, s);
     if (e != cudaSuccess) {
@@ -498,7 +499,7 @@ int fused_run(mfr_plan_t plan, const void* expert_out, const int32_t* permuted_r
     }
     if (plan->opt.debug_checks) {
         int st = 0;
-        const int rc = moe_finalize_rmsnorm_get_status(plan, stream, &st);
+        const int rc = take_status(plan, stream, &st);
         if (rc != MFR_OK) return rc;
         if (st & MFR_STATUS_TIMEOUT)
             return fail(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
@@ -624,17 +625,8 @@ int moe_finalize_rmsnorm_run_host(mfr_plan_t plan, const void* h_expert_out, con
 int moe_finalize_rmsnorm_get_status(mfr_plan_t plan, void* stream, int* device_status) {
     g_last_error[0] = '\0';
     if (!plan || !device_status) return fail(MFR_ERR_INVALID_ARG, "plan and device_status must not be NULL");
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int h = 0;
-    cudaError_t e = cudaMemcpyAsync(&h, plan->d_status, sizeof(int), cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(plan->d_status, 0, sizeof(int), s);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail_cuda(MFR_ERR_CUDA, "reading the status word", e);
-    }
-    *device_status = h;
-    return MFR_OK;
+    const std::lock_guard<std::mutex> turn(plan->status.turn);
+    return take_status(plan, stream, device_status);
 }
 
 int moe_finalize_rmsnorm_wait_selftest(mfr_plan_t plan, int64_t limit_cycles, int arrive, void* stream) {
@@ -642,7 +634,7 @@ int moe_finalize_rmsnorm_wait_selftest(mfr_plan_t plan, int64_t limit_cycles, in
     if (!plan) return fail(MFR_ERR_INVALID_ARG, "plan must not be NULL");
     if (limit_cycles < 1 || limit_cycles > (int64_t(1) << 32))
         return fail(MFR_ERR_INVALID_ARG, "limit_cycles must be in [1, 2^32] (got %lld)", (long long)limit_cycles);
-    const cudaError_t e = mfr::wait_selftest_launch(plan->d_status, static_cast<long long>(limit_cycles),
+    const cudaError_t e = mfr::wait_selftest_launch(plan->status.words, static_cast<long long>(limit_cycles),
                                                     arrive ? 1 : 0, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -655,7 +647,7 @@ int moe_finalize_rmsnorm_launch_floor(mfr_plan_t plan, void* stream) {
     g_last_error[0] = '\0';
     if (!plan) return fail(MFR_ERR_INVALID_ARG, "plan must not be NULL");
     if (plan->T == 0) return MFR_OK;
-    const cudaError_t e = mfr::floor_launch(plan->d_status, plan->launch, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = mfr::floor_launch(plan->status.words, plan->launch, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail_cuda(MFR_ERR_LAUNCH, "floor kernel launch", e);
@@ -703,7 +695,7 @@ int moe_finalize_rmsnorm_launch_floor_work(mfr_plan_t plan, int work, const void
     p.residual_in = residual_in;
     p.residual_out = residual_out;
     p.out = static_cast<uint16_t*>(out);
-    p.status = plan->d_status;
+    p.status = plan->status.words;
     p.T = T;
     p.R = R;
     p.H = static_cast<int>(H);
@@ -734,10 +726,7 @@ int moe_finalize_rmsnorm_plan_info(mfr_plan_t plan, mfr_plan_info* info) {
 
 void moe_finalize_rmsnorm_destroy(mfr_plan_t plan) {
     if (!plan) return;
-    if (plan->d_status) {
-        cudaFree(plan->d_status);
-        cudaGetLastError();
-    }
+    mfr::status_free(plan->status);
     delete plan;
 }
 

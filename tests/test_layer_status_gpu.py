@@ -39,12 +39,36 @@ class Route:
         self.plan.run(self.ids, *self.outs, None, stream)
 
 
-def test_a_status_read_on_one_stream_keeps_the_bits_of_another():
+class Finalize:
+    """The same for the finalize: rows in range, or one of them is not."""
+
+    def __init__(self, plan, bad):
+        T, H, k, R = plan.T, plan.H, plan.k, plan.R
+        row_of = torch.arange(T * k, dtype=I32).view(T, k)
+        if bad:
+            row_of[T // 2, 0] = R
+        g = torch.Generator().manual_seed(1)
+        self.plan, self.row_of = plan, row_of.cuda()
+        self.rows, self.w = torch.randn((R, H), generator=g).to(B16).cuda(), torch.rand((T, k), generator=g).cuda()
+        self.res, self.res_out, self.out = new((T, H)), new((T, H)), new((T, H), B16)
+        self.gamma = torch.ones(H, dtype=B16, device="cuda")
+
+    def run(self, stream=None):
+        self.plan.run(self.rows, self.row_of, self.w, self.res, self.res_out, self.gamma, 1e-6, self.out, stream)
+
+
+CALLS = {"route": (Route, lambda **kw: mfr.RoutePlan(8, 8, 16, **kw)),
+         "finalize": (Finalize, lambda **kw: mfr.Plan(8, 256, 4, **kw))}
+
+
+@pytest.mark.parametrize("kind", CALLS)
+def test_a_status_read_on_one_stream_keeps_the_bits_of_another(kind):
     """A call that raises a bit runs on one stream while the word is read and
     cleared on another, at ever different moments: every call's bit is reported by
     one of the reads."""
-    plan = mfr.RoutePlan(8, 8, 16)
-    call = Route(plan, bad=True)
+    make, plan_of = CALLS[kind]
+    plan = plan_of()
+    call = make(plan, bad=True)
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     lost = 0
@@ -59,11 +83,13 @@ def test_a_status_read_on_one_stream_keeps_the_bits_of_another():
     assert lost == 0
 
 
-def test_debug_checks_report_each_threads_own_call():
+@pytest.mark.parametrize("kind", CALLS)
+def test_debug_checks_report_each_threads_own_call(kind):
     """Two threads, each with a stream, share a plan with debug_checks: every
     call of the one that passes a bad id fails, no call of the other does."""
-    plan = mfr.RoutePlan(8, 8, 16, debug_checks=True)
-    calls = [Route(plan, bad=False), Route(plan, bad=True)]
+    make, plan_of = CALLS[kind]
+    plan = plan_of(debug_checks=True)
+    calls = [make(plan, bad=False), make(plan, bad=True)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     failures, errors = [0, 0], []
     torch.cuda.synchronize()
