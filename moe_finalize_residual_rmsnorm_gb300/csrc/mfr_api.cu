@@ -63,6 +63,24 @@ int take_status(mfr_plan_t plan, void* stream, int* bits) {
     return fail_cuda(MFR_ERR_CUDA, "reading the status word", e);
 }
 
+// The end of a run, whose DebugTurn the caller holds.
+int finish_run(mfr_plan_t plan, cudaError_t e, void* stream) {
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail_cuda(MFR_ERR_LAUNCH, "kernel launch", e);
+    }
+    if (plan->opt.debug_checks) {
+        int st = 0;
+        const int rc = take_status(plan, stream, &st);
+        if (rc != MFR_OK) return rc;
+        if (st & MFR_STATUS_TIMEOUT)
+            return fail(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
+        if (st & MFR_STATUS_BAD_INDEX)
+            return fail(MFR_ERR_BAD_INDEX, "a permuted_row_of entry was outside [0, %lld)", (long long)plan->R);
+    }
+    return MFR_OK;
+}
+
 }  // namespace
 
 void mfr::set_last_error(const char* fmt, ...) {
@@ -339,18 +357,7 @@ int moe_finalize_expert_rmsnorm_run(mfr_plan_t plan, const void* expert_out, con
     const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
     e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
                                                    : mfr::expert_norm_launch(p, plan->launch, s);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail_cuda(MFR_ERR_LAUNCH, "kernel launch", e);
-    }
-    if (plan->opt.debug_checks) {
-        int st = 0;
-        const int rc = take_status(plan, stream, &st);
-        if (rc != MFR_OK) return rc;
-        if (st & MFR_STATUS_BAD_INDEX)
-            return fail(MFR_ERR_BAD_INDEX, "a permuted_row_of entry was outside [0, %lld)", (long long)R);
-    }
-    return MFR_OK;
+    return finish_run(plan, e, stream);
 }
 
 int moe_finalize_run(mfr_plan_t plan, const void* expert_out, const int32_t* permuted_row_of,
@@ -397,20 +404,7 @@ int moe_finalize_run(mfr_plan_t plan, const void* expert_out, const int32_t* per
     const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
     e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
                                                    : mfr::rows_launch(p, plan->launch, s);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail_cuda(MFR_ERR_LAUNCH, "kernel launch", e);
-    }
-    if (plan->opt.debug_checks) {
-        int st = 0;
-        const int rc = take_status(plan, stream, &st);
-        if (rc != MFR_OK) return rc;
-        if (st & MFR_STATUS_TIMEOUT)
-            return fail(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
-        if (st & MFR_STATUS_BAD_INDEX)
-            return fail(MFR_ERR_BAD_INDEX, "a permuted_row_of entry was outside [0, %lld)", (long long)R);
-    }
-    return MFR_OK;
+    return finish_run(plan, e, stream);
 }
 
 }  // extern "C"
@@ -493,20 +487,7 @@ int fused_run(mfr_plan_t plan, const void* expert_out, const int32_t* permuted_r
     const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
     e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
                                                    : mfr::rows_launch(p, plan->launch, s);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail_cuda(MFR_ERR_LAUNCH, "kernel launch", e);
-    }
-    if (plan->opt.debug_checks) {
-        int st = 0;
-        const int rc = take_status(plan, stream, &st);
-        if (rc != MFR_OK) return rc;
-        if (st & MFR_STATUS_TIMEOUT)
-            return fail(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
-        if (st & MFR_STATUS_BAD_INDEX)
-            return fail(MFR_ERR_BAD_INDEX, "a permuted_row_of entry was outside [0, %lld)", (long long)R);
-    }
-    return MFR_OK;
+    return finish_run(plan, e, stream);
 }
 
 }  // namespace

@@ -111,3 +111,27 @@ def test_debug_checks_report_each_threads_own_call(kind):
         t.join()
     assert not errors
     assert failures == [0, 500]
+
+
+@pytest.mark.parametrize("cls,fused", [(mfr.Plan, True), (mfr.FinalizePlan, False), (mfr.ExpertNormPlan, False)])
+def test_debug_checks_report_a_timeout_in_every_form(cls, fused):
+    """A wait that ran out (the self test's) is an error of the checked call that
+    reads it, whatever the plan computes; the next call is clean."""
+    T, H, k = 4, 256, 4
+    plan = cls(T, H, k, debug_checks=True)
+    rows, row_of = torch.ones((T * k, H), dtype=B16, device="cuda"), torch.arange(T * k, dtype=I32, device="cuda").view(T, k)
+    w, gamma, out = torch.ones((T, k), device="cuda"), torch.ones(H, dtype=B16, device="cuda"), new((T, H), B16)
+
+    def run():
+        if fused:
+            plan.run(rows, row_of, w, new((T, H)), new((T, H)), gamma, 1e-6, out)
+        elif cls is mfr.FinalizePlan:
+            plan.run(rows, row_of, w, out)
+        else:
+            plan.run(rows, row_of, w, gamma, 1e-6, out)
+    run()
+    plan.wait_selftest(2_000_000, arrive=False)
+    with pytest.raises(mfr.MFRError, match="timed out"):
+        run()
+    run()
+    assert plan.get_status() == 0
