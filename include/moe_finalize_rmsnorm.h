@@ -299,8 +299,9 @@ int moe_finalize_rmsnorm_wait_selftest(mfr_plan_t plan, int64_t limit_cycles, in
 /* Copies what the plan decided into *info. */
 int moe_finalize_rmsnorm_plan_info(mfr_plan_t plan, mfr_plan_info* info);
 
-/* Frees the plan and its status word.  NULL is a no-op.  The caller makes
- * sure no run of this plan is still in flight. */
+/* Frees the plan and its status word, also while a graph that does not use it is
+ * being captured.  NULL is a no-op.  The caller makes sure no run of this plan
+ * is still in flight. */
 void moe_finalize_rmsnorm_destroy(mfr_plan_t plan);
 
 /* ---- finalize with an RMSNorm per expert row (a reading) ----------------

@@ -73,7 +73,8 @@ extern "C" {
 
 typedef struct moe_op_s* moe_op_t;
 
-/* Frees a plan (NULL is allowed).  No call with it may be in flight. */
+/* Frees a plan (NULL is allowed), also while a graph that does not use it is
+ * being captured.  No call with it may be in flight. */
 void moe_op_destroy(moe_op_t op);
 
 /* Waits for `stream`, then reads the plan's status word (MFR_STATUS_* bits) into

@@ -43,8 +43,15 @@ cudaError_t status_make(StatusWord& w) {
     return e;
 }
 
+// A plan may go at any time (Python's collector chooses its own), also while a
+// graph is being captured, by this thread or another: outside the relaxed mode
+// cudaFree would then fail and end that capture.
 void status_free(StatusWord& w) {
-    if (w.words) cudaFree(w.words);
+    if (!w.words) return;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;   // mode: the one before
+    cudaFree(w.words);
+    if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
     w.words = nullptr;
     cudaGetLastError();
 }

@@ -135,3 +135,27 @@ def test_debug_checks_report_a_timeout_in_every_form(cls, fused):
         run()
     run()
     assert plan.get_status() == 0
+
+
+@pytest.mark.parametrize("kind", CALLS)
+@pytest.mark.parametrize("where", ["this thread", "another thread"])
+def test_a_plan_may_go_while_a_graph_is_captured(kind, where):
+    """Closing a plan that the graph has nothing to do with leaves the capture whole."""
+    make, plan_of = CALLS[kind]
+    call, gone = make(plan_of(), bad=False), plan_of()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        call.run()
+        if where == "this thread":
+            gone.close()
+        else:
+            t = threading.Thread(target=gone.close)
+            t.start()
+            t.join()
+        call.run()
+    outs = call.outs if kind == "route" else [call.res_out, call.out]
+    assert not any(o.any() for o in outs)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert any(o.any() for o in outs) and call.plan.get_status() == 0
