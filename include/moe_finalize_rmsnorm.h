@@ -85,7 +85,9 @@ typedef struct mfr_options {
     int force_variant; /* MFR_VARIANT_*; AUTO picks by T, H and the device */
     int cluster_size;  /* MFR_VARIANT_CLUSTER: CTAs per token (2, 4, 8 or 16); 0 = auto */
     int debug_checks;  /* 1: run() waits for the kernel and returns MFR_ERR_BAD_INDEX
-                          when a slot index was out of range (slow; for debugging) */
+                          when a slot index was out of range (slow; for debugging).
+                          Refused (MFR_ERR_INVALID_ARG) on a stream that is being
+                          captured; the capture goes on */
     int sentinel_skip; /* 1: a NEGATIVE permuted_row_of entry marks a slot whose expert
                           is not local (expert parallelism): the slot adds nothing and
                           is not an error.  Entries >= R still raise
@@ -248,8 +250,9 @@ int moe_finalize_rmsnorm_run_host(mfr_plan_t plan, const void* h_expert_out,
 
 /* Waits for `stream`, then reads the plan's status word into *device_status
  * (MFR_STATUS_* bits) and clears it in one step: a bit that a call on another
- * stream raises meanwhile is in this reading or in the next.  Returns MFR_OK or
- * MFR_ERR_CUDA. */
+ * stream raises meanwhile is in this reading or in the next.  Refused
+ * (MFR_ERR_INVALID_ARG) on a stream that is being captured; works on others
+ * meanwhile. */
 int moe_finalize_rmsnorm_get_status(mfr_plan_t plan, void* stream, int* device_status);
 
 /* Enqueues an EMPTY kernel with exactly the plan's launch geometry (grid,

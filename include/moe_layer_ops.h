@@ -38,8 +38,10 @@
  *    plan's calls take turns, each from its launch to its check, so that a
  *    call reports its own bits.
  *  - Runs may be captured into a graph, which must not outlive its plans.  Make
- *    plans before the capture; debug_checks waits for the stream and cannot be
- *    captured.
+ *    plans before the capture.  debug_checks and moe_op_get_status wait for
+ *    their stream: on a stream that is being captured they are refused with
+ *    MFR_ERR_INVALID_ARG and the capture goes on; on another stream they work
+ *    while it does.
  *  - T == 0 is a no-op returning MFR_OK unless the function says otherwise.
  *
  * The pair of index maps.  A pair s = t * k + j (token t, slot j) has the row

@@ -63,6 +63,18 @@ int take_status(mfr_plan_t plan, void* stream, int* bits) {
     return fail_cuda(MFR_ERR_CUDA, "reading the status word", e);
 }
 
+// What every run checks last.
+int check_place(mfr_plan_t plan, void* stream) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) { cudaGetLastError(); return fail_cuda(MFR_ERR_CUDA, "cudaGetDevice", e); }
+    if (dev != plan->device)
+        return fail(MFR_ERR_INVALID_ARG, "current device %d is not the plan's device %d", dev, plan->device);
+    if (plan->opt.debug_checks && mfr::being_captured(static_cast<cudaStream_t>(stream)))
+        return fail(MFR_ERR_INVALID_ARG, "a call with debug_checks waits for its stream, which is being captured");
+    return MFR_OK;
+}
+
 // The end of a run, whose DebugTurn the caller holds.
 int finish_run(mfr_plan_t plan, cudaError_t e, void* stream) {
     if (e != cudaSuccess) {
@@ -333,11 +345,8 @@ int moe_finalize_expert_rmsnorm_run(mfr_plan_t plan, const void* expert_out, con
     if (overlaps(out, n_out, expert_out, n_e) || overlaps(out, n_out, permuted_row_of, n_tk) ||
         overlaps(out, n_out, topk_weights, n_tk) || overlaps(out, n_out, gamma, static_cast<size_t>(H) * 2))
         return fail(MFR_ERR_INVALID_ARG, "out overlaps an input");
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) { cudaGetLastError(); return fail_cuda(MFR_ERR_CUDA, "cudaGetDevice", e); }
-    if (dev != plan->device)
-        return fail(MFR_ERR_INVALID_ARG, "current device %d is not the plan's device %d", dev, plan->device);
+    const int rc = check_place(plan, stream);
+    if (rc != MFR_OK) return rc;
 
     mfr::Params p{};
     p.expert_out = static_cast<const uint16_t*>(expert_out);
@@ -355,8 +364,8 @@ int moe_finalize_expert_rmsnorm_run(mfr_plan_t plan, const void* expert_out, con
     p.early_trigger = plan->launch.early_trigger;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
-    e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
-                                                   : mfr::expert_norm_launch(p, plan->launch, s);
+    const cudaError_t e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
+                                                                        : mfr::expert_norm_launch(p, plan->launch, s);
     return finish_run(plan, e, stream);
 }
 
@@ -382,11 +391,8 @@ int moe_finalize_run(mfr_plan_t plan, const void* expert_out, const int32_t* per
     if (overlaps(out, n_out, expert_out, n_e) || overlaps(out, n_out, permuted_row_of, n_tk) ||
         overlaps(out, n_out, topk_weights, n_tk))
         return fail(MFR_ERR_INVALID_ARG, "out overlaps an input");
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) { cudaGetLastError(); return fail_cuda(MFR_ERR_CUDA, "cudaGetDevice", e); }
-    if (dev != plan->device)
-        return fail(MFR_ERR_INVALID_ARG, "current device %d is not the plan's device %d", dev, plan->device);
+    const int rc = check_place(plan, stream);
+    if (rc != MFR_OK) return rc;
 
     mfr::Params p{};
     p.expert_out = static_cast<const uint16_t*>(expert_out);
@@ -402,8 +408,8 @@ int moe_finalize_run(mfr_plan_t plan, const void* expert_out, const int32_t* per
     p.early_trigger = plan->launch.early_trigger;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
-    e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
-                                                   : mfr::rows_launch(p, plan->launch, s);
+    const cudaError_t e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
+                                                                        : mfr::rows_launch(p, plan->launch, s);
     return finish_run(plan, e, stream);
 }
 
@@ -457,11 +463,8 @@ int fused_run(mfr_plan_t plan, const void* expert_out, const int32_t* permuted_r
     if (fp4 && overlaps(out_q, out_bytes[0], out_sf, out_bytes[1]))
         return fail(MFR_ERR_INVALID_ARG, "out_q and out_sf overlap");
 
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) { cudaGetLastError(); return fail_cuda(MFR_ERR_CUDA, "cudaGetDevice", e); }
-    if (dev != plan->device)
-        return fail(MFR_ERR_INVALID_ARG, "current device %d is not the plan's device %d", dev, plan->device);
+    const int rc = check_place(plan, stream);
+    if (rc != MFR_OK) return rc;
 
     mfr::Params p{};
     p.expert_out = static_cast<const uint16_t*>(expert_out);
@@ -485,8 +488,8 @@ int fused_run(mfr_plan_t plan, const void* expert_out, const int32_t* permuted_r
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const mfr::DebugTurn turn(plan->status, plan->opt.debug_checks != 0);
-    e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
-                                                   : mfr::rows_launch(p, plan->launch, s);
+    const cudaError_t e = plan->launch.variant == MFR_VARIANT_STREAM ? mfr::stream_launch(p, plan->launch, s)
+                                                                        : mfr::rows_launch(p, plan->launch, s);
     return finish_run(plan, e, stream);
 }
 
@@ -606,6 +609,8 @@ int moe_finalize_rmsnorm_run_host(mfr_plan_t plan, const void* h_expert_out, con
 int moe_finalize_rmsnorm_get_status(mfr_plan_t plan, void* stream, int* device_status) {
     g_last_error[0] = '\0';
     if (!plan || !device_status) return fail(MFR_ERR_INVALID_ARG, "plan and device_status must not be NULL");
+    if (mfr::being_captured(static_cast<cudaStream_t>(stream)))
+        return fail(MFR_ERR_INVALID_ARG, "the stream to wait for is being captured");
     const std::lock_guard<std::mutex> turn(plan->status.turn);
     return take_status(plan, stream, device_status);
 }

@@ -146,12 +146,15 @@ int check_op(moe_op_t op, Kind kind) {
     return MFR_OK;
 }
 
-int check_device(moe_op_t op) {
+// What every run checks last.
+int check_place(moe_op_t op, void* stream) {
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail_cuda(MFR_ERR_CUDA, "cudaGetDevice", e);
     if (dev != op->device)
         return MFR_FAIL(MFR_ERR_INVALID_ARG, "current device %d is not the plan's device %d", dev, op->device);
+    if (op->opt.debug_checks && mfr::being_captured(static_cast<cudaStream_t>(stream)))
+        return MFR_FAIL(MFR_ERR_INVALID_ARG, "a call with debug_checks waits for its stream, which is being captured");
     return MFR_OK;
 }
 
@@ -208,6 +211,8 @@ void moe_op_destroy(moe_op_t op) {
 int moe_op_get_status(moe_op_t op, void* stream, int* device_status) {
     mfr::set_last_error("%s", "");
     if (!op || !device_status) return MFR_FAIL(MFR_ERR_INVALID_ARG, "the plan and device_status must not be NULL");
+    if (mfr::being_captured(static_cast<cudaStream_t>(stream)))
+        return MFR_FAIL(MFR_ERR_INVALID_ARG, "the stream to wait for is being captured");
     const std::lock_guard<std::mutex> turn(op->status.turn);
     return take(op, stream, device_status);
 }
@@ -265,7 +270,7 @@ int moe_route_run(moe_op_t op, const int32_t* expert_ids, int32_t* permuted_row_
     const Span out[] = {{permuted_row_of, N * 4}, {slot_of_row, op->R * 4}, {expert_offsets, (op->E + 1) * int64_t(4)},
                         {expert_counts, op->E * int64_t(4)}, {workspace, op->workspace}};
     if (outputs_meet(out, in)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "two arguments overlap");
-    if ((rc = check_device(op)) != MFR_OK) return rc;
+    if ((rc = check_place(op, stream)) != MFR_OK) return rc;
     mfr::RouteParams p{};
     p.ids = expert_ids;
     p.row_of = permuted_row_of;
@@ -327,7 +332,7 @@ int moe_dispatch_run(moe_op_t op, const void* x, const void* sf, const int32_t* 
     const Span in[] = {{x, T * row}, {sf, T * op->sf_bytes}, {permuted_row_of, N * 4}, {slot_of_row, R * 4}};
     const Span out[] = {{rows_out, R * row}, {sf_out, R * op->sf_bytes}};
     if (outputs_meet(out, in)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "an output overlaps another argument");
-    if ((rc = check_device(op)) != MFR_OK) return rc;
+    if ((rc = check_place(op, stream)) != MFR_OK) return rc;
     mfr::DispatchParams p{};
     p.m = map_params(op, permuted_row_of, slot_of_row);
     p.x = static_cast<const uint8_t*>(x);
@@ -353,7 +358,7 @@ int moe_dispatch_grad_run(moe_op_t op, const void* d_rows, const int32_t* permut
     const Span in[] = {{d_rows, R * H * 2}, {permuted_row_of, N * 4}};
     const Span out[] = {{d_x, T * H * 2}};
     if (outputs_meet(out, in)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "d_x overlaps an input");
-    if ((rc = check_device(op)) != MFR_OK) return rc;
+    if ((rc = check_place(op, stream)) != MFR_OK) return rc;
     mfr::DispatchGradParams p{};
     p.m = map_params(op, permuted_row_of, nullptr);
     p.d_rows = static_cast<const uint16_t*>(d_rows);
@@ -401,7 +406,7 @@ int moe_finalize_grad_run(moe_op_t op, const void* d_out, const void* expert_out
                        {slot_of_row, R * 4}, {topk_weights, N * 4}};
     const Span out[] = {{d_expert_out, R * H * 2}, {d_topk_weights, N * 4}};
     if (outputs_meet(out, in)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "an output overlaps another argument");
-    if ((rc = check_device(op)) != MFR_OK) return rc;
+    if ((rc = check_place(op, stream)) != MFR_OK) return rc;
     mfr::FinalizeGradParams p{};
     p.m = map_params(op, permuted_row_of, slot_of_row);
     p.d_out = d_out;
@@ -465,7 +470,7 @@ int moe_residual_rmsnorm_run(moe_op_t op, const void* x, const float* residual_i
     const Span in[] = {{x, n * 2}, {residual_in == residual_out ? nullptr : residual_in, n * 4}, {gamma, op->H * 2}};
     const Span outs[] = {{residual_out, n * 4}, {out, n * 2}, {out_q, n}, {out_sf, moe_residual_rmsnorm_sf_bytes(op)}};
     if (outputs_meet(outs, in)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "an output overlaps another argument");
-    if ((rc = check_device(op)) != MFR_OK) return rc;
+    if ((rc = check_place(op, stream)) != MFR_OK) return rc;
     mfr::ResNormParams p{};
     p.x = static_cast<const uint16_t*>(x);
     p.residual_in = residual_in;
@@ -513,7 +518,7 @@ int moe_residual_rmsnorm_grad_run(moe_op_t op, const void* d_out, const float* d
                        {residual, n * 4}, {gamma, op->H * 2}};
     const Span outs[] = {{d_residual_in, n * 4}, {d_x, n * 2}, {d_gamma, op->H * 4}, {workspace, op->workspace}};
     if (outputs_meet(outs, in)) return MFR_FAIL(MFR_ERR_INVALID_ARG, "an output overlaps another argument");
-    if ((rc = check_device(op)) != MFR_OK) return rc;
+    if ((rc = check_place(op, stream)) != MFR_OK) return rc;
     mfr::ResNormGradParams p{};
     p.d_out = static_cast<const uint16_t*>(d_out);
     p.d_res = d_residual_out;

@@ -30,7 +30,24 @@ struct OnDevice {
     }
 };
 
+// Lets this thread free and wait while a graph is being captured elsewhere:
+// outside the relaxed mode such calls fail and end that capture.
+struct Relaxed {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;    // then the one before
+    const bool changed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    ~Relaxed() {
+        if (changed) cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+};
+
 }  // namespace
+
+bool being_captured(cudaStream_t s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) == cudaSuccess) return st != cudaStreamCaptureStatusNone;
+    cudaGetLastError();
+    return true;      // the default stream, while a stream that it is in step with is being captured
+}
 
 cudaError_t status_make(StatusWord& w) {
     cudaFuncAttributes a;     // loads the kernel, which a later capture could not
@@ -44,14 +61,11 @@ cudaError_t status_make(StatusWord& w) {
 }
 
 // A plan may go at any time (Python's collector chooses its own), also while a
-// graph is being captured, by this thread or another: outside the relaxed mode
-// cudaFree would then fail and end that capture.
+// graph is being captured, by this thread or another.
 void status_free(StatusWord& w) {
     if (!w.words) return;
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;   // mode: the one before
+    const Relaxed relaxed;
     cudaFree(w.words);
-    if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
     w.words = nullptr;
     cudaGetLastError();
 }
@@ -59,6 +73,7 @@ void status_free(StatusWord& w) {
 cudaError_t status_take(StatusWord& w, cudaStream_t s, int* bits) {
     const OnDevice on(w.device);
     if (on.error != cudaSuccess) return on.error;
+    const Relaxed relaxed;
     void* args[] = {&w.words};
     int h = 0;
     cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(take_status_kernel), dim3(1), dim3(1), args, 0, s);

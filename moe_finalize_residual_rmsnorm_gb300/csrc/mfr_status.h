@@ -20,6 +20,9 @@ void status_free(StatusWord& w);
 // pending on return.  The caller holds w.turn.
 cudaError_t status_take(StatusWord& w, cudaStream_t s, int* bits);
 
+// Whether the stream is being captured, so that nothing may wait for it.
+bool being_captured(cudaStream_t s);
+
 // A call's turn with a plan that checks each call (debug_checks): from its launch to
 // its reading, so that the bits it finds are its own.  No lock otherwise.
 class DebugTurn {

@@ -159,3 +159,34 @@ def test_a_plan_may_go_while_a_graph_is_captured(kind, where):
     graph.replay()
     torch.cuda.synchronize()
     assert any(o.any() for o in outs) and call.plan.get_status() == 0
+
+
+@pytest.mark.parametrize("kind", CALLS)
+def test_checks_and_readings_while_a_graph_is_captured(kind):
+    """On another stream they work; on the captured one they are refused, before
+    anything is enqueued, and the capture goes on."""
+    make, plan_of = CALLS[kind]
+    call, checked, refused = make(plan_of(), False), make(plan_of(debug_checks=True), False), make(plan_of(debug_checks=True), False)
+    wrong = make(plan_of(debug_checks=True), True)
+
+    def outs(c):
+        return c.outs if kind == "route" else [c.res_out, c.out]
+    graph, side, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        call.run()
+        checked.run(other)
+        assert checked.plan.get_status(other) == 0
+        with pytest.raises(mfr.MFRError) as e:
+            wrong.run(other)
+        assert e.value.name == "MFR_ERR_BAD_INDEX"
+        for refusal in (refused.run, refused.plan.get_status):
+            with pytest.raises(mfr.MFRError, match="being captured") as e:
+                refusal(side)
+            assert e.value.name == "MFR_ERR_INVALID_ARG"
+        call.run()
+    assert any(o.any() for o in outs(checked))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert any(o.any() for o in outs(call)) and not any(o.any() for o in outs(refused))
+    assert call.plan.get_status() == 0
