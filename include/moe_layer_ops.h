@@ -37,6 +37,8 @@
  *    since the last reading, whatever their streams.  With debug_checks a
  *    plan's calls take turns, each from its launch to its check, so that a
  *    call reports its own bits.
+ *    MFR_STATUS_TIMEOUT: every output of that call, its workspace included, is
+ *    invalid.
  *  - Runs may be captured into a graph, which must not outlive its plans.  Make
  *    plans before the capture.  debug_checks and moe_op_get_status wait for
  *    their stream: on a stream that is being captured they are refused with
@@ -200,6 +202,12 @@ int moe_residual_rmsnorm_run(moe_op_t op, const void* x, const float* residual_i
  *  workspace       moe_op_workspace_bytes(op) bytes, 16-byte aligned
  * Matrices and gamma 16-byte aligned, d_gamma 4-byte.  Needs H % 8 == 0, 8 <= H <= 16384. */
 int moe_residual_rmsnorm_grad_plan(moe_op_t* op, int64_t T, int64_t H, const mfr_options* opt);
+/* Failure-path self test.  Rows of more than 512 columns pass through a ring in
+ * shared memory, whose waits give up after about 2 s with MFR_STATUS_TIMEOUT.  This
+ * sets another limit for the plan's later runs, in SM cycles from 0 (every
+ * wait gives up at once) to 4000000000 (the limit a plan begins with), else
+ * MFR_ERR_INVALID_ARG.  The next run is not affected by one that gave up. */
+int moe_residual_rmsnorm_grad_set_wait_limit(moe_op_t op, int64_t limit_cycles);
 int moe_residual_rmsnorm_grad_run(moe_op_t op, const void* d_out, const float* d_residual_out, const float* residual,
                                   const void* gamma, float eps, float* d_residual_in, void* d_x, float* d_gamma,
                                   void* workspace, int64_t workspace_bytes, void* stream);

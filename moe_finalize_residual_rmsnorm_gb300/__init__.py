@@ -123,6 +123,7 @@ SIGNATURES = {
     "moe_residual_rmsnorm_sf_bytes": (_I64, [_VP]),
     "moe_residual_rmsnorm_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP]),
     "moe_residual_rmsnorm_grad_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, ctypes.POINTER(Options)]),
+    "moe_residual_rmsnorm_grad_set_wait_limit": (_I, [_VP, _I64]),
     "moe_residual_rmsnorm_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP, _I64, _VP]),
 }
 

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "moe_finalize_rmsnorm.h"
+#include "mfr_policy.h"
 
 namespace mfr {
 
@@ -121,8 +122,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return true;
 }
 
-// Every wait of the kernels: bounded at ~2 s at 2 GHz.
-constexpr long long kWaitCycles = 4000000000LL;
+// A wait with the library's limit.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_wait_bounded(bar, parity, kWaitCycles);
 }

@@ -147,10 +147,11 @@ struct ResNormGradParams {
     int64_t T;
     int H;
     float eps;
+    long long wait_limit; // cycles after which a wait of the ring gives up: kWaitCycles, or less to test that
 };
 
 // Rows of the workspace of partial gamma gradients: resnorm_grad_partials.
-cudaError_t resnorm_grad_prepare(int H);
+cudaError_t resnorm_grad_prepare(int H, bool limited);
 int resnorm_grad_partials(int64_t T, int H, int sms);
 cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s);
 

@@ -33,6 +33,7 @@ struct moe_op_s {
     int64_t H;
     int64_t R;
     int64_t workspace;
+    int64_t wait_limit;
     int k;
     int E;
     int align;
@@ -146,13 +147,19 @@ int check_op(moe_op_t op, Kind kind) {
     return MFR_OK;
 }
 
-// What every run checks last.
-int check_place(moe_op_t op, void* stream) {
+int check_device(moe_op_t op) {
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail_cuda(MFR_ERR_CUDA, "cudaGetDevice", e);
     if (dev != op->device)
         return MFR_FAIL(MFR_ERR_INVALID_ARG, "current device %d is not the plan's device %d", dev, op->device);
+    return MFR_OK;
+}
+
+// What every run checks last.
+int check_place(moe_op_t op, void* stream) {
+    const int rc = check_device(op);
+    if (rc != MFR_OK) return rc;
     if (op->opt.debug_checks && mfr::being_captured(static_cast<cudaStream_t>(stream)))
         return MFR_FAIL(MFR_ERR_INVALID_ARG, "a call with debug_checks waits for its stream, which is being captured");
     return MFR_OK;
@@ -497,8 +504,23 @@ int moe_residual_rmsnorm_grad_plan(moe_op_t* op, int64_t T, int64_t H, const mfr
     if (rc != MFR_OK) return rc;
     moe_op_s* p = *op;
     p->H = H;
+    p->wait_limit = mfr::kWaitCycles;
     p->workspace = mfr::resnorm_grad_partials(T, static_cast<int>(H), p->sms) * H * 4;
-    return prepared(op, mfr::resnorm_grad_prepare(static_cast<int>(H)));
+    return prepared(op, mfr::resnorm_grad_prepare(static_cast<int>(H), false));
+}
+
+int moe_residual_rmsnorm_grad_set_wait_limit(moe_op_t op, int64_t limit_cycles) {
+    int rc = check_op(op, kResNormGrad);
+    if (rc != MFR_OK) return rc;
+    if (limit_cycles < 0 || limit_cycles > mfr::kWaitCycles)
+        return MFR_FAIL(MFR_ERR_INVALID_ARG, "limit_cycles must be in [0, %lld] (got %lld)", mfr::kWaitCycles, (long long)limit_cycles);
+    if ((rc = check_device(op)) != MFR_OK) return rc;
+    if (limit_cycles != mfr::kWaitCycles) {
+        const cudaError_t e = mfr::resnorm_grad_prepare(static_cast<int>(op->H), true);
+        if (e != cudaSuccess) return fail_cuda(MFR_ERR_CUDA, "kernel setup", e);
+    }
+    op->wait_limit = limit_cycles;
+    return MFR_OK;
 }
 
 int moe_residual_rmsnorm_grad_run(moe_op_t op, const void* d_out, const float* d_residual_out, const float* residual,
@@ -528,6 +550,7 @@ int moe_residual_rmsnorm_grad_run(moe_op_t op, const void* d_out, const float* d
     p.d_x = static_cast<uint16_t*>(d_x);
     p.d_gamma = d_gamma;
     p.partial = static_cast<float*>(workspace);
+    p.wait_limit = op->wait_limit;
     p.status = op->status.words;
     p.T = op->T;
     p.H = static_cast<int>(op->H);

@@ -12,6 +12,9 @@
 
 namespace mfr {
 
+// The limit of every on-chip wait, in SM cycles: ~2 s at 2 GHz.
+constexpr long long kWaitCycles = 4000000000LL;
+
 constexpr int kMaxK = 16;               // slots per token
 constexpr int kMaxH = 16384;            // hidden size
 constexpr int kRowsMaxThreads = 512;    // one-CTA-per-token kernels

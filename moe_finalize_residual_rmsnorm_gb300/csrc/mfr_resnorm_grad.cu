@@ -48,7 +48,18 @@ constexpr int stages_ahead() { return GT == 128 ? 2 : 3; }
 template <int GT>
 int ring_smem(int stages) { return kRingHeader + stages * stage_bytes<GT>(); }
 
-template <int GT, int NT>
+// One side's wait for the other.  When it runs out the CTA's producer stops
+// filling, its consumers leave together at the next sum, without their row of
+// the partial sums, and MFR_STATUS_TIMEOUT says so.
+// LIMITED: the limit is the call's, at 0 none waits (a kernel of its own: as an
+// argument of the usual one the limit cost 4096 x 16384 2 %).
+template <bool LIMITED>
+__device__ __forceinline__ bool ring_wait(const ResNormGradParams& p, uint32_t bar, uint32_t parity) {
+    if constexpr (LIMITED) return p.wait_limit > 0 && mbar_wait_bounded(bar, parity, p.wait_limit);
+    return mbar_wait(bar, parity);
+}
+
+template <int GT, int NT, bool LIMITED>
 __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const ResNormGradParams p) {
     constexpr int CB = tile_cols<GT>(), WARPS = GT / 32;
     static_assert(NT + stages_ahead<GT>() <= kMaxStages && 16 * kMaxStages <= kRingHeader, "the barriers fit the header");
@@ -76,7 +87,7 @@ __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const Res
         bool ok = true;
         for (int64_t t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
             for (int b = 0; b < ntiles; ++b) {
-                const bool freed = fill < S || mbar_wait(smem_addr(&bars[S + s]), phase ^ 1u);
+                const bool freed = fill < S || ring_wait<LIMITED>(p, smem_addr(&bars[S + s]), phase ^ 1u);
                 if (!__all_sync(0xFFFFFFFFu, freed)) {
                     if (lane == 0) atomicOr(p.status, MFR_STATUS_TIMEOUT);
                     ok = false;
@@ -96,7 +107,8 @@ __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const Res
                 if (++s == S) { s = 0; phase ^= 1u; }
             }
         }
-        // every copy has landed before the CTA exits
+        // every copy has landed before the CTA exits (they need no one else: the
+        // full limit, whatever the ring's)
         if (lane == 0)
             for (int64_t f = fill > S ? fill - S : 0; f < fill; ++f)
                 if (!mbar_wait(smem_addr(&bars[f % S]), static_cast<uint32_t>(f / S) & 1u)) {
@@ -126,7 +138,7 @@ __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const Res
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
             if (b >= ntiles) break;
-            ok = ok && mbar_wait(smem_addr(&bars[s]), phase);
+            ok = ok && ring_wait<LIMITED>(p, smem_addr(&bars[s]), phase);
             const unsigned char* st = ring + s * stage_bytes<GT>();
             if (b * CB + tid * 4 < H) {
                 const float4 r = *reinterpret_cast<const float4*>(st + tid * 16);
@@ -342,24 +354,25 @@ struct Form {
 };
 
 template <int GT, int NT>
-Form ring_form(int H) {
+Form ring_form(int H, bool limited) {
     const int tiles = (H + tile_cols<GT>() - 1) / tile_cols<GT>();
-    return {resnorm_grad_ring<GT, NT>, GT + 32, ring_smem<GT>(tiles + stages_ahead<GT>()), 512 / GT, 1};
+    return {limited ? resnorm_grad_ring<GT, NT, true> : resnorm_grad_ring<GT, NT, false>, GT + 32, ring_smem<GT>(tiles + stages_ahead<GT>()), 512 / GT, 1};
 }
 
-Form form_for(int H) {
+// limited: the call has a wait limit of its own (rows that pass through the ring).
+Form form_for(int H, bool limited) {
     if (H <= 256) return {resnorm_grad_narrow<1>, 32 * kNarrowWarps, 0, 3, kNarrowWarps};
     if (H <= kNarrowMaxH) return {resnorm_grad_narrow<2>, 32 * kNarrowWarps, 0, 2, kNarrowWarps};
-    if (H <= 2048) return ring_form<128, 4>(H);
-    if (H <= 4096) return ring_form<256, 4>(H);
-    if (H <= 8192) return ring_form<512, 4>(H);
-    return ring_form<512, 8>(H);
+    if (H <= 2048) return ring_form<128, 4>(H, limited);
+    if (H <= 4096) return ring_form<256, 4>(H, limited);
+    if (H <= 8192) return ring_form<512, 4>(H, limited);
+    return ring_form<512, 8>(H, limited);
 }
 
 }  // namespace
 
-cudaError_t resnorm_grad_prepare(int H) {
-    const Form f = form_for(H);
+cudaError_t resnorm_grad_prepare(int H, bool limited) {
+    const Form f = form_for(H, limited);
     cudaError_t e = preload(gamma_sum_kernel);
     if (e == cudaSuccess) e = preload(f.kernel);
     if (e != cudaSuccess || f.smem == 0) return e;
@@ -367,17 +380,17 @@ cudaError_t resnorm_grad_prepare(int H) {
     // plan needs, which the widest rows of each form do
     const int widest = H <= 2048 ? 2048 : H <= 4096 ? 4096 : H <= 8192 ? 8192 : kMaxH;
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(f.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                form_for(widest).smem);
+                                form_for(widest, limited).smem);
 }
 
 int resnorm_grad_partials(int64_t T, int H, int sms) {
-    const Form f = form_for(H);
+    const Form f = form_for(H, false);
     const int64_t want = (T + f.tokens - 1) / f.tokens, most = static_cast<int64_t>(sms) * f.per_sm;
     return static_cast<int>(want < most ? want : most);
 }
 
 cudaError_t resnorm_grad_launch(const ResNormGradParams& p, int sms, int pdl, cudaStream_t s) {
-    const Form f = form_for(p.H);
+    const Form f = form_for(p.H, p.wait_limit != kWaitCycles);
     const int grid = resnorm_grad_partials(p.T, p.H, sms);
     cudaError_t e = cudaSuccess;
     if (grid > 0) e = layer_launch(f.kernel, grid, f.threads, f.smem, 1, pdl, s, p);

@@ -258,6 +258,12 @@ class ResidualNormGradPlan(_OpPlan):
         self._make("moe_residual_rmsnorm_grad_plan", self.T, self.H, enable_pdl=enable_pdl, debug_checks=debug_checks)
         self._need = self.workspace_bytes()
 
+    def set_wait_limit(self, limit_cycles: int) -> None:
+        """SM cycles after which an on-chip wait of this plan's runs gives up and
+        raises STATUS_TIMEOUT; 0: at once (C: moe_residual_rmsnorm_grad_set_wait_limit)."""
+        _check(self._lib.moe_residual_rmsnorm_grad_set_wait_limit(self._h, int(limit_cycles)),
+               "moe_residual_rmsnorm_grad_set_wait_limit")
+
     def run(self, d_out, d_residual_out, residual, gamma, eps: float, d_residual_in, d_gamma, workspace, d_x=None,
             stream=None) -> None:
         """d_out bf16, d_residual_out FP32 (None: zeros), residual FP32 (the
