@@ -59,13 +59,6 @@ static_assert(kMaxK % 4 == 0, "the consumers read the slot weights four at a tim
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return smem_addr(p); }
 
-// Bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned) from
-// global memory into this CTA's shared memory; completion is counted on bar.
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-
 // MAXTILES: upper bound on ceil(H / CB) for this instantiation;
 // FUSED: residual + RMSNorm (true) or plain finalize (false); EN: per-expert
 // RMSNorm (with FUSED = false); SFT (with FP4): block scales in the tiled
@@ -193,10 +186,10 @@ stream_kernel(const Params p, const int nstages, const int stage_bytes)
                 __syncwarp();
                 if (kParallelIssue || (kParallelFills > 0 && fill < kParallelFills)) {
                     if (valid)
-                        bulk_g2s(smem_u32(st + kHeaderBytes + lane * row_bytes),
-                                 p.expert_out + static_cast<int64_t>(row) * H + c0, static_cast<uint32_t>(cb * 2), bar);
+                        bulk_load(smem_u32(st + kHeaderBytes + lane * row_bytes),
+                                  p.expert_out + static_cast<int64_t>(row) * H + c0, static_cast<uint32_t>(cb * 2), bar);
                     if (FUSED && lane == kMaxK)
-                        bulk_g2s(smem_u32(st + res_off), p.residual_in + t * H + c0, static_cast<uint32_t>(cb * 4), bar);
+                        bulk_load(smem_u32(st + res_off), p.residual_in + t * H + c0, static_cast<uint32_t>(cb * 4), bar);
                 } else {
                     int32_t rl[kMaxK];
 #pragma unroll
@@ -204,13 +197,13 @@ stream_kernel(const Params p, const int nstages, const int stage_bytes)
                     if (lane == 0) {
                         // the residual segment first (measured: prefill 246.1 -> 245.3 us)
                         if (FUSED)   // only fused stages carry a residual segment (and count its bytes)
-                            bulk_g2s(smem_u32(st + res_off), p.residual_in + t * H + c0, static_cast<uint32_t>(cb * 4), bar);
+                            bulk_load(smem_u32(st + res_off), p.residual_in + t * H + c0, static_cast<uint32_t>(cb * 4), bar);
 #pragma unroll
                         for (int j = 0; j < kMaxK; ++j)
                             if (mask & (1u << j))
-                                bulk_g2s(smem_u32(st + kHeaderBytes + j * row_bytes),
-                                         p.expert_out + static_cast<int64_t>(rl[j]) * H + c0,
-                                         static_cast<uint32_t>(cb * 2), bar);
+                                bulk_load(smem_u32(st + kHeaderBytes + j * row_bytes),
+                                          p.expert_out + static_cast<int64_t>(rl[j]) * H + c0,
+                                          static_cast<uint32_t>(cb * 2), bar);
                     }
                 }
                 ++fill;
