@@ -44,6 +44,9 @@
  *    their stream: on a stream that is being captured they are refused with
  *    MFR_ERR_INVALID_ARG and the capture goes on; on another stream they work
  *    while it does.
+ *  - Sums are FP32, in an order that the plan fixes: the same plan and inputs
+ *    give the same bits.  A plan of another T may add a token's terms in
+ *    another order, so a token's last bits can change with the size of its batch.
  *  - T == 0 is a no-op returning MFR_OK unless the function says otherwise.
  *
  * The pair of index maps.  A pair s = t * k + j (token t, slot j) has the row
@@ -142,7 +145,7 @@ int moe_dispatch_grad_run(moe_op_t op, const void* d_rows, const int32_t* permut
 /* ---- gradient of the finalize's weighted sum --------------------------------
  * For out[t] = sum_j w[t, j] * E[permuted_row_of[t, j]] (moe_finalize_run):
  *   d_expert_out[permuted_row_of[t, j], h] = bf16( w[t, j] * d_out[t, h] )
- *   d_topk_weights[t, j] = sum_h d_out[t, h] * E[permuted_row_of[t, j], h]   (FP32, fixed order)
+ *   d_topk_weights[t, j] = sum_h d_out[t, h] * E[permuted_row_of[t, j], h]   (FP32)
  * d_topk_weights of a pair without a row is 0.
  *  grad_fp32   0: d_out is bf16 [T, H]; 1: FP32 [T, H]
  *  expert_out, d_out, d_expert_out 16-byte aligned; the others 4-byte
@@ -192,7 +195,7 @@ int moe_residual_rmsnorm_run(moe_op_t op, const void* x, const float* residual_i
  * with d_out the gradient of y and d_residual_out that of r from elsewhere:
  *   d_r = d_residual_out + inv * (gamma * d_out) - r * inv^3 * mean_h(gamma * d_out * r)
  *   d_residual_in = d_r (FP32);   d_x = bf16(d_r)
- *   d_gamma[h] = sum_t d_out[t, h] * r[t, h] * inv[t]           (FP32, fixed order)
+ *   d_gamma[h] = sum_t d_out[t, h] * r[t, h] * inv[t]           (FP32)
  *  d_out           bf16 [T, H]
  *  d_residual_out  FP32 [T, H], or NULL for zeros
  *  residual        FP32 [T, H]: r, the forward's residual_out

@@ -11,7 +11,7 @@
 // behind the segment's own loads.
 //
 // Measured on GB300 at 16384 x 4096 bf16 rows, k = 8, blocks padded to 128
-// rows (1.27 GB): 189 us, the copy rate of half reads and half writes (a plain
+// rows (1.27 GB): 190 us, the copy rate of half reads and half writes (a plain
 // fill of as many bytes runs at 0.6 of it); 4096 x 8192 8-bit rows with scales
 // 44.7 us (0.92).  Copies through shared memory (a bulk load and k bulk stores a
 // segment, 4 or 8 warps with 2 or 3 stages) took 6 % longer; stores that keep
@@ -41,9 +41,11 @@ __device__ __forceinline__ void copy_scales(const DispatchParams& p, int64_t t, 
 
 // One warp per (token, segment of C * 32 chunks of 16 bytes), behind the warps
 // that look after the rows' side of the maps, `rpw` rows each.  Segments of 2
-// KB where the call fills the GPU, fewer map reads a byte, else of 512 bytes
-// (measured at 16384 x 4096, rows' warps last: 213 us with 512-byte segments,
-// 207 with 1 KB, 206 with 2 KB, 208 with 4 KB).
+// KB where the call fills the GPU, fewer map reads a byte, else of 512 bytes.
+// Measured with segments of 512 bytes, 1, 2 and 4 KB: 16384 x 4096 in blocks of 128
+// 187, 188, 190, 192 us, 4096 x 8192 8-bit rows with scales 43.8, 44.2, 44.8,
+// 46.3; so where the rows' warps come first, 512 bytes would do for every
+// call (with them last: 208, 204, 208, 207 us).
 template <int C>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchParams p, const int segs, const int64_t row_warps,
                                                             const int rpw) {

@@ -11,13 +11,16 @@
 // k = 2 at 16384 x 4096: 126 us with one, 99 with two; with more than eight
 // slots sixteen loads and two CTAs of 256 threads an SM, k = 16: 653 us, 820 in
 // two groups of eight), and 768 threads an SM (measured at k = 8: 344 us, 1.01
-// of the copy rate; with 512 threads and more registers 430 us and more, with
-// 1024 and fewer 380).
+// of the copy rate, and with an FP32 gradient 362 us, 1.01; with 512 threads and
+// more registers 430 us and more, with 1024 and fewer 380).  At the registers
+// that 768 threads leave, three of the bf16 forms (k = 3 and 4, and k = 5 to 8 with
+// and without a cluster) spill 12 bytes a thread.
 // Rows are written past L1.  The dot products are summed per thread in column
 // order, over the lanes by a reduce-scatter butterfly and over the warps in
-// order, all in FP32, so a call gives the same bits every time; a row's
-// gradient is rounded once, from the FP32 product to bf16, the type of the rows
-// that the experts' GEMMs take their gradients in.
+// order, all in FP32, so a call gives the same bits every time; a token's
+// threads, turns and CTAs go by T, so in another batch its sums may be added in
+// another order.  A row's gradient is rounded once, from the FP32 product to
+// bf16, the type of the rows that the experts' GEMMs take their gradients in.
 #include <cooperative_groups.h>
 
 #include "mfr_maps.cuh"

@@ -70,9 +70,9 @@ inline bool fills_gpu(int64_t chunks, int sms) { return chunks > int64_t(2048) *
 // SM, more where rows outnumber them by far, 1 to 32.  The warps that do come
 // first in the grid, so that the zeros they write, row after row, are not the
 // call's tail (measured, dispatch of 16384 x 4096 to 8 slots, blocks of 128:
-// 209 us with them last, 192 first), and a small call has many of them (1024 x
-// 2048, blocks of 16: 12.7 us with 32 rows, 7.4 with 8, 6.7 with 4; 16384 x
-// 4096: 192, 193, 196 us).
+// 208 us with them last, 190 first), and a small call has many of them (1024 x
+// 2048, blocks of 16: 12.7 us with 32 rows, 7.3 with 8, 6.7 with 4 and with the
+// rule's 3; 16384 x 4096: 190 us with 32, 192 with 8, 194 with 4).
 inline int rows_per_warp(int64_t T, int64_t R, int sms) {
     const int64_t by_tokens = T / (2 * static_cast<int64_t>(sms)), by_rows = R / (64 * static_cast<int64_t>(sms));
     const int64_t rows = by_tokens > by_rows ? by_tokens : by_rows;

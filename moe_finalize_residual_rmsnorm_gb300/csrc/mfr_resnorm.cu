@@ -10,7 +10,8 @@
 // output, so bytes bound it (2 + 4 read, 4 + 1 (+ 2) written an element) and
 // one CTA per token is enough, as long as several are resident on an SM, each
 // in another phase of load, sum and store.  The launch bounds below hold that
-// up; CTAs are at most 512 threads of one to four chunks (8 columns).
+// up, at 4 and 20 bytes of spills a thread in the two one-chunk forms with a
+// scale per token; CTAs are at most 512 threads of one to four chunks (8 columns).
 // Measured on GB300, of the copy rate: 16384 x 4096 107 us (1.03), with bf16
 // output and MX scales 127 us (1.02); 8192 x 8192 109 us (1.00; 117 with 1024
 // threads of a chunk, 121 with two 512-thread CTAs an SM); 4096 x 16384 119
@@ -22,7 +23,8 @@
 //   few tokens of wide rows: a cluster of 4 or 8 CTAs per token, which
 //     exchange their sums through distributed shared memory (T = 1: H = 4096
 //     1.96 -> 1.71 us, 8192 2.98 -> 1.86, 16384 5.24 -> 2.03)
-//   H <= 512: a warp per token, no barrier
+//   H <= 512: a warp per token, no barrier; under 256 columns lanes are idle
+//     (of the copy rate at 256, 128 and 64 columns: 0.96, 0.74, 0.42)
 #include <cfloat>
 
 #include <cooperative_groups.h>

@@ -9,8 +9,10 @@
 // Bytes bound it: 4 + 4 + 2 read and 4 (+ 2) written an element.  Measured on
 // GB300, of the copy rate: 8192 x 8192 166 us (0.96; 224 us a token at a time
 // without the ring below), 16384 x 4096 160 us (0.99), 32768 x 2048 164 us
-// (0.96), 4096 x 16384 166 us (0.96), 32768 x 1024 85 us (0.93); 511 x 4104
-// 11.5 us, of which the second launch is 2.3.
+// (0.96), 4096 x 16384 164 us (0.97), 32768 x 1024 86 us (0.92); 511 x 4104
+// 11.5 us (0.43), of which the second launch is 2.3: its last tile holds 8 columns
+// but costs a stage and a wait like a full one, and 511 tokens are four turns
+// of 152 CTAs.
 //
 // Wide rows: persistent CTAs, whose GT consumer threads own the same columns
 // of every token, so that d_gamma is a running sum in registers, written once
@@ -211,7 +213,8 @@ __global__ void __launch_bounds__(GT + 32, 512 / GT) resnorm_grad_ring(const Res
 
 // ---- narrow rows ------------------------------------------------------------------------------
 // A warp per token, lane l owning the chunks (8 columns) l, l + 32, ...
-// Measured: 32768 x 512 46 us (0.85 of the copy rate), 32768 x 256 25 us (0.78);
+// Measured: 32768 x 512 46 us (0.86 of the copy rate), 32768 x 256 25 us (0.78),
+// 65536 x 256 46 us (0.86), 131072 x 128 51 us (0.78), 262144 x 64 85 us (0.47);
 // above, the ring is faster (32768 x 1024 85 us, 92 with a warp per token).
 constexpr int kNarrowWarps = 8;
 constexpr int kNarrowMaxH = 512;

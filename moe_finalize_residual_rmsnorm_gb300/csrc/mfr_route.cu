@@ -18,8 +18,12 @@
 // one launch; more are two launches over all SMs, the first of which counts
 // each CTA's pairs and the second sums the counts before its own and writes.
 // Measured on GB300: 64 pairs of 128 experts 1.9 us, 8192 pairs 3.6 us, 32768
-// pairs 5.7 us, 262144 pairs of 256 experts in 128-row blocks 8.1 us (28 us in
-// one cluster of 16 CTAs with warp matches).
+// pairs 5.7 us, 262144 pairs of 256 experts in 128-row blocks 8.2 us (28 us in
+// one cluster of 16 CTAs with warp matches), 524288 pairs of 128 experts 10.7 us,
+// of 1024 experts 16.2 us, 2 M pairs of 256 experts 32 us.  These large calls
+// count: every CTA sums the counts of all blocks (blocks^2 * E * 4 bytes out of
+// L2), and from 4096 pairs an SM up a CTA's rounds run one after another, with a
+// barrier around each scan and a thread per expert in it.
 #include <cooperative_groups.h>
 
 #include "moe_layer_ops.h"
