@@ -44,9 +44,12 @@ struct Relaxed {
 
 bool being_captured(cudaStream_t s) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &st) == cudaSuccess) return st != cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(s, &st);
+    if (e == cudaSuccess) return st != cudaStreamCaptureStatusNone;
     cudaGetLastError();
-    return true;      // the default stream, while a stream that it is in step with is being captured
+    // the default stream, while a stream that it is in step with is being
+    // captured; any other error is for the calls that follow to report
+    return e == cudaErrorStreamCaptureImplicit;
 }
 
 cudaError_t status_make(StatusWord& w) {
@@ -56,7 +59,10 @@ cudaError_t status_make(StatusWord& w) {
     if (e == cudaSuccess) e = cudaMalloc(&w.words, 2 * sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(w.words, 0, 2 * sizeof(int));
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);   // cleared before a run on any stream
-    if (e != cudaSuccess) status_free(w);
+    if (e != cudaSuccess) {
+        status_free(w);
+        cudaGetLastError();   // the caller reports it; nothing later does
+    }
     return e;
 }
 

@@ -190,3 +190,19 @@ def test_checks_and_readings_while_a_graph_is_captured(kind):
     torch.cuda.synchronize()
     assert any(o.any() for o in outs(call)) and not any(o.any() for o in outs(refused))
     assert call.plan.get_status() == 0
+
+
+@pytest.mark.parametrize("kind", CALLS)
+def test_a_plan_that_could_not_be_made_leaves_no_error_behind(kind):
+    """Plans are made before a capture; one that is tried inside fails and ends it.
+    Later calls of the library are as if it had not been tried."""
+    make, plan_of = CALLS[kind]
+    before, other = make(plan_of(), False), mfr.Plan(8, 256, 4)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with pytest.raises((mfr.MFRError, RuntimeError)):
+        with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+            plan_of()
+    other.wait_selftest(2_000_000, arrive=True)
+    before.run()
+    assert other.get_status() == 0 and before.plan.get_status() == 0
