@@ -32,13 +32,18 @@ __all__ = [
 # the operators around the finalize (layer_ops.py), loaded when first named
 _LAYER_OPS = ("RoutePlan", "DispatchPlan", "FinalizeGradPlan", "ResidualNormPlan", "ResidualNormGradPlan",
               "QUANT_NONE", "QUANT_TOKEN", "QUANT_GROUP128", "QUANT_MX32", "ROW_PADDING", "ROW_UNUSED")
-__all__ += _LAYER_OPS
+# further operators of a MoE layer's step (step_ops.py), likewise
+_STEP_OPS = ("MoeLayerPlan",)
+__all__ += _LAYER_OPS + _STEP_OPS
 
 
 def __getattr__(name: str):
     if name in _LAYER_OPS:
         from . import layer_ops
         return getattr(layer_ops, name)
+    if name in _STEP_OPS:
+        from . import step_ops
+        return getattr(step_ops, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
@@ -125,6 +130,8 @@ SIGNATURES = {
     "moe_residual_rmsnorm_grad_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, ctypes.POINTER(Options)]),
     "moe_residual_rmsnorm_grad_set_wait_limit": (_I, [_VP, _I64]),
     "moe_residual_rmsnorm_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP, _I64, _VP]),
+    "moe_small_layer_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, _I64, _I, _I, _I, ctypes.POINTER(Options)]),
+    "moe_small_layer_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP]),
 }
 
 _lib = None
