@@ -33,7 +33,7 @@ __all__ = [
 _LAYER_OPS = ("RoutePlan", "DispatchPlan", "FinalizeGradPlan", "ResidualNormPlan", "ResidualNormGradPlan",
               "QUANT_NONE", "QUANT_TOKEN", "QUANT_GROUP128", "QUANT_MX32", "ROW_PADDING", "ROW_UNUSED")
 # further operators of a MoE layer's step (step_ops.py), likewise
-_STEP_OPS = ("MoeLayerPlan",)
+_STEP_OPS = ("GatePlan", "MoeLayerPlan", "QkNormRopePlan", "GradClipPlan", "SCORE_SOFTMAX", "SCORE_SIGMOID")
 __all__ += _LAYER_OPS + _STEP_OPS
 
 
@@ -130,8 +130,17 @@ SIGNATURES = {
     "moe_residual_rmsnorm_grad_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, ctypes.POINTER(Options)]),
     "moe_residual_rmsnorm_grad_set_wait_limit": (_I, [_VP, _I64]),
     "moe_residual_rmsnorm_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP, _I64, _VP]),
+    "moe_gate_plan": (_I, [ctypes.POINTER(_VP), _I64, _I, _I, _I, _I, _F, _I, ctypes.POINTER(Options)]),
+    "moe_gate_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_gate_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP]),
     "moe_small_layer_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, _I64, _I, _I, _I, ctypes.POINTER(Options)]),
     "moe_small_layer_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP]),
+    "moe_qk_norm_rope_plan": (_I, [ctypes.POINTER(_VP), _I64, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(Options)]),
+    "moe_qk_norm_rope_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP, _VP]),
+    "moe_qk_norm_rope_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64,
+                                       _VP]),
+    "moe_grad_clip_plan": (_I, [ctypes.POINTER(_VP), _I, _VP, _VP, ctypes.POINTER(Options)]),
+    "moe_grad_clip_run": (_I, [_VP, _VP, _VP, _F, _F, _VP, _VP, _I64, _VP]),
 }
 
 _lib = None

@@ -1,5 +1,7 @@
 // Host side of the C ABI declared in include/moe_layer_ops.h: argument checks,
 // launch geometry, the plan's status word.
+#include <cstdlib>
+
 #include "mfr_op.h"
 
 namespace {
@@ -25,6 +27,7 @@ extern "C" {
 void moe_op_destroy(moe_op_t op) {
     if (!op) return;
     mfr::status_free(op->status);
+    std::free(op->host);
     delete op;
 }
 

@@ -17,7 +17,7 @@
 
 namespace mfr {
 
-enum Kind { kRoute = 1, kDispatch, kFinalizeGrad, kResNorm, kResNormGrad, kMoeLayer };
+enum Kind { kRoute = 1, kDispatch, kFinalizeGrad, kResNorm, kResNormGrad, kMoeLayer, kGate, kQkNorm, kGradClip };
 
 inline const char* kind_name(Kind kind) {
     switch (kind) {
@@ -26,7 +26,10 @@ inline const char* kind_name(Kind kind) {
         case kFinalizeGrad: return "moe_finalize_grad_plan";
         case kResNorm: return "moe_residual_rmsnorm_plan";
         case kResNormGrad: return "moe_residual_rmsnorm_grad_plan";
-        default: return "moe_small_layer_plan";
+        case kMoeLayer: return "moe_small_layer_plan";
+        case kGate: return "moe_gate_plan";
+        case kQkNorm: return "moe_qk_norm_rope_plan";
+        default: return "moe_grad_clip_plan";
     }
 }
 
@@ -52,6 +55,10 @@ struct moe_op_s {
     mfr_options opt;
     mfr::RouteLaunch route;
     mfr::MoeLayerShape layer;
+    mfr::GateShape gate;
+    mfr::QkShape qk;
+    mfr::ClipShape clip;
+    void* host;          // owned: the clip shape's arrays
     mfr::StatusWord status;
 };
 
@@ -194,7 +201,7 @@ inline int finish(moe_op_t op, cudaError_t e, void* stream) {
         if (rc != MFR_OK) return rc;
         if (st & MFR_STATUS_TIMEOUT)
             return MFR_FAIL(MFR_ERR_CUDA, "an on-chip wait timed out; the outputs are not valid");
-        if (st & MFR_STATUS_BAD_INDEX) return MFR_FAIL(MFR_ERR_BAD_INDEX, "an expert id or an index map entry was out of range");
+        if (st & MFR_STATUS_BAD_INDEX) return MFR_FAIL(MFR_ERR_BAD_INDEX, "an expert id, an index map entry or a position was out of range");
     }
     return MFR_OK;
 }

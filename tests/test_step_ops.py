@@ -31,7 +31,8 @@ def declared():
 
 def test_every_declared_symbol_is_exported_and_bound(lib):
     names = declared()
-    assert "moe_small_layer_run" in names
+    assert {"moe_gate_run", "moe_gate_grad_run", "moe_small_layer_run", "moe_qk_norm_rope_run", "moe_qk_norm_rope_grad_run",
+            "moe_grad_clip_run"} <= names
     assert not [n for n in names if not hasattr(lib, n)]
     assert names <= set(mfr.SIGNATURES)
 
@@ -43,7 +44,24 @@ def test_header_is_c99(tmp_path):
                    check=True)
 
 
+N = float("nan")
+TWO = (ctypes.c_int64 * 2)(5, 7), (ctypes.c_int * 2)(0, 1)
 PLANS = {
+    "moe_gate_plan": ((4, 64, 8, 0, 1, 1.0, 0), [
+        ((-1, 64, 8, 0, 1, 1.0, 0), INVALID), ((4, 64, 8, 2, 1, 1.0, 0), INVALID), ((4, 64, 8, -1, 1, 1.0, 0), INVALID),
+        ((4, 64, 8, 0, 2, 1.0, 0), INVALID), ((4, 64, 8, 0, 1, 1.0, 3), INVALID), ((4, 64, 8, 0, 1, 0.0, 0), INVALID),
+        ((4, 64, 8, 0, 1, N, 0), INVALID), ((4, 64, 0, 0, 1, 1.0, 0), SHAPE), ((4, 64, 17, 0, 1, 1.0, 0), SHAPE),
+        ((4, 7, 8, 0, 1, 1.0, 0), SHAPE), ((4, 1025, 8, 0, 1, 1.0, 0), SHAPE), (((1 << 26) + 1, 64, 8, 0, 1, 1.0, 0), SHAPE)]),
+    "moe_qk_norm_rope_plan": ((4, 8, 2, 64, 64, 0, 0, 100), [
+        ((-1, 8, 2, 64, 64, 0, 0, 100), INVALID), ((4, 8, 2, 64, 64, 2, 0, 100), INVALID), ((4, 8, 2, 64, 64, 0, 2, 100), INVALID),
+        ((4, 0, 2, 64, 64, 0, 0, 100), SHAPE), ((4, 8, 0, 64, 64, 0, 0, 100), SHAPE), ((4, 1025, 2, 64, 64, 0, 0, 100), SHAPE),
+        ((4, 8, 2, 60, 16, 0, 0, 100), SHAPE), ((4, 8, 2, 520, 64, 0, 0, 100), SHAPE), ((4, 8, 2, 0, 0, 0, 0, 100), SHAPE),
+        ((4, 8, 2, 64, 72, 0, 0, 100), SHAPE), ((4, 8, 2, 64, 80, 0, 0, 100), SHAPE), ((4, 8, 2, 64, 24, 0, 0, 100), SHAPE),
+        ((4, 8, 2, 64, -16, 0, 0, 100), SHAPE), ((4, 8, 2, 64, 64, 0, 0, 0), SHAPE)]),
+    "moe_grad_clip_plan": ((2, *TWO), [
+        ((-1, *TWO), INVALID), ((2, None, TWO[1]), INVALID), ((2, TWO[0], None), INVALID), ((65537, *TWO), SHAPE),
+        ((2, (ctypes.c_int64 * 2)(5, -1), TWO[1]), INVALID), ((2, (ctypes.c_int64 * 2)(1 << 40, 5), TWO[1]), SHAPE),
+        ((2, TWO[0], (ctypes.c_int * 2)(0, 3)), INVALID), ((2, TWO[0], (ctypes.c_int * 2)(-1, 0)), INVALID)]),
     "moe_small_layer_plan": ((4, 64, 64, 8, 2, 0), [
         ((-1, 64, 64, 8, 2, 0), INVALID), ((4, 64, 64, 8, 2, 2), INVALID), ((4, 64, 64, 8, 2, -1), INVALID),
         ((4, 60, 64, 8, 2, 0), SHAPE), ((4, 0, 64, 8, 2, 0), SHAPE), ((4, 16392, 64, 8, 2, 0), SHAPE),
@@ -83,6 +101,14 @@ def test_null_plans_are_refused(lib):
 def test_binding_refuses_other_types():
     with pytest.raises(ValueError, match="dtype"):
         mfr.MoeLayerPlan(4, 64, 64, 8, 2, dtype=torch.float16)
+    with pytest.raises(ValueError, match="dtype"):
+        mfr.GatePlan(4, 64, 8, dtype=torch.float16)
+    with pytest.raises(ValueError, match="dtype"):
+        mfr.QkNormRopePlan(4, 8, 2, 64, dtype=torch.float32, max_positions=10)
+    with pytest.raises(ValueError, match="dtypes"):
+        mfr.GradClipPlan([4, 5], [torch.float32, torch.float64])
+    with pytest.raises(ValueError, match="dtypes"):
+        mfr.GradClipPlan([4, 5], [torch.float32])
 
 
 # ---- the binding's checks of tensors: nothing below reaches the library --------------
@@ -115,7 +141,33 @@ def _layer(dtype):
     return _plan(mfr.MoeLayerPlan, T=T, H=H, I=I, E=E, k=k, dtype=dtype, _need=64), a, "run"
 
 
-CALLS = {"layer_bf16": lambda: _layer(B16), "layer_e4m3": lambda: _layer(FP8)}
+def _gate(grad):
+    T, E, k = 4, 64, 8
+    plan = _plan(mfr.GatePlan, T=T, E=E, k=k, score=mfr.SCORE_SIGMOID, dtype=B16)
+    if grad:
+        return plan, dict(d_topk_weights=_z(T, k), logits=_z(T, E, dtype=B16), expert_ids=_z(T, k, dtype=I32),
+                          d_logits=_z(T, E, dtype=B16)), "run_grad"
+    return plan, dict(logits=_z(T, E, dtype=B16), expert_ids=_z(T, k, dtype=I32), topk_weights=_z(T, k), bias=_z(E)), "run"
+
+
+def _qk(grad):
+    T, hq, hk, D, most = 4, 6, 2, 64, 10
+    plan = _plan(mfr.QkNormRopePlan, T=T, heads_q=hq, heads_k=hk, D=D, dtype=F16, rotary_dim=32, max_positions=most, _need=64)
+
+    def q():
+        return _z(T, hq, D, dtype=F16)
+
+    def k():
+        return _z(T, hk, D, dtype=F16)
+    shared = dict(gamma_q=_z(D, dtype=F16), gamma_k=_z(D, dtype=F16), eps=1e-6, cos_sin=_z(most, 32), positions=_z(T, dtype=I32))
+    if grad:
+        return plan, dict(d_q_out=q(), d_k_out=k(), q=q(), k=k(), **shared, d_q=q(), d_k=k(), d_gamma_q=_z(D), d_gamma_k=_z(D),
+                          workspace=_z(64, dtype=torch.uint8)), "run_grad"
+    return plan, dict(q=q(), k=k(), **shared, q_out=q(), k_out=k()), "run"
+
+
+CALLS = {"gate": lambda: _gate(False), "gate_grad": lambda: _gate(True), "qk": lambda: _qk(False), "qk_grad": lambda: _qk(True),
+         "layer_bf16": lambda: _layer(B16), "layer_e4m3": lambda: _layer(FP8)}
 
 
 @pytest.mark.parametrize("op", list(CALLS))
@@ -144,3 +196,60 @@ def test_a_layer_for_bf16_takes_no_scales():
     plan, args, _ = _layer(B16)
     with pytest.raises(ValueError, match="bf16"):
         plan.run(**args, w2_sf=_z(8, 2, 1))
+
+
+def test_a_bias_needs_sigmoid_scores():
+    plan, args, _ = _gate(False)
+    plan.score = mfr.SCORE_SOFTMAX
+    with pytest.raises(ValueError, match="bias"):
+        plan.run(**args)
+
+
+# ---- the references ----------------------------------------------------------------------
+
+def test_reference_gradients_against_differentiation():
+    g = torch.Generator().manual_seed(0)
+    logits = torch.randn((3, 9), generator=g, dtype=torch.float64)
+    d_w = torch.randn((3, 4), generator=g, dtype=torch.float64)
+    for sigmoid in (False, True):
+        for renorm in (False, True):
+            ids, w, _ = ref.gate(logits, 4, sigmoid, renorm, 1.5)
+            l = logits.clone().requires_grad_(True)
+            p = torch.sigmoid(l) if sigmoid else torch.softmax(l, 1)
+            q = torch.gather(p, 1, ids)
+            q = 1.5 * (q / q.sum(1, keepdim=True) if renorm else q)
+            assert torch.allclose(q.detach(), w, atol=1e-14)
+            (q * d_w).sum().backward()
+            assert torch.allclose(ref.gate_grad(d_w, logits, ids, sigmoid, renorm, 1.5)[0], l.grad, atol=1e-14)
+    table = torch.randn((7, 16), generator=g)
+    pos = torch.tensor([0, 6, 3])
+    for interleaved in (False, True):
+        x = torch.randn((3, 2, 24), generator=g, dtype=torch.float64, requires_grad=True)
+        gamma = torch.randn(24, generator=g, dtype=torch.float64, requires_grad=True)
+        d = torch.randn((3, 2, 24), generator=g, dtype=torch.float64)
+        n = x / torch.sqrt(x.pow(2).mean(-1, keepdim=True) + float(torch.tensor(1e-3))) * gamma
+        r = n[..., :16].unflatten(-1, (8, 2)) if interleaved else n[..., :16].unflatten(-1, (2, 8)).transpose(-1, -2)
+        c, s = (table[pos].double()[:, None, :8], table[pos].double()[:, None, 8:])
+        z = torch.stack([r[..., 0] * c - r[..., 1] * s, r[..., 0] * s + r[..., 1] * c], -1)
+        z = z.flatten(-2) if interleaved else z.transpose(-1, -2).flatten(-2)
+        out = torch.cat([z, n[..., 16:]], -1)
+        assert torch.allclose(out, ref.qk_norm(x, gamma, 1e-3, table, pos, 16, interleaved)[0], atol=1e-12)
+        (out * d).sum().backward()
+        d_x, _, d_g, _ = ref.qk_norm_grad(d, x, gamma, 1e-3, table, pos, 16, interleaved)
+        assert torch.allclose(d_x, x.grad, atol=1e-12) and torch.allclose(d_g, gamma.grad, atol=1e-12)
+
+
+def test_reference_layer_is_the_formula():
+    g = torch.Generator().manual_seed(0)
+    T, H, I, E, k = 3, 16, 8, 4, 2
+    x, w13, w2 = (torch.randn(s, generator=g, dtype=torch.float64) for s in ((T, H), (E, 2 * I, H), (E, H, I)))
+    ids, w = torch.tensor([[0, 3], [-1, 2], [1, 1]]), torch.rand((T, k), generator=g, dtype=torch.float64)
+    out, _ = ref.moe_layer(x, ids, w, w13, w2)
+    for t in range(T):
+        want = torch.zeros(H, dtype=torch.float64)
+        for j in range(k):
+            e = int(ids[t, j])
+            if e >= 0:
+                both = w13[e] @ x[t]
+                want += w[t, j] * (w2[e] @ (torch.nn.functional.silu(both[:I]) * both[I:]))
+        assert torch.allclose(out[t], want, atol=1e-12)
