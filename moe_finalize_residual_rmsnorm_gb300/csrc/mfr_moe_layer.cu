@@ -1,4 +1,4 @@
-// A whole MoE layer for a few tokens, in two launches:
+// A whole MoE layer for a few tokens:
 //
 //   h[t, j] = silu(G_e x[t]) * (U_e x[t]),   e = expert of token t's slot j
 //   out[t]  = sum_j w[t, j] * (D_e h[t, j])
@@ -10,21 +10,31 @@
 // Every chosen expert's weights are read once, and up to about a hundred pairs an
 // expert those bytes bound the layer, so the weights are the streamed operand:
 // they are the 128 rows of the product's A, and the expert's pairs its 16 .. 128
-// columns (B).  A warp keeps a ring of stages of 128 bytes of K filled by
-// tensor-map copies (two boxes of 128 weight rows, the pairs' rows gathered four
-// at a time), one thread issues tcgen05 products into tensor memory, and eight
-// warps finish one tile while the next one is multiplied.
+// columns (B).  One warp keeps a ring of stages of 32 KB of weights filled by
+// tensor-map copies, one gathers the pairs' rows next to them, four a copy, one
+// thread issues tcgen05 products into tensor memory, and eight warps finish one
+// unit while the next one is multiplied.
 //
 // Each CTA sorts the pairs by expert itself (at most 4096, from L2), so that no
-// launch before it is needed; work is (expert, chunk of its pairs) x (tile of
-// weight rows), in turns over persistent CTAs.
-//   first launch:  a tile is 128 rows of G and the same 128 of U, so that a thread
-//                  holds both halves of an element of h
-//   second launch: a tile is 256 rows of D; the products go to y[pair] in FP32, and
-//                  the CTA that finishes the last expert of a tile adds the pairs of
-//                  each token in slot order: no atomics on values, the same bits in
-//                  every call
+// launch before it is needed.  A unit is (tile of weight rows, chunk of an expert's
+// pairs) over all of K, in turns over persistent CTAs; chunks of one expert are
+// neighbours, so that its weights come from DRAM once.
+//   first launch:  64 rows of G and the same 64 of U (E4M3: 128 and 128, a group of
+//                  h's scales), h to the workspace
+//   second launch: 256 rows of D, products to y[pair] in FP32; it loads weights
+//                  before it waits for the first launch
+//   then the pairs of every token are added in slot order, by a small third launch:
+//                  no atomics, the same bits in every call
+// Not taken: dividing the steps along K evenly over the CTAs, with partial sums put
+// together by the last to arrive (every piece's end is a fence, an atomic and a round
+// trip: one token 54 us that way and 42 this, 37 tokens 85 and 51, 128 in E4M3 378 and
+// 289); adding the pairs in the second launch by the last CTA of a tile (128 tokens: 50
+// us at its end); two CTAs an SM, so that the launches overlap (half the ring each: one
+// token 52 us); fetching w2 to L2 at the first launch's end (no difference).
 //
+// bf16: h is kept as the sum of two bf16 values (16 bits of it), two products of the
+// same weights, which cost nothing where bytes bound it; rounded once it alone would
+// put the output 1.4 times as far from the exact one as its own rounding does.
 // E4M3: products of 128 columns of K are one accumulation in tensor memory, which
 // the finishing warps scale and add in FP32 registers.
 #include <cfloat>
@@ -40,25 +50,50 @@ namespace {
 
 constexpr int kWarps = kMoeThreads / 32;
 constexpr int kFinishWarps = 8;
-constexpr int kTileBytes = 2 * kMoeRows * 128;     // weights of a stage
+constexpr int kPanel = kMoeRows * 128;             // 128 weight rows of 128 bytes of K; a stage has two
 constexpr int kRingStages = 6;
 constexpr float kAmaxFloor = 0x1p-100f;
 
-template <int NB>
-constexpr int stage_bytes() { return kTileBytes + NB * 128; }
+// Rows of pairs in a stage.  bf16: two panels, of the two steps of K in a stage of the
+// first launch, or of the two parts of h in the second.
+template <bool FP8, int NB>
+constexpr int stage_bytes() { return 2 * kPanel + NB * 128 * (FP8 ? 1 : 2); }
+
+// Accumulators of a unit: gate and up rows in one (bf16), or two of 128 rows.
+template <bool FP8, bool DOWN>
+constexpr int accumulators() { return FP8 || DOWN ? 2 : 1; }
+
+// The two parts of h are columns of one product, side by side, where tensor memory
+// holds that twice; else two products.
+template <bool FP8, bool DOWN, int NB>
+constexpr bool stacked() { return DOWN && !FP8 && NB <= 64; }
+
+// Columns of an accumulator, and of two units' accumulators.
+template <bool FP8, bool DOWN, int NB>
+constexpr int columns() { return stacked<FP8, DOWN, NB>() ? 2 * NB : NB; }
+template <bool FP8, bool DOWN, int NB>
+constexpr uint32_t tmem_columns() {
+    constexpr int n = 2 * accumulators<FP8, DOWN>() * columns<FP8, DOWN, NB>();
+    return n < 32 ? 32 : n;
+}
 
 // Behind the ring.
+template <int NB>
 struct Shared {
     uint64_t full[kRingStages], empty[kRingStages];
     uint64_t done[2], taken[2];       // an accumulator is complete; its values are in registers
     uint64_t drain;
     uint32_t tmem;
     int dead;                         // a wait ran out: every role leaves
-    int last;                         // this CTA finished the last piece of a tile
-    int entries;
+    int issued[2];                    // stages that the loading warps have begun
     int scan[kWarps];
-    float sx[kFinishWarps][64];       // E4M3: scales of a warp's columns
-    uint32_t top[2][4][64];           // E4M3: largest magnitudes, by half, warp and column
+    union {
+        struct {                      // E4M3
+            float sx[kFinishWarps][NB / 2];   // scales of a warp's columns
+            uint32_t top[2][4][8];            // largest magnitudes, by side, warp and column
+        };
+        float up[2][8][64];           // bf16: the up rows' products, by side and column
+    };
 };
 
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -76,9 +111,9 @@ __device__ __forceinline__ bool finishers_well(bool ok) {
 }
 
 // A role's wait for another.  It gives up after kWaitCycles, or when another has given up.
-__device__ bool role_wait(Shared* s, int* status, uint32_t bar, uint32_t parity) {
+__device__ bool role_wait(int* dead_word, int* status, uint32_t bar, uint32_t parity) {
     if (mbar_test_parity(bar, parity)) return true;
-    volatile int* dead = &s->dead;
+    volatile int* dead = dead_word;
     const long long t0 = clock64();
     while (!mbar_test_parity(bar, parity)) {
         if (*dead) return false;
@@ -91,7 +126,7 @@ __device__ bool role_wait(Shared* s, int* status, uint32_t bar, uint32_t parity)
     return true;
 }
 
-// (expert, first place in the sorted list, pairs) of a chunk of pairs.
+// A chunk of an expert's pairs: (expert, first place in the sorted list, pairs).
 struct Entry {
     int expert, start, n;
 };
@@ -106,19 +141,27 @@ __device__ __forceinline__ bool valid_expert(int id, int E) { return static_cast
 
 // Stable counting sort of the pairs by expert, the same in every CTA: `list` gets
 // the pairs, `entries` the chunks of at most NB of them; returns their number.
-// `hist`: [kWarps + 1][E].  All threads call it.
+// `hist`: [kWarps + 1][E], and the ids behind it.  All threads call it.
 template <int NB>
-__device__ int sort_pairs(const MoeParams& p, Shared* s, uint16_t* list, uint32_t* entries, int* hist, bool report) {
+__device__ int sort_pairs(const MoeParams& p, Shared<NB>* s, uint16_t* list, uint32_t* entries, int* hist, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.T * p.k, E = p.E;
     const int seg = ((P + kWarps - 1) / kWarps + 31) & ~31, first = warp * seg, last = min(P, first + seg);
-    for (int i = tid; i < kWarps * E; i += kMoeThreads) hist[i] = 0;
+    const int warps = (P + seg - 1) / seg;            // that have pairs
+    int* ids = hist + (kWarps + 1) * E;
+    for (int i = tid; i < P; i += kMoeThreads) ids[i] = __ldg(p.ids + i);
+    for (int i = tid; i < warps * E; i += kMoeThreads) hist[i] = 0;
     __syncthreads();
     bool bad = false;
-    for (int i = first + lane; i < last; i += 32) {
-        const int id = p.ids[i];
-        if (valid_expert(id, E)) atomicAdd(&hist[warp * E + id], 1);
-        else bad |= !(p.sentinel && id < 0);
+    for (int i0 = first; i0 < last; i0 += 32) {
+        const int i = i0 + lane, e = i < last ? ids[i] : -1;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        if (valid_expert(e, E)) {
+            if (lane == __ffs(same) - 1) hist[warp * E + e] += __popc(same);
+        } else {
+            bad |= i < last && !(p.sentinel && e < 0);
+        }
+        __syncwarp();
     }
     if (report && bad) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
     __syncthreads();
@@ -127,7 +170,7 @@ __device__ int sort_pairs(const MoeParams& p, Shared* s, uint16_t* list, uint32_
     uint32_t sum = 0;
     for (int e = e0; e < e1; ++e) {
         int n = 0;
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < warps; ++w) {
             const int c = hist[w * E + e];
             hist[w * E + e] = n;
             n += c;
@@ -143,51 +186,60 @@ __device__ int sort_pairs(const MoeParams& p, Shared* s, uint16_t* list, uint32_
     }
     if (lane == 31) s->scan[warp] = static_cast<int>(incl);
     __syncthreads();
-    uint32_t base = incl - sum;
-    for (int w = 0; w < warp; ++w) base += static_cast<uint32_t>(s->scan[w]);
+    uint32_t base = incl - sum, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base += static_cast<uint32_t>(s->scan[w]);
+        all += static_cast<uint32_t>(s->scan[w]);
+    }
     int at = static_cast<int>(base & 0xFFFFu), chunk = static_cast<int>(base >> 16);
     for (int e = e0; e < e1; ++e) {
-        for (int w = 0; w < kWarps; ++w) hist[w * E + e] += at;
         const int n = hist[kWarps * E + e];
+        if (n == 0) continue;
+        for (int w = 0; w < warps; ++w) hist[w * E + e] += at;
         for (int c = 0; c < n; c += NB) entries[chunk++] = pack_entry(e, at + c, min(NB, n - c));
         at += n;
     }
-    if (tid == kMoeThreads - 1) s->entries = chunk;
     __syncthreads();
     for (int i0 = first; i0 < last; i0 += 32) {
-        const int i = i0 + lane, id = i < last ? p.ids[i] : -1;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-        const bool ok = valid_expert(id, E);
-        if (ok) list[hist[warp * E + id] + __popc(same & ((1u << lane) - 1))] = static_cast<uint16_t>(i);
+        const int i = i0 + lane, e = i < last ? ids[i] : -1;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        const bool ok = valid_expert(e, E);
+        if (ok) list[hist[warp * E + e] + __popc(same & ((1u << lane) - 1))] = static_cast<uint16_t>(i);
         __syncwarp();
-        if (ok && lane == __ffs(same) - 1) hist[warp * E + id] += __popc(same);
+        if (ok && lane == __ffs(same) - 1) hist[warp * E + e] += __popc(same);
         __syncwarp();
     }
-    __syncthreads();
-    return s->entries;
+    return static_cast<int>(all >> 16);               // the caller's barrier ends it
 }
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
-// One launch of the layer.  DOWN: the second one.
+// One launch of products.  DOWN: the second one.
 template <bool FP8, bool DOWN, int NB>
 __global__ void __launch_bounds__(kMoeThreads, 1)
 moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights, const __grid_constant__ CUtensorMap rows) {
-    constexpr int KE = FP8 ? 128 : 64;               // elements of K in a stage
+    constexpr bool GATES = !FP8 && !DOWN;            // gate and up rows in one accumulator, two steps of K a stage
+    constexpr int KE = FP8 ? 128 : 64;               // elements of 128 bytes of K
+    constexpr int KS = GATES ? 2 * KE : KE;          // of a stage
     constexpr int HALF = NB / 2;                     // columns that one finishing warp holds at most
+    constexpr bool STACKED = stacked<FP8, DOWN, NB>();
+    constexpr int COLS = columns<FP8, DOWN, NB>();   // of an accumulator
+    constexpr int ACC = accumulators<FP8, DOWN>() * COLS;
+    constexpr int STAGE = stage_bytes<FP8, NB>();
+    constexpr int ROWS = GATES ? kMoeRows / 2 : DOWN ? 2 * kMoeRows : kMoeRows;     // of a tile
     extern __shared__ unsigned char raw[];
     const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
-    unsigned char* behind = raw + (ring - smem_addr(raw)) + p.stages * stage_bytes<NB>();
-    Shared* s = reinterpret_cast<Shared*>(behind);
-    uint32_t* entries = reinterpret_cast<uint32_t*>(behind + sizeof(Shared));
+    const int S = p.stages;
+    unsigned char* behind = raw + (ring - smem_addr(raw)) + S * STAGE;
+    Shared<NB>* s = reinterpret_cast<Shared<NB>*>(behind);
+    uint32_t* entries = reinterpret_cast<uint32_t*>(behind + sizeof(Shared<NB>));
     uint16_t* list = reinterpret_cast<uint16_t*>(entries + p.entries);
     int* hist = reinterpret_cast<int*>(raw + (ring - smem_addr(raw)));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int S = p.stages;
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(smem_addr(&s->full[i]), 1);
+            mbar_init(smem_addr(&s->full[i]), 2);
             mbar_init(smem_addr(&s->empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -195,14 +247,19 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             mbar_init(smem_addr(&s->taken[i]), kFinishWarps);
         }
         mbar_init(smem_addr(&s->drain), 1);
-        s->dead = 0;
+        s->dead = s->issued[0] = s->issued[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&weights);
         prefetch_map(&rows);
     }
-    if (warp == 1) tmem_alloc(smem_addr(&s->tmem), 4 * NB < 32 ? 32 : 4 * NB);
-    pdl_wait();
-    pdl_launch_dependents();
+    if (warp == 1) tmem_alloc(smem_addr(&s->tmem), tmem_columns<FP8, DOWN, NB>());
+    // The second launch starts when every CTA of the first has waited for what lay
+    // before it, so only what the first one writes is still to come: the ids, the
+    // weights and their scales are there.
+    if (!DOWN) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     const int M = sort_pairs<NB>(p, s, list, entries, hist, !DOWN && blockIdx.x == 0);
     proxy_fence();                    // the ring's memory held the counts
     tcgen05_fence_before();
@@ -210,255 +267,361 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
     tcgen05_fence_after();
     const uint32_t tmem = s->tmem;
 
-    const int H = p.H, I = p.I, K = DOWN ? I : H;
-    const int KB = (K + KE - 1) / KE;
-    const int tiles = DOWN ? (H + 2 * kMoeRows - 1) / (2 * kMoeRows) : (I + kMoeRows - 1) / kMoeRows;
-    const int units = M * tiles;
-    const int HB = (H + 127) / 128, IB = I / 128;    // scale blocks
-    if (!DOWN && blockIdx.x == 0)
-        for (int i = tid; i < (H + 2 * kMoeRows - 1) / (2 * kMoeRows); i += kMoeThreads) p.counters[i] = 0;
-    int issued = 0;                   // stages that the loading warp has begun
+    const int H = p.H, I = p.I, K = DOWN ? I : H, P = p.T * p.k;
+    const int KB = (K + KS - 1) / KS;                // stages of a unit
+    const int units = M * (((DOWN ? H : I) + ROWS - 1) / ROWS);
+    const int G = gridDim.x;
 
-    if (warp == 0) {
+    if (warp == 0) {                  // the weights
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const Entry en = unpack_entry(entries[u / tiles]);
-            const int tile = u % tiles;
-            const int c1a = DOWN ? tile * 2 * kMoeRows : tile * kMoeRows;
-            const int c1b = DOWN ? c1a + kMoeRows : I + c1a;
-            const int gathers = (en.n + 3) >> 2;
-            int r[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pair = list[en.start + min(4 * lane + i, en.n - 1)];
-                r[i] = DOWN ? pair : pair / p.k;
-            }
-            for (int kb = 0; kb < KB; ++kb, ++issued) {
-                const int st = issued % S, turn = issued / S;
-                if (turn > 0) ok = role_wait(s, p.status, smem_addr(&s->empty[st]), (turn - 1) & 1);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+        int i = 0, st = 0, parity = 1;
+        for (int u = blockIdx.x; ok && u < units; u += G) {
+            const int tile = u / M, expert = unpack_entry(entries[u - tile * M]).expert;
+            const int c1a = tile * ROWS, c1b = DOWN ? c1a + kMoeRows : I + c1a;
+            for (int kb = 0; kb < KB; ++kb, ++i) {
+                if (i >= S) ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p.status, smem_addr(&s->empty[st]), parity));
                 if (!ok) break;
-                const uint32_t bar = smem_addr(&s->full[st]), a = ring + st * stage_bytes<NB>();
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, kTileBytes + gathers * 512);
-                    map_load3(a, &weights, kb * KE, c1a, en.expert, bar);
-                    map_load3(a + kMoeRows * 128, &weights, kb * KE, c1b, en.expert, bar);
+                const uint32_t bar = smem_addr(&s->full[st]), a = ring + st * STAGE;
+                if (elect_lane()) {
+                    mbar_arrive_expect_tx(bar, 2 * kPanel);
+                    map_load3(a, &weights, kb * KS, c1a, expert, bar);
+                    if constexpr (GATES) {           // 64 rows a box; a box behind the end of K reads zeros
+                        map_load3(a + kPanel / 2, &weights, kb * KS, c1b, expert, bar);
+                        map_load3(a + kPanel, &weights, kb * KS + KE, c1a, expert, bar);
+                        map_load3(a + kPanel + kPanel / 2, &weights, kb * KS + KE, c1b, expert, bar);
+                    } else {
+                        map_load3(a + kPanel, &weights, kb * KS, c1b, expert, bar);
+                    }
                 }
                 __syncwarp();
-                if (lane < gathers)
-                    map_gather4(a + kTileBytes + lane * 512, &rows, kb * KE, make_int4(r[0], r[1], r[2], r[3]), bar);
+                if (++st == S) {
+                    st = 0;
+                    parity ^= 1;
+                }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            int stage = 0, uses = 0;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const Entry en = unpack_entry(entries[u / tiles]);
-                const uint32_t desc = mma_desc(FP8, (en.n + 15) & ~15);
-                for (int kb = 0; kb < KB; ++kb, ++stage) {
-                    const int st = stage % S;
-                    if (FP8 || kb == 0) {
-                        if (uses > 1) ok = role_wait(s, p.status, smem_addr(&s->taken[uses & 1]), ((uses >> 1) - 1) & 1);
-                        if (!ok) break;
-                        tcgen05_fence_after();
-                    }
-                    ok = role_wait(s, p.status, smem_addr(&s->full[st]), (stage / S) & 1);
-                    if (!ok) break;
-                    tcgen05_fence_after();
-                    const uint32_t a = ring + st * stage_bytes<NB>(), d = tmem + (uses & 1) * 2 * NB;
-                    const uint64_t da = operand_desc(a), db = operand_desc(a + kTileBytes);
+        if (lane == 0) s->issued[0] = i;
+    } else if (warp == kWarps - 1) {  // the pairs' rows
+        if (DOWN) {
+            pdl_wait();
+            pdl_launch_dependents();
+            proxy_fence();
+        }
+        bool ok = true;
+        int i = 0, st = 0, parity = 1;
+        for (int u = blockIdx.x; ok && u < units; u += G) {
+            const Entry en = unpack_entry(entries[u % M]);
+            int v[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int pair = list[en.start + min(4 * lane + n, en.n - 1)];
+                v[n] = DOWN ? pair : pair / p.k;
+            }
+            const int4 r = make_int4(v[0], v[1], v[2], v[3]);
+            const int4 r2 = DOWN ? make_int4(v[0] + P, v[1] + P, v[2] + P, v[3] + P) : r;     // lower parts
+            const int gathers = (en.n + 3) >> 2;
+            const uint32_t second = ring + 2 * kPanel + (STACKED ? (en.n + 15) & ~15 : NB) * 128;
+            for (int kb = 0; kb < KB; ++kb, ++i) {
+                if (i >= S) ok = role_wait(&s->dead, p.status, smem_addr(&s->empty[st]), parity);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t bar = smem_addr(&s->full[st]), b = ring + st * STAGE + 2 * kPanel;
+                if (lane == 0) mbar_arrive_expect_tx(bar, gathers * (FP8 ? 512 : 1024));
+                __syncwarp();
+                if (lane < gathers) {
+                    map_gather4(b + lane * 512, &rows, kb * KS, r, bar);
+                    if constexpr (!FP8) map_gather4(second + st * STAGE + lane * 512, &rows, kb * KS + (GATES ? KE : 0), r2, bar);
+                }
+                if (++st == S) {
+                    st = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+        if (lane == 0) s->issued[1] = i;
+    } else if (warp == 1) {           // the products
+        bool ok = true;
+        int st = 0, parity = 0, uses = 0;
+        for (int u = blockIdx.x; ok && u < units; u += G) {
+            const int n = (unpack_entry(entries[u % M]).n + 15) & ~15;
+            const uint32_t desc = mma_desc(FP8, STACKED ? 2 * n : n);
+            for (int kb = 0; kb < KB; ++kb) {
+                if ((FP8 || kb == 0) && uses > 1)
+                    ok = role_wait(&s->dead, p.status, smem_addr(&s->taken[uses & 1]), ((uses >> 1) - 1) & 1);
+                ok = ok && role_wait(&s->dead, p.status, smem_addr(&s->full[st]), parity);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tcgen05_fence_after();
+                const bool last = FP8 || kb == KB - 1;
+                if (elect_lane()) {
+                    const uint32_t a = ring + st * STAGE, d = tmem + (uses & 1) * ACC;
+                    const uint64_t da = operand_desc(a), db = operand_desc(a + 2 * kPanel);
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_issue<FP8>(d + half * NB, da + half * (kMoeRows * 128 >> 4) + i * 2, db + i * 2, desc,
-                                           i > 0 || (!FP8 && kb > 0));
+                        for (int i = 0; i < 4; ++i) {
+                            const uint64_t from = da + half * (kPanel >> 4) + i * 2;
+                            const bool more = i > 0 || (!FP8 && kb > 0) || (GATES && half > 0);
+                            mma_issue<FP8>(d + (GATES ? 0 : half * COLS), from, db + (GATES ? half * (NB * 128 >> 4) : 0) + i * 2, desc, more);
+                            if constexpr (DOWN && !FP8 && !STACKED)
+                                mma_issue<FP8>(d + half * COLS, from, db + (NB * 128 >> 4) + i * 2, desc, true);
+                        }
                     mma_commit(smem_addr(&s->empty[st]));
-                    if (FP8 || kb == KB - 1) {
-                        mma_commit(smem_addr(&s->done[uses & 1]));
-                        ++uses;
-                    }
+                    if (last) mma_commit(smem_addr(&s->done[uses & 1]));
+                }
+                __syncwarp();
+                if (last) ++uses;
+                if (++st == S) {
+                    st = 0;
+                    parity ^= 1;
                 }
             }
-            if (!ok) {                // products may be in flight
-                mma_commit(smem_addr(&s->drain));
-                mbar_wait(smem_addr(&s->drain), 0);
-            }
         }
-    } else {
+        if (!ok) {                    // products may be in flight
+            if (elect_lane()) mma_commit(smem_addr(&s->drain));
+            __syncwarp();
+            mbar_wait(smem_addr(&s->drain), 0);
+        }
+    } else {                          // the ends of the units
+        if (DOWN) pdl_wait();
         const int quad = warp & 3, side = (warp - 2) >> 2, row = quad * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + side * 8;
         int uses = 0;
         bool ok = true;
-        // column j of this warp is column (j / 8) * 16 + side * 8 + j % 8 of the accumulator
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const Entry en = unpack_entry(entries[u / tiles]);
-            const int tile = u % tiles;
-            float d0[HALF], d1[HALF];
+        for (int u = blockIdx.x; ok && u < units; u += G) {
+            const int tile = u / M;
+            const Entry en = unpack_entry(entries[u - tile * M]);
+            const uint16_t* pairs = list + en.start;
+            // this warp's columns: eight from side * 8 on, from side * 8 + 16 on, ...
+            const int groups = (en.n - side * 8 + 15) >> 4;
+            // Columns c0 .. c0 + 7 of the second launch: products to y.
+            auto to_y = [&](int c0, const float (&a)[8], const float (&b)[8]) {
+                const int h0 = tile * ROWS + row, h1 = h0 + kMoeRows;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (c0 + j >= en.n) break;
+                    float* y = p.y + static_cast<int64_t>(pairs[c0 + j]) * H;
+                    if (h0 < H) y[h0] = a[j];
+                    if (h1 < H) y[h1] = b[j];
+                }
+            };
             if constexpr (FP8) {
+                const int HB = (H + 127) / 128, IB = I / 128;        // scale blocks
+                float d0[NB / 16][8], d1[NB / 16][8];
                 float* sx = s->sx[warp - 2];
-                int from[2];          // this lane's columns' rows of scales
+                const float* from[2]; // this lane's columns' rows of scales
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int j = lane + 32 * i, c = (j >> 3) * 16 + side * 8 + (j & 7);
-                    const int pair = list[en.start + min(c, en.n - 1)];
-                    from[i] = DOWN ? pair : pair / p.k;
+                    const int j = (lane + 32 * i) & (HALF - 1);
+                    const int pair = pairs[min((j >> 3) * 16 + side * 8 + (j & 7), en.n - 1)];
+                    from[i] = DOWN ? p.act_sf + static_cast<int64_t>(pair) * KB : p.x_sf + static_cast<int64_t>(pair / p.k) * KB;
                 }
-                const float* scales = DOWN ? p.act_sf : p.x_sf;
                 const float* w0 = DOWN ? p.w2_sf + (static_cast<int64_t>(en.expert) * HB + 2 * tile) * IB
                                        : p.w13_sf + (static_cast<int64_t>(en.expert) * 2 * IB + tile) * HB;
                 const float* w1 = DOWN ? w0 + (2 * tile + 1 < HB ? IB : 0) : w0 + static_cast<int64_t>(IB) * HB;
 #pragma unroll
-                for (int j = 0; j < HALF; ++j) d0[j] = d1[j] = 0.f;
-                for (int kb = 0; kb < KB; ++kb, ++uses) {
-                    const float sw0 = w0[kb], sw1 = w1[kb];
-                    __syncwarp();
+                for (int q = 0; q < NB / 16; ++q)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (lane + 32 * i < HALF) sx[lane + 32 * i] = scales[static_cast<int64_t>(from[i]) * KB + kb];
-                    __syncwarp();
-                    ok = role_wait(s, p.status, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    tcgen05_fence_after();
-                    const uint32_t at = lanes + (uses & 1) * 2 * NB;
+                    for (int i = 0; i < 8; ++i) d0[q][i] = d1[q][i] = 0.f;
+                // the scales of four steps, and the next four on their way
+                constexpr int AHEAD = 4;
+                float sw0[AHEAD], sw1[AHEAD], f0[AHEAD], f1[AHEAD], nw0[AHEAD], nw1[AHEAD], n0[AHEAD], n1[AHEAD];
+                auto load_scales = [&](int kb) {
 #pragma unroll
-                    for (int q = 0; q < NB / 16; ++q) {
-                        if (q * 16 + side * 8 >= en.n) break;
-                        uint32_t a[8], b[8];
-                        tmem_load8(at + q * 16, a);
-                        tmem_load8(at + NB + q * 16, b);
-                        tmem_wait_load(a, b);
+                    for (int i = 0; i < AHEAD; ++i) {
+                        const int at = min(kb + i, KB - 1);
+                        nw0[i] = __ldg(w0 + at);
+                        nw1[i] = __ldg(w1 + at);
+                        n0[i] = __ldcg(from[0] + at);
+                        n1[i] = HALF > 32 ? __ldcg(from[1] + at) : 0.f;
+                    }
+                };
+                load_scales(0);
+                for (int kb0 = 0; ok && kb0 < KB; kb0 += AHEAD) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float f = sx[q * 8 + i];
-                            d0[q * 8 + i] = fmaf(__uint_as_float(a[i]), f * sw0, d0[q * 8 + i]);
-                            d1[q * 8 + i] = fmaf(__uint_as_float(b[i]), f * sw1, d1[q * 8 + i]);
+                    for (int i = 0; i < AHEAD; ++i) {
+                        sw0[i] = nw0[i];
+                        sw1[i] = nw1[i];
+                        f0[i] = n0[i];
+                        f1[i] = n1[i];
+                    }
+                    load_scales(kb0 + AHEAD);
+#pragma unroll
+                    for (int step = 0; step < AHEAD; ++step) {
+                        if (kb0 + step >= KB) break;
+                        __syncwarp();
+                        if (lane < HALF) sx[lane] = f0[step];
+                        if (HALF > 32) sx[lane + 32] = f1[step];
+                        __syncwarp();
+                        const float a0 = sw0[step], a1 = sw1[step];
+                        ok = role_wait(&s->dead, p.status, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        tcgen05_fence_after();
+                        const uint32_t acc = lanes + (uses & 1) * ACC;
+#pragma unroll
+                        for (int q = 0; q < NB / 16; ++q) {
+                            if (q >= groups) break;
+                            uint32_t a[8], b[8];
+                            tmem_load8(acc + q * 16, a);
+                            tmem_load8(acc + COLS + q * 16, b);
+                            tmem_wait_load(a, b);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float f = sx[q * 8 + i];
+                                d0[q][i] = fmaf(__uint_as_float(a[i]), f * a0, d0[q][i]);
+                                d1[q][i] = fmaf(__uint_as_float(b[i]), f * a1, d1[q][i]);
+                            }
                         }
+                        tcgen05_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses & 1]));
+                        ++uses;
                     }
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses & 1]));
                 }
-            } else {
-                ok = role_wait(s, p.status, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (ok) {
-                    tcgen05_fence_after();
-                    const uint32_t at = lanes + (uses & 1) * 2 * NB;
+                ok = finishers_well(ok);
+                if (!ok) break;
 #pragma unroll
-                    for (int q = 0; q < NB / 16; ++q) {
-                        if (q * 16 + side * 8 >= en.n) break;
-                        uint32_t a[8], b[8];
-                        tmem_load8(at + q * 16, a);
-                        tmem_load8(at + NB + q * 16, b);
-                        tmem_wait_load(a, b);
+                for (int q = 0; q < NB / 16; ++q) {
+                    const int c0 = q * 16 + side * 8;
+                    if (c0 >= en.n) break;
+                    if constexpr (DOWN) {
+                        to_y(c0, d0[q], d1[q]);
+                    } else {
+                        uint32_t(*top)[8] = s->top[side];
+                        const int i = tile * ROWS + row;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            d0[q * 8 + i] = __uint_as_float(a[i]);
-                            d1[q * 8 + i] = __uint_as_float(b[i]);
+                        for (int j = 0; j < 8; ++j) {
+                            d0[q][j] = swiglu(d0[q][j], d1[q][j]);
+                            const float m = fabsf(d0[q][j]);
+                            const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, m == m ? __float_as_uint(m) : 0u);
+                            if (lane == j) top[quad][j] = t;
                         }
-                    }
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses & 1]));
-                    ++uses;
-                }
-            }
-            ok = finishers_well(ok);
-            if (!ok) break;
-            if constexpr (!DOWN) {
-                const int i = tile * kMoeRows + row;
+                        group_sync(1 + side, 128);
 #pragma unroll
-                for (int j = 0; j < HALF; ++j) d0[j] = swiglu(d0[j], d1[j]);
-                if constexpr (FP8) {
-                    uint32_t(*top)[64] = s->top[side];
-#pragma unroll
-                    for (int j = 0; j < HALF; ++j) {
-                        if ((j >> 3) * 16 + side * 8 + (j & 7) >= en.n) continue;
-                        const float m = fabsf(d0[j]);
-                        const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, m == m ? __float_as_uint(m) : 0u);
-                        if (lane == (j & 31)) top[quad][j] = t;
-                    }
-                    group_sync(1 + side, 128);
-#pragma unroll
-                    for (int j = 0; j < HALF; ++j) {
-                        const int c = (j >> 3) * 16 + side * 8 + (j & 7);
-                        if (c < en.n) {
+                        for (int j = 0; j < 8; ++j) {
+                            if (c0 + j >= en.n) break;
                             const uint32_t t = max(max(top[0][j], top[1][j]), max(top[2][j], top[3][j]));
                             const float amax = fminf(fmaxf(__uint_as_float(t), kAmaxFloor), FLT_MAX);
-                            const int pair = list[en.start + c];
-                            p.act[static_cast<int64_t>(pair) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[j] * (448.f / amax)));
+                            const int pair = pairs[c0 + j];
+                            p.act[static_cast<int64_t>(pair) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[q][j] * (448.f / amax)));
                             if (row == 0) p.act_sf[static_cast<int64_t>(pair) * IB + tile] = amax / 448.f;
                         }
+                        group_sync(1 + side, 128);
                     }
-                    group_sync(1 + side, 128);
-                } else {
-                    if (i < I)
-#pragma unroll
-                        for (int j = 0; j < HALF; ++j) {
-                            const int c = (j >> 3) * 16 + side * 8 + (j & 7);
-                            if (c < en.n)
-                                reinterpret_cast<__nv_bfloat16*>(p.act)[static_cast<int64_t>(list[en.start + c]) * I + i] =
-                                    __float2bfloat16_rn(d0[j]);
-                        }
                 }
             } else {
-                const int h0 = tile * 2 * kMoeRows + row, h1 = h0 + kMoeRows;
+                ok = role_wait(&s->dead, p.status, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
+                ok = finishers_well(ok);
+                if (!ok) break;
+                tcgen05_fence_after();
+                const uint32_t acc = lanes + (uses & 1) * ACC;
+#pragma unroll 1
+                for (int q = 0; q < groups; ++q) {
+                    const int c0 = q * 16 + side * 8;
+                    uint32_t a[8], b[8];
+                    float v0[8], v1[8];
+                    tmem_load8(acc + q * 16, a);
+                    tmem_load8(acc + (GATES ? 0 : COLS) + q * 16, b);
+                    tmem_wait_load(a, b);
 #pragma unroll
-                for (int j = 0; j < HALF; ++j) {
-                    const int c = (j >> 3) * 16 + side * 8 + (j & 7);
-                    if (c < en.n) {
-                        float* y = p.y + static_cast<int64_t>(list[en.start + c]) * H;
-                        if (h0 < H) y[h0] = d0[j];
-                        if (h1 < H) y[h1] = d1[j];
+                    for (int i = 0; i < 8; ++i) {
+                        v0[i] = __uint_as_float(a[i]);
+                        v1[i] = __uint_as_float(b[i]);
+                    }
+                    if constexpr (STACKED) {
+                        const int n16 = (en.n + 15) & ~15;
+                        tmem_load8(acc + n16 + q * 16, a);
+                        tmem_load8(acc + COLS + n16 + q * 16, b);
+                        tmem_wait_load(a, b);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            v0[i] += __uint_as_float(a[i]);
+                            v1[i] += __uint_as_float(b[i]);
+                        }
+                    }
+                    if constexpr (DOWN) {
+                        to_y(c0, v0, v1);
+                    } else {
+                        // lanes 64 .. 127 hold the up rows
+                        float(*up)[64] = s->up[side];
+                        if (row >= 64)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) up[j][row - 64] = v0[j];
+                        group_sync(1 + side, 128);
+                        const int i = tile * ROWS + row;
+                        if (row < 64 && i < I) {
+                            __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(p.act);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                if (c0 + j >= en.n) break;
+                                const float h = swiglu(v0[j], up[j][row]);
+                                const int64_t pair = pairs[c0 + j];
+                                const __nv_bfloat16 high = __float2bfloat16_rn(h);
+                                act[pair * I + i] = high;
+                                // an infinity is whole in its upper part
+                                act[(pair + P) * I + i] = __float2bfloat16_rn(fabsf(h) < INFINITY ? h - __bfloat162float(high) : 0.f);
+                            }
+                        }
+                        group_sync(1 + side, 128);
                     }
                 }
-                __threadfence();
-                group_sync(3, 32 * kFinishWarps);
-                if (tid == 64) s->last = atomicAdd(&p.counters[tile], 1) == M - 1;
-                group_sync(3, 32 * kFinishWarps);
-                if (s->last) {        // every pair's products for these columns are there
-                    __threadfence();
-                    const int q = (tid - 64) & 63, h = tile * 2 * kMoeRows + q * 4;
-                    if (h < H)
-                        for (int t = (tid - 64) >> 6; t < p.T; t += 4) {
-                            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                            for (int j = 0; j < p.k; ++j) {
-                                const int pair = t * p.k + j;
-                                if (!valid_expert(p.ids[pair], p.E)) continue;
-                                const float w = p.w[pair];
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<int64_t>(pair) * H + h));
-                                sum.x = fmaf(w, v.x, sum.x);
-                                sum.y = fmaf(w, v.y, sum.y);
-                                sum.z = fmaf(w, v.z, sum.z);
-                                sum.w = fmaf(w, v.w, sum.w);
-                            }
-                            st_u2(p.out + static_cast<int64_t>(t) * H + h,
-                                  make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w)));
-                        }
-                }
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses & 1]));
+                ++uses;
             }
         }
     }
-    if (DOWN && M == 0)               // no pair has an expert here
-        for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoeThreads + tid) * 4; i < static_cast<int64_t>(p.T) * H;
-             i += static_cast<int64_t>(gridDim.x) * kMoeThreads * 4)
-            st_u2(p.out + i, make_uint2(0, 0));
     __syncwarp();
-    if (warp == 0) {
-        // copies still in flight, when a role gave up before it took their stage
-        if (s->dead && lane == 0)
-            for (int i = max(0, issued - S); i < issued; ++i) mbar_wait(smem_addr(&s->full[i % S]), (i / S) & 1);
-        __syncwarp();
-    }
     tcgen05_fence_before();
     __syncthreads();
+    if (s->dead && tid == 0) {
+        // Copies still in flight when the roles gave up: a stage that one of the two
+        // loading warps did not come to gets its arrival, so that its phase can end.
+        const int lo = min(s->issued[0], s->issued[1]), hi = max(s->issued[0], s->issued[1]);
+        for (int i = lo; i < hi; ++i) mbar_arrive(smem_addr(&s->full[i % S]));
+        for (int i = max(0, hi - S); i < hi; ++i) mbar_wait(smem_addr(&s->full[i % S]), (i / S) & 1);
+    }
+    __syncwarp();
     if (warp == 1) {
         tcgen05_fence_after();
-        tmem_free(tmem, 4 * NB < 32 ? 32 : 4 * NB);
+        tmem_free(tmem, tmem_columns<FP8, DOWN, NB>());
     }
+}
+
+// out[t] from y, a thread for four columns of a token: the pairs in slot order, eight
+// rows in flight.
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const MoeParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int t = blockIdx.y, h = (blockIdx.x * kSumThreads + threadIdx.x) * 4;
+    if (h >= p.H) return;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* y = p.y + static_cast<int64_t>(t) * p.k * p.H + h;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        float4 v[8];
+        float w[8];
+        uint32_t on = 0;                              // a row without an expert holds anything: not added
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int pair = t * p.k + j0 + j;
+            const bool in = j0 + j < p.k;
+            v[j] = in ? __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(j0 + j) * p.H)) : sum;
+            w[j] = in ? __ldg(p.w + pair) : 0.f;
+            if (in && valid_expert(__ldg(p.ids + pair), p.E)) on |= 1u << j;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!(on >> j & 1u)) continue;
+            sum.x = fmaf(w[j], v[j].x, sum.x);
+            sum.y = fmaf(w[j], v[j].y, sum.y);
+            sum.z = fmaf(w[j], v[j].z, sum.z);
+            sum.w = fmaf(w[j], v[j].w, sum.w);
+        }
+    }
+    st_u2(p.out + static_cast<int64_t>(t) * p.H + h, make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w)));
 }
 
 using Kernel = void (*)(const MoeParams, const CUtensorMap, const CUtensorMap);
@@ -479,6 +642,11 @@ Kernel kernel_for(const MoeLayerShape& s, bool down) {
 }
 
 constexpr int kMaxSmem = 227 * 1024;
+
+int shared_bytes(int columns) {
+    return static_cast<int>(columns == 16 ? sizeof(Shared<16>) : columns == 32 ? sizeof(Shared<32>)
+                            : columns == 64 ? sizeof(Shared<64>) : sizeof(Shared<128>));
+}
 
 bool encode(void* encoder, CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint32_t* box) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -504,21 +672,24 @@ int64_t align256(int64_t v) { return (v + 255) & ~int64_t(255); }
 }  // namespace
 
 void moe_layer_choose(MoeLayerShape& s, int sms) {
-    const int64_t P = static_cast<int64_t>(s.T) * s.k, elem = s.fp8 ? 1 : 2;
-    s.columns = s.T <= 16 ? 16 : s.T <= 32 ? 32 : s.T <= 64 ? 64 : 128;
-    const int stage = kTileBytes + s.columns * 128;
+    const int64_t P = static_cast<int64_t>(s.T) * s.k;
+    // columns for twice an expert's mean share of the pairs: fewer leave more of the ring
+    // to the weights, and a popular expert's further chunks read its weights from L2
+    int64_t want = 2 * P / s.E + 8;
+    if (want > s.T) want = s.T;
+    s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
     const int64_t entries = (P < s.E ? P : s.E) + P / s.columns;
-    s.entries = static_cast<int>((entries < P ? entries : P) + 1) & ~1;
-    const int behind = static_cast<int>(sizeof(Shared)) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
+    s.entries = static_cast<int>((entries < P ? entries : P) + 3) & ~3;
+    const int behind = shared_bytes(s.columns) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
+    const int stage = 2 * kPanel + s.columns * 128 * (s.fp8 ? 1 : 2);
     s.stages = (kMaxSmem - 1024 - behind) / stage;
     if (s.stages > kRingStages) s.stages = kRingStages;
     s.smem = 1024 + behind + s.stages * stage;
     s.grid = sms;
     s.act = 0;
-    s.act_sf = align256(P * s.I * elem);
+    s.act_sf = align256(P * s.I * (s.fp8 ? 1 : 4));
     s.y = s.act_sf + (s.fp8 ? align256(P * (s.I / 128) * 4) : 0);
-    s.counters = s.y + align256(P * s.H * 4);
-    s.bytes = s.counters + align256((s.H + 2 * kMoeRows - 1) / (2 * kMoeRows) * 4);
+    s.bytes = s.y + align256(P * s.H * 4);
 }
 
 void* moe_layer_encoder() {
@@ -544,24 +715,34 @@ cudaError_t moe_layer_prepare(const MoeLayerShape& s) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return e;
     }
-    return cudaSuccess;
+    return preload(moe_sum_kernel);
 }
 
 cudaError_t moe_layer_launch(const MoeLayerShape& s, const MoeParams& p, const void* x, const void* w13, const void* w2,
                              int pdl, cudaStream_t st) {
     void* enc = moe_layer_encoder();
     if (!enc) return cudaErrorNotSupported;
-    const uint64_t T = s.T, H = s.H, I = s.I, E = s.E, P = T * s.k;
+    const uint64_t T = s.T, H = s.H, I = s.I, E = s.E, P = T * s.k * (s.fp8 ? 1 : 2);
     const uint32_t ke = s.fp8 ? 128 : 64;
     const uint64_t dx[] = {H, T}, d13[] = {H, 2 * I, E}, da[] = {I, P}, d2[] = {I, H, E};
-    const uint32_t row[] = {ke, 1}, box[] = {ke, kMoeRows, 1};
+    const uint32_t row[] = {ke, 1}, box13[] = {ke, s.fp8 ? kMoeRows : kMoeRows / 2, 1}, box2[] = {ke, kMoeRows, 1};
     CUtensorMap mx, m13, ma, m2;
-    if (!encode(enc, &mx, s.fp8, 2, x, dx, row) || !encode(enc, &m13, s.fp8, 3, w13, d13, box) ||
-        !encode(enc, &ma, s.fp8, 2, p.act, da, row) || !encode(enc, &m2, s.fp8, 3, w2, d2, box))
+    if (!encode(enc, &mx, s.fp8, 2, x, dx, row) || !encode(enc, &m13, s.fp8, 3, w13, d13, box13) ||
+        !encode(enc, &ma, s.fp8, 2, p.act, da, row) || !encode(enc, &m2, s.fp8, 3, w2, d2, box2))
         return cudaErrorInvalidValue;
     cudaError_t e = layer_launch(kernel_for(s, false), s.grid, kMoeThreads, s.smem, 1, pdl, st, p, m13, mx);
     if (e == cudaSuccess) e = layer_launch(kernel_for(s, true), s.grid, kMoeThreads, s.smem, 1, pdl, st, p, m2, ma);
-    return e;
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((s.H + 4 * kSumThreads - 1) / (4 * kSumThreads), s.T, 1);
+    cfg.blockDim = dim3(kSumThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, moe_sum_kernel, p);
 }
 
 }  // namespace mfr

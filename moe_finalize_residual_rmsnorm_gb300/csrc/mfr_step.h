@@ -11,7 +11,7 @@ namespace mfr {
 // ---- a MoE layer for a few tokens (mfr_moe_layer.cu) ---------------------------------
 constexpr int kMoeMaxPairs = 4096;
 constexpr int kMoeRows = 128;      // weight rows of one accumulator; a tile of weights has two
-constexpr int kMoeThreads = 320;   // a warp that loads, one that multiplies, eight that finish
+constexpr int kMoeThreads = 352;   // two warps that load, one that multiplies, eight that finish
 
 struct MoeLayerShape {
     int T;
@@ -21,15 +21,14 @@ struct MoeLayerShape {
     int k;
     int fp8;
     int columns;      // NB: pairs that one accumulator holds, 16 .. 128
-    int stages;
+    int stages;       // of the ring
     int smem;
     int entries;      // most (expert, chunk of pairs) entries
     int grid;
     // workspace: byte offsets
-    int64_t act;      // [pairs, I] bf16 or E4M3
+    int64_t act;      // [pairs, I] E4M3, or [2, pairs, I] bf16: upper and lower parts
     int64_t act_sf;   // [pairs, I / 128] FP32 (E4M3)
     int64_t y;        // [pairs, H] FP32
-    int64_t counters; // [tiles of H] int
     int64_t bytes;
 };
 
@@ -42,7 +41,6 @@ struct MoeParams {
     uint8_t* act;
     float* act_sf;
     float* y;
-    int* counters;
     uint16_t* out;            // [T, H]
     int* status;
     int T;

@@ -10,6 +10,16 @@
 
 namespace mfr {
 
+// One lane of a whole warp.  Products and copies take their operands from uniform
+// registers: in a loop that all lanes run, with this around the issue alone, they are
+// there; in a branch of one lane each operand is moved there anew (a stage of eight
+// products: 600 cycles).
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- tensor memory ---------------------------------------------------------------------
 // One whole warp allocates `columns` (a power of two, 32 to 512) and frees them.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_result, uint32_t columns) {
