@@ -80,32 +80,50 @@ __device__ __forceinline__ float shared_sigmoid(float l, float top) {
     return top > 0.f ? sigmoid(l) : expf(l - fmaxf(top, -FLT_MAX)) / (1.f + expf(l));
 }
 
-// The choice by keys in 64 bits, a round at a time; lane j gets the j-th expert.
+// Rises with f, a double that is no NaN; above 0.
+__device__ __forceinline__ unsigned long long order_key64(double f) {
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(f + 0.0));
+    return u ^ ((static_cast<long long>(u) >> 63) | 0x8000000000000000ull);
+}
+
+// The choice by keys in 64 bits among the experts whose FP32 key is at least `from`;
+// lane j gets the j-th one.  FP64 instructions are rare on this chip (a warp's takes 16
+// cycles), so that only those few experts' keys are computed, once.
 template <bool B16>
-__device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, int lane) {
-    double last = INFINITY;
-    int last_e = -1, mine = -1;
+__device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, float from, int lane) {
+    unsigned long long keys[kMaxExperts / 32];
+    const int n = (p.E + 31) / 32;
+    for (int i = 0; i < n; ++i) {
+        const int e = i * 32 + lane;
+        const float l = e < p.E ? logit_at<B16>(p.logits, at + e) : -INFINITY;
+        keys[i] = 0;
+        if (!(l > -INFINITY)) continue;
+        const float bias = p.bias[e];
+        if (sigmoid(l) + bias >= from)
+            keys[i] = order_key64(1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(bias));
+    }
+    int mine = -1;
     for (int j = 0; j < p.k; ++j) {
-        // the largest (key, lowest index) behind the last one
-        double best = -INFINITY;
-        int best_e = INT32_MAX;
-        for (int e = lane; e < p.E; e += 32) {
-            const float l = logit_at<B16>(p.logits, at + e);
-            if (!(l > -INFINITY)) continue;
-            const double key = 1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(p.bias[e]);
-            if (!(key > -INFINITY)) continue;
-            if (!(key < last || (key == last && e > last_e))) continue;
-            if (key > best || (key == best && e < best_e)) { best = key; best_e = e; }
-        }
+        unsigned long long best = 0;
+        int best_i = 0;
+        for (int i = 0; i < n; ++i)
+            if (keys[i] > best) {
+                best = keys[i];
+                best_i = i;
+            }
+        unsigned long long top = best;
+        int e = best_i * 32 + lane;
         for (int off = 16; off > 0; off >>= 1) {
-            const double k2 = __shfl_xor_sync(0xFFFFFFFFu, best, off);
-            const int e2 = __shfl_xor_sync(0xFFFFFFFFu, best_e, off);
-            if (k2 > best || (k2 == best && e2 < best_e)) { best = k2; best_e = e2; }
+            const unsigned long long k2 = __shfl_xor_sync(0xFFFFFFFFu, top, off);
+            const int e2 = __shfl_xor_sync(0xFFFFFFFFu, e, off);
+            if (k2 > top || (k2 == top && e2 < e)) {
+                top = k2;
+                e = e2;
+            }
         }
-        if (best_e == INT32_MAX) break;
-        if (lane == j) mine = best_e;
-        last = best;
-        last_e = best_e;
+        if (top == 0) break;
+        if (e % 32 == lane) keys[e / 32] = 0;
+        if (lane == j) mine = e;
     }
     return mine;
 }
@@ -142,6 +160,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams 
     int mine = -1;
     uint32_t before = 0;
     bool close = false;
+    float least = -INFINITY;
     const int rounds = p.bias ? p.k + 1 : p.k;            // one more: whether the first left out is close
     for (int j = 0; j < rounds; ++j) {
         uint32_t m = 0;
@@ -164,9 +183,11 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams 
             const float v = key_value(m);
             close |= j > 0 && !(key_value(before) - v > 0x1p-20f * (1.f + fabsf(v)));
             before = m;
+            if (j < p.k) least = v;
         }
     }
-    if (close) mine = choose_in_64_bits<B16>(p, at, lane);
+    // the least key that may be among the chosen: that of the k-th, less both errors
+    if (close) mine = choose_in_64_bits<B16>(p, at, least - 0x1p-20f * (1.f + fabsf(least)), lane);
     float w = mine >= 0 ? fminf(logit_at<B16>(p.logits, at + mine), FLT_MAX) : 0.f;
     if (p.sigmoid) {
         if (p.renormalize) top = warp_max(mine >= 0 ? w : -INFINITY);
