@@ -18,6 +18,7 @@ namespace mfr {
 namespace {
 
 constexpr int kClipThreads = 256;
+constexpr int kClipCtas = 6;             // an SM
 
 // The tensor that piece c belongs to.
 template <int N>
@@ -40,18 +41,18 @@ struct Piece {
     bool first, last;
 };
 
-__device__ __forceinline__ Piece piece_of(const void* in, int64_t n, int size, uint32_t index, int64_t vectors) {
+__device__ __forceinline__ Piece piece_of(const void* in, int64_t n, bool f32, uint32_t index, int64_t vectors) {
     Piece p;
-    const int64_t to = (16 - (reinterpret_cast<uintptr_t>(in) & 15)) & 15;
-    p.head = to / size < n ? to / size : n;
-    const int per = 16 / size;
-    const int64_t all = (n - p.head) / per;
-    p.tail = p.head + all * per;
+    const int to = static_cast<int>(16 - (reinterpret_cast<uintptr_t>(in) & 15)) & 15;
+    const int head = f32 ? to >> 2 : to >> 1, shift = f32 ? 2 : 3;      // elements of a vector: 4 or 8
+    p.head = head < n ? head : n;
+    const int64_t all = (n - p.head) >> shift;
+    p.tail = p.head + (all << shift);
     p.v0 = index * vectors;
     p.v1 = p.v0 + vectors < all ? p.v0 + vectors : all;
     p.first = index == 0;
     // the count of pieces is fixed by n alone, so the last piece may hold no vector
-    p.last = (static_cast<int64_t>(index) + 1) * vectors * per >= n;
+    p.last = ((static_cast<int64_t>(index) + 1) * vectors << shift) >= n;
     return p;
 }
 
@@ -130,7 +131,7 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads) squares_kernel(const __grid_constant__ ClipList<N> l, const ClipParams p) {
+__global__ void __launch_bounds__(kClipThreads, kClipCtas) squares_kernel(const __grid_constant__ ClipList<N> l, const ClipParams p) {
     __shared__ double s[kClipThreads / 32];
     const int tid = threadIdx.x;
     pdl_wait();
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kClipThreads) squares_kernel(const __grid_cons
         const int i = tensor_of(l, c), type = l.type[i], size = type == MFR_GRAD_F32 ? 4 : 2;
         const void* in = l.in[i];
         const int64_t n = l.numel[i];
-        const Piece q = piece_of(in, n, size, c - l.first[i], p.vectors);
+        const Piece q = piece_of(in, n, type == MFR_GRAD_F32, c - l.first[i], p.vectors);
         const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(in) + q.head * size);
         float a[4] = {0.f, 0.f, 0.f, 0.f};
         int64_t at = q.v0 + tid;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kClipThreads) squares_kernel(const __grid_cons
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_constant__ ClipList<N> l, const ClipParams p) {
+__global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __grid_constant__ ClipList<N> l, const ClipParams p) {
     __shared__ double s[kClipThreads / 32];
     const int tid = threadIdx.x;
     pdl_wait();
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_consta
         void* out = l.out[i];
         if (in == out && scale == 1.f) continue;
         const int64_t n = l.numel[i];
-        const Piece q = piece_of(in, n, size, c - l.first[i], p.vectors);
+        const Piece q = piece_of(in, n, type == MFR_GRAD_F32, c - l.first[i], p.vectors);
         if (q.first && tid < q.head) scale_element(in, out, tid, type, scale);
         if (q.last && q.tail + tid < n) scale_element(in, out, q.tail + tid, type, scale);
         if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
@@ -261,7 +262,7 @@ void clip_choose(ClipShape& s, int sms) {
         for (int i = g * kClipGroup; i < s.n && i < (g + 1) * kClipGroup; ++i) pieces += s.pieces[i];
         if (pieces > most) most = pieces;
     }
-    s.grid = static_cast<int>(most < sms * 4 ? most : sms * 4);
+    s.grid = static_cast<int>(most < sms * kClipCtas ? most : sms * kClipCtas);
 }
 
 cudaError_t clip_prepare() {

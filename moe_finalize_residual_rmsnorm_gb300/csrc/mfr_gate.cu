@@ -5,16 +5,17 @@
 //            equals the lowest index
 //   weights  w_j = scale * p_j, or scale * p_j / (p_1 + .. + p_k)
 //
-// A warp per token, its logits in registers (E / 32 a lane).  Each of the k
-// rounds is one maximum over the warp of order-preserving integer keys and one
-// minimum over the indices that hold it.  With softmax scores, and with sigmoid
-// ones without a bias, the keys are the logits themselves (both functions rise),
+// A warp per token, its logits in registers (E / 32 a lane) as order-preserving integer
+// keys.  k maxima over the lanes' largest keys give a bound that the k chosen reach and
+// few others do; those few (up to 32, else they are taken one by one) are compared
+// with each other.  With softmax scores, and with sigmoid ones without a bias, the keys
+// are the logits themselves (both functions rise),
 // so the choice is exact.  With a bias the FP32 keys are off by some of their last
 // bits: neighbours in the order that lie closer than those errors reach (about a
 // token in a thousand) are chosen once more by keys in 64 bits.
 //
-// Bytes bound neither direction on paper (32768 x 256: 5 us); the rounds'
-// instructions do.  The gradient of renormalised softmax weights reads the chosen
+// Bytes bound neither direction on paper (32768 x 256: 5 us); the choice's
+// instructions do (taking the k experts one by one: 50 us).  The gradient of renormalised softmax weights reads the chosen
 // logits alone.
 #include <cfloat>
 
@@ -44,12 +45,13 @@ __device__ __forceinline__ float logit_at(const void* l, int64_t i) {
     else return static_cast<const float*>(l)[i];
 }
 
-// This lane's logits of row `at`: vector v holds experts (v * 32 + lane) * V and on.
-template <bool B16, int V, int NV>
-__device__ __forceinline__ void load_row(const void* l, int64_t at, int E, int lane, float (&f)[NV * V]) {
+// This lane's N logits of row `at`, from expert lane * N on: lower lanes have lower
+// experts.  V: logits a load, where rows start on such a boundary.
+template <bool B16, int V, int N>
+__device__ __forceinline__ void load_row(const void* l, int64_t at, int E, int lane, float (&f)[N]) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int e = (v * 32 + lane) * V;
+    for (int v = 0; v < N; v += V) {
+        const int e = lane * N + v;
         if constexpr (V == 4) {
             float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             if (e < E) {
@@ -60,7 +62,7 @@ __device__ __forceinline__ void load_row(const void* l, int64_t at, int E, int l
                     x = *reinterpret_cast<const float4*>(static_cast<const float*>(l) + at + e);
                 }
             }
-            f[v * 4] = x.x; f[v * 4 + 1] = x.y; f[v * 4 + 2] = x.z; f[v * 4 + 3] = x.w;
+            f[v] = x.x; f[v + 1] = x.y; f[v + 2] = x.z; f[v + 3] = x.w;
         } else {
             f[v] = e < E ? logit_at<B16>(l, at + e) : -INFINITY;
         }
@@ -68,6 +70,10 @@ __device__ __forceinline__ void load_row(const void* l, int64_t at, int E, int l
 }
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+
+// For keys: __expf is off by 2 + 1.173 |l| ulp and __fdividef by 2, so that this is off
+// by 6.25 u (u = 2^-24): where |l| is large the sigmoid is flat.
+__device__ __forceinline__ float near_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
 
 __device__ __forceinline__ float warp_max(float v) {
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
@@ -99,7 +105,7 @@ __device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, f
         keys[i] = 0;
         if (!(l > -INFINITY)) continue;
         const float bias = p.bias[e];
-        if (sigmoid(l) + bias >= from)
+        if (near_sigmoid(l) + bias >= from)
             keys[i] = order_key64(1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(bias));
     }
     int mine = -1;
@@ -128,62 +134,110 @@ __device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, f
     return mine;
 }
 
-template <bool B16, int V, int NV>
+template <bool B16, int V, int N>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams p) {
+    __shared__ unsigned long long s_few[kGateWarps][32];
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_dependents();
     if (t >= p.T) return;
     const int64_t at = t * p.E;
-    float l[NV * V];
-    load_row<B16, V, NV>(p.logits, at, p.E, lane, l);
+    float l[N];
+    load_row<B16, V, N>(p.logits, at, p.E, lane, l);
     float denominator = 1.f, top = 0.f;
     if (!p.sigmoid && !p.renormalize) {
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NV * V; ++i) m = fmaxf(m, l[i]);
+        for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
         m = warp_max(m);
         top = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV * V; ++i) sum += l[i] > -INFINITY ? expf(fminf(l[i], FLT_MAX) - top) : 0.f;
+        for (int i = 0; i < N; ++i) sum += l[i] > -INFINITY ? expf(fminf(l[i], FLT_MAX) - top) : 0.f;
         denominator = warp_allreduce_sum(sum);
     }
-    uint32_t key[NV * V];
+    uint32_t key[N], best = 0;                            // this lane's largest
 #pragma unroll
-    for (int i = 0; i < NV * V; ++i) {
-        const int e = (i / V * 32 + lane) * V + i % V;
+    for (int i = 0; i < N; ++i) {
         key[i] = order_key(l[i]);
-        if (p.bias && key[i]) key[i] = order_key(sigmoid(l[i]) + p.bias[e]);
+        if (p.bias && key[i]) key[i] = order_key(near_sigmoid(l[i]) + __ldg(p.bias + lane * N + i));
+        best = max(best, key[i]);
     }
     int mine = -1;
-    uint32_t before = 0;
     bool close = false;
     float least = -INFINITY;
-    const int rounds = p.bias ? p.k + 1 : p.k;            // one more: whether the first left out is close
-    for (int j = 0; j < rounds; ++j) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < NV * V; ++i) m = max(m, key[i]);
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
+    const int wanted = p.bias ? p.k + 1 : p.k;            // one more: whether the first left out is close
+    // A bound below the last of the wanted keys: that many lanes' largest reach it.
+    uint32_t bound = 1, left = best;
+    for (int j = 0; j < wanted; ++j) {
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, left);
+        bound = max(m, 1u);
         if (m == 0) break;
-        uint32_t e = UINT32_MAX;
+        if (left == m) left = 0;
+    }
+    int count = 0;
 #pragma unroll
-        for (int i = NV * V - 1; i >= 0; --i)
-            if (key[i] == m) e = static_cast<uint32_t>((i / V * 32 + lane) * V + i % V);
-        e = __reduce_min_sync(0xFFFFFFFFu, e);
+    for (int i = 0; i < N; ++i) count += key[i] >= bound;
+    count = __reduce_add_sync(0xFFFFFFFFu, count);
+    if (count <= 32) {
+        // The few experts that reach it, one a lane, find their ranks by comparing.
+        unsigned long long* mem = s_few[threadIdx.x >> 5];
+        int at_mem = 0;
 #pragma unroll
-        for (int i = 0; i < NV * V; ++i)
-            if (e == static_cast<uint32_t>((i / V * 32 + lane) * V + i % V)) key[i] = 0;
-        if (lane == j && j < p.k) mine = static_cast<int>(e);
+        for (int i = 0; i < N; ++i) {
+            const bool in = key[i] >= bound;
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+            // falling order of these: keys, then rising experts
+            if (in) mem[at_mem + __popc(who & ((1u << lane) - 1))] = (static_cast<unsigned long long>(key[i]) << 32) | (0xFFFFFFFFu - (lane * N + i));
+            at_mem += __popc(who);
+        }
+        __syncwarp();
+        const unsigned long long own = lane < count ? mem[lane] : 0;
+        int rank = 0;
+        for (int j = 0; j < count; ++j) rank += mem[j] > own;
+        __syncwarp();
+        if (lane < count) mem[rank] = own;
+        __syncwarp();
+        const unsigned long long sorted = lane < count ? mem[lane] : 0;
+        if (lane < p.k && lane < count) mine = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(sorted));
         if (p.bias) {
-            // an FP32 key is off by at most 4 u for the sigmoid (exp, sum, quotient)
-            // and u |key| for the sum: two of them by less than 2^-20 (1 + |key|)
-            const float v = key_value(m);
-            close |= j > 0 && !(key_value(before) - v > 0x1p-20f * (1.f + fabsf(v)));
-            before = m;
-            if (j < p.k) least = v;
+            // a key is off by less than 2^-21 (1 + |key|): 6.25 u for the sigmoid, u |key| for the sum
+            const float v = key_value(static_cast<uint32_t>(sorted >> 32));
+            const float next = __shfl_down_sync(0xFFFFFFFFu, v, 1);
+            close = __any_sync(0xFFFFFFFFu, lane < p.k && lane + 1 < count && !(v - next > 0x1p-20f * (1.f + fabsf(next))));
+            least = __shfl_sync(0xFFFFFFFFu, v, min(p.k, count) - 1 < 0 ? 0 : min(p.k, count) - 1);
+        }
+    } else {
+        uint32_t before = 0;
+        for (int j = 0; j < wanted; ++j) {
+            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+            if (m == 0) break;
+            const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+            int e = 0;
+            if (lane == owner) {
+                // its first expert with this key goes
+                best = 0;
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const bool hit = !found && key[i] == m;
+                    if (hit) {
+                        e = i;
+                        key[i] = 0;
+                    }
+                    found |= hit;
+                    best = max(best, key[i]);
+                }
+            }
+            e = __shfl_sync(0xFFFFFFFFu, e, owner) + owner * N;
+            if (lane == j && j < p.k) mine = e;
+            if (p.bias) {
+                const float v = key_value(m);
+                close |= j > 0 && !(key_value(before) - v > 0x1p-20f * (1.f + fabsf(v)));
+                before = m;
+                if (j < p.k) least = v;
+            }
         }
     }
     // the least key that may be among the chosen: that of the k-th, less both errors
@@ -205,6 +259,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams 
 }
 
 // d_logits: what every expert gets, then the chosen ones once more with their own part.
+// Vector v of a lane holds experts (v * 32 + lane) * V and on.
 template <bool B16, int V, int NV>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GateParams p) {
     const int lane = threadIdx.x & 31;
@@ -213,23 +268,32 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GatePa
     pdl_launch_dependents();
     if (t >= p.T) return;
     const int64_t at = t * p.E;
+    const bool full = !p.sigmoid && !p.renormalize;       // every expert gets something
+    float l[NV * V];
+    if (full)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float x[V];
+            load_row<B16, V, V>(p.logits, at + v * 32 * V, p.E - v * 32 * V, lane, x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[v * V + i] = x[i];
+        }
     // lane j: the j-th chosen expert, its logit and the gradient of its weight
     int e = lane < p.k ? p.ids_in[t * p.k + lane] : -1;
-    if (e >= p.E || (e < 0 && e != -1)) {
+    const float d_w = lane < p.k ? p.d_w[t * p.k + lane] : 0.f;
+    if (e >= p.E || e < -1) {
         atomicOr(p.status, MFR_STATUS_BAD_INDEX);
         e = -1;
     }
     const bool on = e >= 0;
     const float x = on ? logit_at<B16>(p.logits, at + e) : -INFINITY, le = fminf(x, FLT_MAX);
-    const float g = on ? p.scale * p.d_w[t * p.k + lane] : 0.f;
-    float d, all = 0.f;                                   // of the chosen; factor of p_e for every expert
-    float l[NV * V];
-    float top = 0.f, denominator = 1.f;
+    const float g = on ? p.scale * d_w : 0.f;
+    float d, all = 0.f, own = 0.f;                        // of the chosen; factor of the others' scores; that of the chosen
     if (p.sigmoid) {
         float q = on ? sigmoid(le) : 0.f;
         d = g;
         if (p.renormalize) {
-            const float m = warp_max(x);              // all lanes, those without a slot too
+            const float m = warp_max(x);                  // all lanes, those without a slot too
             q = on ? shared_sigmoid(le, m) : 0.f;
             const float total = warp_allreduce_sum(q);
             q = total > 0.f ? q / total : 0.f;
@@ -244,51 +308,55 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GatePa
         q = total > 0.f ? q / total : 0.f;
         d = q * (g - warp_allreduce_sum(g * q));
     } else {
-        load_row<B16, V, NV>(p.logits, at, p.E, lane, l);
         float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV * V; ++i) m = fmaxf(m, l[i]);
         m = warp_max(m);
-        top = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
+        m = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV * V; ++i) {
-            l[i] = l[i] > -INFINITY ? expf(fminf(l[i], FLT_MAX) - top) : 0.f;
+            l[i] = l[i] > -INFINITY ? expf(fminf(l[i], FLT_MAX) - m) : 0.f;
             sum += l[i];
         }
-        denominator = fmaxf(warp_allreduce_sum(sum), FLT_MIN);
-        const float q = x > -INFINITY ? expf(le - top) / denominator : 0.f;
-        all = -warp_allreduce_sum(g * q);
+        const float inv = 1.f / fmaxf(warp_allreduce_sum(sum), FLT_MIN);
+        const float q = x > -INFINITY ? expf(le - m) * inv : 0.f;
+        const float mean = warp_allreduce_sum(g * q);
+        all = -mean * inv;
+        own = -mean * q;
         d = q * g;
     }
     // the same expert in several slots: the first of them has the sum
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     float mine = d;
+    bool first = on;
     for (int j = 0; j < p.k; ++j) {
         const float v = __shfl_sync(0xFFFFFFFFu, d, j);
-        if (j != lane && (same >> j & 1u)) mine += v;
+        const int other = __shfl_sync(0xFFFFFFFFu, e, j);
+        if (other == e && j != lane) {
+            mine += v;
+            first = first && j > lane;
+        }
     }
-    const float own = !p.sigmoid && !p.renormalize && on ? all * (x > -INFINITY ? expf(le - top) / denominator : 0.f) : 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int first = (v * 32 + lane) * V;
-        if (first >= p.E) continue;
+        const int from = (v * 32 + lane) * V;
+        if (from >= p.E) continue;
         float o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = all != 0.f ? all * (l[v * V + i] / denominator) : 0.f;
+        for (int i = 0; i < V; ++i) o[i] = full ? all * l[v * V + i] : 0.f;
         if constexpr (V == 4) {
             if constexpr (B16)
-                st_u2(static_cast<uint16_t*>(p.d_logits) + at + first, make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])));
+                st_u2(static_cast<uint16_t*>(p.d_logits) + at + from, make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])));
             else
-                st_f4(static_cast<float*>(p.d_logits) + at + first, make_float4(o[0], o[1], o[2], o[3]));
+                st_f4(static_cast<float*>(p.d_logits) + at + from, make_float4(o[0], o[1], o[2], o[3]));
         } else if constexpr (B16) {
-            static_cast<__nv_bfloat16*>(p.d_logits)[at + first] = __float2bfloat16_rn(o[0]);
+            static_cast<__nv_bfloat16*>(p.d_logits)[at + from] = __float2bfloat16_rn(o[0]);
         } else {
-            static_cast<float*>(p.d_logits)[at + first] = o[0];
+            static_cast<float*>(p.d_logits)[at + from] = o[0];
         }
     }
     __syncwarp();                                         // the warp's own stores come in this order
-    if (on && lane == __ffs(same) - 1) {
+    if (first) {
         if constexpr (B16) static_cast<__nv_bfloat16*>(p.d_logits)[at + e] = __float2bfloat16_rn(mine + own);
         else static_cast<float*>(p.d_logits)[at + e] = mine + own;
     }
@@ -296,17 +364,17 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GatePa
 
 using Kernel = void (*)(const GateParams);
 
-template <bool B16, int V, int NV>
-Kernel pick(bool grad) { return grad ? gate_grad_kernel<B16, V, NV> : gate_kernel<B16, V, NV>; }
+template <bool B16, int V, int N>
+Kernel pick(bool grad) { return grad ? gate_grad_kernel<B16, V, N / V> : gate_kernel<B16, V, N>; }
 
-// Four logits a load where rows start on such a boundary, else one.
+// N logits a lane; four a load where rows start on such a boundary, else one.
 template <bool B16>
 Kernel kernel_for(int E, bool grad) {
     if (E % 4 == 0) {
-        if (E <= 128) return pick<B16, 4, 1>(grad);
-        if (E <= 256) return pick<B16, 4, 2>(grad);
-        if (E <= 512) return pick<B16, 4, 4>(grad);
-        return pick<B16, 4, 8>(grad);
+        if (E <= 128) return pick<B16, 4, 4>(grad);
+        if (E <= 256) return pick<B16, 4, 8>(grad);
+        if (E <= 512) return pick<B16, 4, 16>(grad);
+        return pick<B16, 4, 32>(grad);
     }
     if (E <= 32) return pick<B16, 1, 1>(grad);
     if (E <= 128) return pick<B16, 1, 4>(grad);

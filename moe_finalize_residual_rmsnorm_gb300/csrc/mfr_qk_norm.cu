@@ -12,11 +12,12 @@
 //
 // Bytes bound both: every head is read once (the gradient: twice) and written
 // once.  A lane holds 16 elements of a head, both members of each of its pairs, so
-// that nothing is exchanged but the sums; a head takes 1 to 32 lanes and a
-// warp 32 to 1 heads of one token.  A warp works on a run of such groups of heads,
-// token after token, with the next group's loads in flight and a token's cosines
-// and sines in registers while it lasts.  Queries and keys are runs of different
-// CTAs, so that a lane's gamma and its running sum of d_gamma stay where they are.
+// that nothing is exchanged but the sums; a head takes 1 to 32 lanes and a warp a
+// group of 32 to 1 heads of one token.  A warp's unit of work is a run of groups of one
+// token, whose cosines and sines stay in registers, and it has several groups' loads in
+// flight (four, the gradient two): with one ahead, an iteration was as long as a
+// load.  Queries and keys belong to different CTAs, so that a lane's gamma and its
+// running sum of d_gamma stay where they are.
 #include "moe_step_ops.h"
 #include "mfr_device.cuh"
 #include "mfr_layer.h"
@@ -84,20 +85,14 @@ __device__ __forceinline__ Place place_of(int u, int D, int rotary, bool interle
 }
 
 // The pairs of x turned by the angles, or back.
-template <bool BACK>
-__device__ __forceinline__ void turn(float (&x)[16], const float (&c)[8], const float (&s)[8], bool interleaved) {
+template <bool BACK, bool PAIRED>
+__device__ __forceinline__ void turn(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float sn = BACK ? -s[i] : s[i];
-        if (interleaved) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * c[i] - b * sn;
-            x[2 * i + 1] = a * sn + b * c[i];
-        } else {
-            const float a = x[i], b = x[i + 8];
-            x[i] = a * c[i] - b * sn;
-            x[i + 8] = a * sn + b * c[i];
-        }
+        const int ia = PAIRED ? 2 * i : i, ib = PAIRED ? 2 * i + 1 : i + 8;
+        const float sn = BACK ? -s[i] : s[i], a = x[ia], b = x[ib];
+        x[ia] = a * c[i] - b * sn;
+        x[ib] = a * sn + b * c[i];
     }
 }
 
@@ -108,117 +103,117 @@ __device__ __forceinline__ float head_sum(float v) {
     return v;
 }
 
-// Runs of groups: CTA b < blocks_q has queries' groups, the others keys'.  A group is
-// HPW = 32 / L heads of one token, group g of a side belongs to token g / per_token.
+// Units of work: CTA b < blocks_q has queries' units, the others keys'.  A group is HPW =
+// 32 / L heads; a token's per_token groups are `slices` runs of `run` groups, and
+// unit u is run u % slices of token u / slices.  A warp takes every stride-th unit.
 struct QkRuns {
     int blocks_q;
-    int run[2];             // groups a warp
+    int run[2];
     int per_token[2];
+    int slices[2];
+    int64_t stride[2];
 };
 
-template <bool F16, int L, bool GRAD>
-__global__ void __launch_bounds__(32 * kQkWarps) qk_kernel(const QkParams p, const QkRuns r) {
+// PAIRED: pairs (2 i, 2 i + 1).
+template <bool F16, int L, bool GRAD, bool PAIRED>
+__global__ void __launch_bounds__(32 * kQkWarps, GRAD ? 2 : 3) qk_kernel(const QkParams p, const QkRuns r) {
     constexpr int HPW = 32 / L;
+    constexpr int BATCH = GRAD ? 2 : 4;       // groups whose loads are in flight
     __shared__ float s_gamma[GRAD ? kQkWarps : 1][GRAD ? 16 * L : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int which = static_cast<int>(blockIdx.x) < r.blocks_q ? 0 : 1;
     const QkSide& side = p.side[which];
-    const int64_t block = blockIdx.x - (which ? r.blocks_q : 0);
-    const int per = r.per_token[which];
-    const int64_t groups = p.T * per;
-    const int64_t g0 = (block * kQkWarps + warp) * r.run[which];
-    const int64_t g1 = g0 + r.run[which] < groups ? g0 + r.run[which] : groups;
-    const Place pl = place_of(lane % L, p.D, p.rotary, p.interleaved != 0);
-    const bool interleaved = p.interleaved != 0;
+    const int per = r.per_token[which], slices = r.slices[which], run = r.run[which];
+    const int64_t units = p.T * slices;
+    const Place pl = place_of(lane % L, p.D, p.rotary, PAIRED);
+    const float per_element = 1.f / static_cast<float>(p.D);
     pdl_wait();
     pdl_launch_dependents();
-    float gamma[16], sum[GRAD ? 16 : 1];
+    float sum[GRAD ? 16 : 1];
     const uint4 none = make_uint4(0, 0, 0, 0);
-    widen<F16>(pl.a >= 0 ? *reinterpret_cast<const uint4*>(side.gamma + pl.a) : none, gamma);
-    widen<F16>(pl.b >= 0 ? *reinterpret_cast<const uint4*>(side.gamma + pl.b) : none, gamma + 8);
+    const uint4 gamma_a = pl.a >= 0 ? *reinterpret_cast<const uint4*>(side.gamma + pl.a) : none;
+    const uint4 gamma_b = pl.b >= 0 ? *reinterpret_cast<const uint4*>(side.gamma + pl.b) : none;
     if constexpr (GRAD)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[i] = 0.f;
-    float c[8], s[8];
+    for (int64_t unit = (blockIdx.x - (which ? r.blocks_q : 0)) * int64_t(kQkWarps) + warp; unit < units; unit += r.stride[which]) {
+        const int64_t t = unit / slices;
+        const int g0 = static_cast<int>(unit - t * slices) * run, g1 = min(g0 + run, per);
+        const int pos = p.positions[t];
+        const uint16_t* xs = side.x + t * side.x_token;
+        const uint16_t* ds = GRAD ? side.d_out + t * side.d_token : nullptr;
+        float c[8], s[8];
+        bool known = false, good = false;
+        for (int g = g0; g < g1; g += BATCH) {
+            uint4 xa[BATCH], xb[BATCH], da[GRAD ? BATCH : 1], db[GRAD ? BATCH : 1];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
-    int64_t t = per > 0 ? g0 / per : 0;
-    int in_token = static_cast<int>(g0 - t * per);
-    bool known = false;                       // c and s are those of token t
-    bool good = false;
-    // the next group's loads: x, and for the gradient d_out
-    uint4 xa = none, xb = none, da = none, db = none;
-    auto load = [&](int64_t tok, int grp) {
-        const int head = grp * HPW + lane / L;
-        const bool on = head < side.heads;
-        const uint16_t* x = side.x + tok * side.x_token + head * side.x_head;
-        xa = on && pl.a >= 0 ? ld_stream_u4(x + pl.a) : none;
-        xb = on && pl.b >= 0 ? ld_stream_u4(x + pl.b) : none;
-        if constexpr (GRAD) {
-            const uint16_t* d = side.d_out + tok * side.d_token + head * side.d_head;
-            da = on && pl.a >= 0 ? ld_stream_u4(d + pl.a) : none;
-            db = on && pl.b >= 0 ? ld_stream_u4(d + pl.b) : none;
-        }
-    };
-    if (g0 < g1) load(t, in_token);
-    for (int64_t g = g0; g < g1; ++g) {
-        const uint4 va = xa, vb = xb, ea = da, eb = db;
-        if (!known) {
-            const int pos = p.positions[t];
-            good = static_cast<uint32_t>(pos) < static_cast<uint32_t>(p.max_positions);
-            if (!good && lane == 0) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
-            if (good && pl.turns) {
-                const float* row = p.table + static_cast<int64_t>(pos) * p.rotary + 8 * pl.u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    c[i] = __ldg(row + i);
-                    s[i] = __ldg(row + p.rotary / 2 + i);
+            for (int i = 0; i < BATCH; ++i) {
+                const int head = (g + i) * HPW + lane / L;
+                const bool on = g + i < g1 && head < side.heads;
+                const uint16_t* x = xs + head * side.x_head;
+                xa[i] = ld_stream_u4_if(x + pl.a, on && pl.a >= 0);
+                xb[i] = ld_stream_u4_if(x + pl.b, on && pl.b >= 0);
+                if constexpr (GRAD) {
+                    const uint16_t* d = ds + head * side.d_head;
+                    da[i] = ld_stream_u4_if(d + pl.a, on && pl.a >= 0);
+                    db[i] = ld_stream_u4_if(d + pl.b, on && pl.b >= 0);
                 }
             }
-            known = true;
-        }
-        const int64_t t_now = t;
-        const int head = in_token * HPW + lane / L;
-        const bool good_now = good;
-        if (++in_token == per) {
-            in_token = 0;
-            ++t;
-        }
-        if (g + 1 < g1) load(t, in_token);
-        float x[16];
-        widen<F16>(va, x);
-        widen<F16>(vb, x + 8);
-        float ss = 0.f;
+            if (!known) {
+                known = true;
+                good = static_cast<uint32_t>(pos) < static_cast<uint32_t>(p.max_positions);
+                if (!good && lane == 0) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
+                const float4* row = reinterpret_cast<const float4*>(p.table + static_cast<int64_t>(pos) * p.rotary + 8 * pl.u);
+                const bool on = good && pl.turns;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-        const float inv = rsqrtf(head_sum<L>(ss) / static_cast<float>(p.D) + p.eps);
-        if constexpr (!GRAD) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * gamma[i];
-            if (pl.turns) turn<false>(x, c, s, interleaved);
-        } else {
-            float d[16];
-            widen<F16>(ea, d);
-            widen<F16>(eb, d + 8);
-            if (pl.turns) turn<true>(d, c, s, interleaved);
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] *= inv;                                  // unit
-                if (good_now) sum[i] = fmaf(d[i], x[i], sum[i]);
-                d[i] *= gamma[i];
-                dot = fmaf(d[i], x[i], dot);
+                for (int i = 0; i < 2; ++i) {
+                    const float4 a = on ? __ldg(row + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+                    const float4 b = on ? __ldg(row + p.rotary / 8 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    c[4 * i] = a.x; c[4 * i + 1] = a.y; c[4 * i + 2] = a.z; c[4 * i + 3] = a.w;
+                    s[4 * i] = b.x; s[4 * i + 1] = b.y; s[4 * i + 2] = b.z; s[4 * i + 3] = b.w;
+                }
             }
-            const float mean = head_sum<L>(dot) / static_cast<float>(p.D);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = inv * (d[i] - x[i] * mean);
+            for (int i = 0; i < BATCH; ++i) {
+                if (g + i >= g1) break;
+                const int head = (g + i) * HPW + lane / L;
+                float x[16], gamma[16];
+                widen<F16>(gamma_a, gamma);
+                widen<F16>(gamma_b, gamma + 8);
+                widen<F16>(xa[i], x);
+                widen<F16>(xb[i], x + 8);
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+                const float inv = rsqrtf(fmaf(head_sum<L>(ss), per_element, p.eps));
+                if constexpr (!GRAD) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * gamma[e];
+                    if (pl.turns) turn<false, PAIRED>(x, c, s);
+                } else {
+                    float d[16];
+                    widen<F16>(da[i], d);
+                    widen<F16>(db[i], d + 8);
+                    if (pl.turns) turn<true, PAIRED>(d, c, s);
+                    float dot = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        x[e] *= inv;                                  // unit
+                        if (good) sum[e] = fmaf(d[e], x[e], sum[e]);
+                        d[e] *= gamma[e];
+                        dot = fmaf(d[e], x[e], dot);
+                    }
+                    const float mean = head_sum<L>(dot) * per_element;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = inv * (d[e] - x[e] * mean);
+                }
+                if (good && head < side.heads) {
+                    uint16_t* o = side.out + t * side.out_token + head * side.out_head;
+                    if (pl.a >= 0) st_stream_u4(o + pl.a, narrow<F16>(x));
+                    if (pl.b >= 0) st_stream_u4(o + pl.b, narrow<F16>(x + 8));
+                }
+            }
         }
-        if (good_now && head < side.heads) {
-            uint16_t* o = side.out + t_now * side.out_token + head * side.out_head;
-            if (pl.a >= 0) st_stream_u4(o + pl.a, narrow<F16>(x));
-            if (pl.b >= 0) st_stream_u4(o + pl.b, narrow<F16>(x + 8));
-        }
-        if (t != t_now) known = false;
     }
     if constexpr (GRAD) {
         // this warp's heads, then the CTA's warps, in a fixed order
@@ -231,7 +226,7 @@ __global__ void __launch_bounds__(32 * kQkWarps) qk_kernel(const QkParams p, con
         __syncthreads();
         for (int j = threadIdx.x; j < 16 * L; j += 32 * kQkWarps) {
             const int i = j / L;
-            const Place q = place_of(j % L, p.D, p.rotary, interleaved);
+            const Place q = place_of(j % L, p.D, p.rotary, PAIRED);
             const int at = i < 8 ? q.a : q.b;
             if (at < 0) continue;
             float v = 0.f;
@@ -243,7 +238,7 @@ __global__ void __launch_bounds__(32 * kQkWarps) qk_kernel(const QkParams p, con
 }
 
 // d_gamma from the CTAs' partial sums: a CTA for 32 columns of one side.
-constexpr int kSumWarps = 16;
+constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps) qk_gamma_kernel(const QkParams p, const QkRuns r, int blocks) {
     __shared__ float s_sum[kSumWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tiles = (p.D + 31) / 32;
@@ -251,10 +246,13 @@ __global__ void __launch_bounds__(32 * kSumWarps) qk_gamma_kernel(const QkParams
     pdl_wait();
     pdl_launch_dependents();
     const int first = which ? r.blocks_q : 0, last = which ? blocks : r.blocks_q;
-    float v = 0.f;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};                // four rows in flight
     if (col < p.D)
-        for (int b = first + warp; b < last; b += kSumWarps) v += __ldcg(p.partial + static_cast<int64_t>(b) * p.D + col);
-    s_sum[warp][lane] = v;
+        for (int b = first + warp; b < last; b += 4 * kSumWarps)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (b + i * kSumWarps < last) v[i] += __ldcg(p.partial + static_cast<int64_t>(b + i * kSumWarps) * p.D + col);
+    s_sum[warp][lane] = (v[0] + v[1]) + (v[2] + v[3]);
     __syncthreads();
     if (warp == 0 && col < p.D) {
         float total = 0.f;
@@ -271,40 +269,53 @@ int lanes_for(int D) {
     return l;
 }
 
-template <bool F16, bool GRAD>
+template <bool F16, bool GRAD, bool PAIRED>
 Kernel kernel_of(int D) {
     switch (lanes_for(D)) {
-        case 1: return qk_kernel<F16, 1, GRAD>;
-        case 2: return qk_kernel<F16, 2, GRAD>;
-        case 4: return qk_kernel<F16, 4, GRAD>;
-        case 8: return qk_kernel<F16, 8, GRAD>;
-        case 16: return qk_kernel<F16, 16, GRAD>;
-        default: return qk_kernel<F16, 32, GRAD>;
+        case 1: return qk_kernel<F16, 1, GRAD, PAIRED>;
+        case 2: return qk_kernel<F16, 2, GRAD, PAIRED>;
+        case 4: return qk_kernel<F16, 4, GRAD, PAIRED>;
+        case 8: return qk_kernel<F16, 8, GRAD, PAIRED>;
+        case 16: return qk_kernel<F16, 16, GRAD, PAIRED>;
+        default: return qk_kernel<F16, 32, GRAD, PAIRED>;
     }
 }
 
-Kernel kernel_for(const QkShape& s, bool grad) {
-    if (s.fp16) return grad ? kernel_of<true, true>(s.D) : kernel_of<true, false>(s.D);
-    return grad ? kernel_of<false, true>(s.D) : kernel_of<false, false>(s.D);
+template <bool GRAD>
+Kernel kernel_of(const QkShape& s) {
+    if (s.fp16) return s.interleaved ? kernel_of<true, GRAD, true>(s.D) : kernel_of<true, GRAD, false>(s.D);
+    return s.interleaved ? kernel_of<false, GRAD, true>(s.D) : kernel_of<false, GRAD, false>(s.D);
 }
 
-// A warp's run: as few groups as keep every SM in work, so that small calls have
-// many warps and large ones few partial sums and token changes.
+Kernel kernel_for(const QkShape& s, bool grad) { return grad ? kernel_of<true>(s) : kernel_of<false>(s); }
+
+// A warp's run is a token's groups where tokens are many, fewer where that leaves
+// SMs without work.  The gradient's warps stay for several units, two CTAs an SM, so
+// that there are few partial sums of d_gamma.
 QkRuns runs_for(const QkShape& s, int64_t T, bool grad, int sms, int* blocks) {
-    const int hpw = 32 / lanes_for(s.D);
+    const int hpw = 32 / lanes_for(s.D), heads[2] = {s.heads_q, s.heads_k};
     QkRuns r;
-    r.per_token[0] = (s.heads_q + hpw - 1) / hpw;
-    r.per_token[1] = (s.heads_k + hpw - 1) / hpw;
-    const int64_t groups = T * (r.per_token[0] + r.per_token[1]);
-    const int64_t warps = static_cast<int64_t>(sms) * kQkWarps * (grad ? 3 : 16);
-    int64_t run = (groups + warps - 1) / warps;
-    if (!grad && run > 16) run = 16;
-    if (run < 1) run = 1;
+    int64_t units[2];
+    for (int i = 0; i < 2; ++i) {
+        const int per = (heads[i] + hpw - 1) / hpw;
+        int run = per < 16 ? per : 16;
+        while (run > 1 && T * ((per + run - 1) / run) < static_cast<int64_t>(sms) * 8) run = (run + 1) / 2;
+        r.per_token[i] = per;
+        r.run[i] = run;
+        r.slices[i] = (per + run - 1) / run;
+        units[i] = T * r.slices[i];
+    }
+    const int64_t all = units[0] * r.run[0] + units[1] * r.run[1], most = static_cast<int64_t>(sms) * 2;
     int64_t b[2];
     for (int i = 0; i < 2; ++i) {
-        r.run[i] = static_cast<int>(run);
-        const int64_t per_block = run * kQkWarps;
-        b[i] = (T * r.per_token[i] + per_block - 1) / per_block;
+        b[i] = (units[i] + kQkWarps - 1) / kQkWarps;
+        if (grad && all > 0) {
+            // shares of the CTAs in the proportion of the work
+            int64_t share = most * (units[i] * r.run[i]) / all;
+            if (share < 1) share = 1;
+            if (b[i] > share) b[i] = share;
+        }
+        r.stride[i] = b[i] * kQkWarps;
     }
     r.blocks_q = static_cast<int>(b[0]);
     *blocks = static_cast<int>(b[0] + b[1]);

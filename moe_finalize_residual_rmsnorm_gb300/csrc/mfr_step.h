@@ -120,7 +120,6 @@ struct QkParams {
     int64_t T;
     int D;
     int rotary;
-    int interleaved;
     int max_positions;
     float eps;
 };
@@ -132,7 +131,7 @@ cudaError_t qk_launch(const QkShape& s, const QkParams& p, bool grad, int sms, i
 
 // ---- gradient norm and clipping (mfr_clip.cu) ------------------------------------------------
 constexpr int kClipGroup = 512;           // tensors of one launch
-constexpr int kClipFew = 32;
+constexpr int kClipFew = 64;
 constexpr int kClipMaxVectors = 4096;     // 16-byte vectors of a piece
 constexpr int kClipMaxTensors = 65536;
 

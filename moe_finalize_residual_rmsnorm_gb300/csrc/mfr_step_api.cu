@@ -78,7 +78,6 @@ QkParams qk_params(moe_op_t op, float eps, const float* table, const int32_t* po
     p.T = op->T;
     p.D = op->qk.D;
     p.rotary = op->qk.rotary;
-    p.interleaved = op->qk.interleaved;
     p.max_positions = op->qk.max_positions;
     p.eps = eps;
     return p;
