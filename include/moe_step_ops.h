@@ -90,6 +90,11 @@ int moe_gate_grad_run(moe_op_t op, const float* d_topk_weights, const void* logi
  * 8 <= H, I <= 16384, 1 <= E <= 1024, 1 <= k <= 16.  x, w13, w2, out and the
  * workspace 16-byte aligned, the others 4-byte.  Outputs overlap nothing. */
 int moe_small_layer_plan(moe_op_t* op, int64_t T, int64_t H, int64_t I, int E, int k, int e4m3, const mfr_options* opt);
+/* Failure-path self test.  The kernels' warps hand each other stages of a ring in shared
+ * memory; their waits give up after about 2 s with MFR_STATUS_TIMEOUT.  This sets
+ * another limit for the plan's later runs, in SM cycles from 0 (every wait gives up at
+ * once) to 4000000000 (the limit a plan begins with), else MFR_ERR_INVALID_ARG. */
+int moe_small_layer_set_wait_limit(moe_op_t op, int64_t limit_cycles);
 int moe_small_layer_run(moe_op_t op, const void* x, const float* x_sf, const int32_t* expert_ids,
                         const float* topk_weights, const void* w13, const float* w13_sf, const void* w2,
                         const float* w2_sf, void* out, void* workspace, int64_t workspace_bytes, void* stream);

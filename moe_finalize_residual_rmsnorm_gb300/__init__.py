@@ -134,6 +134,7 @@ SIGNATURES = {
     "moe_gate_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP]),
     "moe_gate_grad_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP]),
     "moe_small_layer_plan": (_I, [ctypes.POINTER(_VP), _I64, _I64, _I64, _I, _I, _I, ctypes.POINTER(Options)]),
+    "moe_small_layer_set_wait_limit": (_I, [_VP, _I64]),
     "moe_small_layer_run": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP]),
     "moe_qk_norm_rope_plan": (_I, [ctypes.POINTER(_VP), _I64, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(Options)]),
     "moe_qk_norm_rope_run": (_I, [_VP, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP, _VP]),

@@ -28,6 +28,7 @@ namespace mfr {
 namespace {
 
 constexpr int kGateWarps = 4;
+constexpr int kGateCtas = 8;           // an SM, of the choice
 
 // Rises with f; 0 for -infinity and NaN, which are never chosen.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -71,9 +72,15 @@ __device__ __forceinline__ void load_row(const void* l, int64_t at, int E, int l
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
 
-// For keys: __expf is off by 2 + 1.173 |l| ulp and __fdividef by 2, so that this is off
-// by 6.25 u (u = 2^-24): where |l| is large the sigmoid is flat.
-__device__ __forceinline__ float near_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+// For keys, off by less than 6.25 u (u = 2^-24): ex2.approx is off by 2^-22 and its
+// rounded argument by 2 u |l|, which the sigmoid's slope makes 1.25 u at most (where
+// |l| is large it is flat); the sum by u, rcp.approx by 2^-23.
+__device__ __forceinline__ float near_sigmoid(float l) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
 __device__ __forceinline__ float warp_max(float v) {
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
@@ -92,9 +99,14 @@ __device__ __forceinline__ unsigned long long order_key64(double f) {
     return u ^ ((static_cast<long long>(u) >> 63) | 0x8000000000000000ull);
 }
 
+// An expert's key in 64 bits.  FP64 instructions are slow on this chip (a warp's takes 16
+// cycles), so that few are computed, a lane each where that goes.
+__device__ __noinline__ unsigned long long exact_key(float l, float bias) {
+    return order_key64(1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(bias));
+}
+
 // The choice by keys in 64 bits among the experts whose FP32 key is at least `from`;
-// lane j gets the j-th one.  FP64 instructions are rare on this chip (a warp's takes 16
-// cycles), so that only those few experts' keys are computed, once.
+// lane j gets the j-th one.
 template <bool B16>
 __device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, float from, int lane) {
     unsigned long long keys[kMaxExperts / 32];
@@ -105,8 +117,7 @@ __device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, f
         keys[i] = 0;
         if (!(l > -INFINITY)) continue;
         const float bias = p.bias[e];
-        if (near_sigmoid(l) + bias >= from)
-            keys[i] = order_key64(1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(bias));
+        if (near_sigmoid(l) + bias >= from) keys[i] = exact_key(l, bias);
     }
     int mine = -1;
     for (int j = 0; j < p.k; ++j) {
@@ -134,127 +145,180 @@ __device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, f
     return mine;
 }
 
+// A warp's tokens are t, t + all warps, ...: the next one's logits are on their way
+// while this one's experts are chosen.
 template <bool B16, int V, int N>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams p) {
-    __shared__ unsigned long long s_few[kGateWarps][32];
+    __shared__ unsigned long long s_key[kGateWarps][32];
+    __shared__ float s_logit[kGateWarps][32];
+    __shared__ int s_expert[kGateWarps][32];
     const int lane = threadIdx.x & 31;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
+    unsigned long long* keys = s_key[threadIdx.x >> 5];
+    float* logits = s_logit[threadIdx.x >> 5];
+    int* experts = s_expert[threadIdx.x >> 5];
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kGateWarps;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_dependents();
-    if (t >= p.T) return;
-    const int64_t at = t * p.E;
-    float l[N];
-    load_row<B16, V, N>(p.logits, at, p.E, lane, l);
-    float denominator = 1.f, top = 0.f;
-    if (!p.sigmoid && !p.renormalize) {
-        float m = -INFINITY;
+    float next[N];
+    if (t < p.T) load_row<B16, V, N>(p.logits, t * p.E, p.E, lane, next);
+    for (; t < p.T; t += warps) {
+        const int64_t at = t * p.E;
+        float l[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
-        m = warp_max(m);
-        top = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
-        float sum = 0.f;
+        for (int i = 0; i < N; ++i) l[i] = next[i];
+        if (t + warps < p.T) load_row<B16, V, N>(p.logits, at + warps * p.E, p.E, lane, next);
+        float denominator = 1.f, top = 0.f;
+        if (!p.sigmoid && !p.renormalize) {
+            float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum += l[i] > -INFINITY ? expf(fminf(l[i], FLT_MAX) - top) : 0.f;
-        denominator = warp_allreduce_sum(sum);
-    }
-    uint32_t key[N], best = 0;                            // this lane's largest
+            for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+            m = warp_max(m);
+            top = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
+            float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        key[i] = order_key(l[i]);
-        if (p.bias && key[i]) key[i] = order_key(near_sigmoid(l[i]) + __ldg(p.bias + lane * N + i));
-        best = max(best, key[i]);
-    }
-    int mine = -1;
-    bool close = false;
-    float least = -INFINITY;
-    const int wanted = p.bias ? p.k + 1 : p.k;            // one more: whether the first left out is close
-    // A bound below the last of the wanted keys: that many lanes' largest reach it.
-    uint32_t bound = 1, left = best;
-    for (int j = 0; j < wanted; ++j) {
-        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, left);
-        bound = max(m, 1u);
-        if (m == 0) break;
-        if (left == m) left = 0;
-    }
-    int count = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) count += key[i] >= bound;
-    count = __reduce_add_sync(0xFFFFFFFFu, count);
-    if (count <= 32) {
-        // The few experts that reach it, one a lane, find their ranks by comparing.
-        unsigned long long* mem = s_few[threadIdx.x >> 5];
-        int at_mem = 0;
+            for (int i = 0; i < N; ++i) sum += l[i] > -INFINITY ? expf(fminf(l[i], FLT_MAX) - top) : 0.f;
+            denominator = warp_allreduce_sum(sum);
+        }
+        uint32_t key[N], best = 0;                        // this lane's largest
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const bool in = key[i] >= bound;
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-            // falling order of these: keys, then rising experts
-            if (in) mem[at_mem + __popc(who & ((1u << lane) - 1))] = (static_cast<unsigned long long>(key[i]) << 32) | (0xFFFFFFFFu - (lane * N + i));
-            at_mem += __popc(who);
+            float k = l[i];
+            if (p.bias) k = k > -INFINITY ? near_sigmoid(k) + __ldg(p.bias + lane * N + i) : -INFINITY;
+            key[i] = order_key(k);
+            best = max(best, key[i]);
         }
-        __syncwarp();
-        const unsigned long long own = lane < count ? mem[lane] : 0;
-        int rank = 0;
-        for (int j = 0; j < count; ++j) rank += mem[j] > own;
-        __syncwarp();
-        if (lane < count) mem[rank] = own;
-        __syncwarp();
-        const unsigned long long sorted = lane < count ? mem[lane] : 0;
-        if (lane < p.k && lane < count) mine = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(sorted));
-        if (p.bias) {
-            // a key is off by less than 2^-21 (1 + |key|): 6.25 u for the sigmoid, u |key| for the sum
-            const float v = key_value(static_cast<uint32_t>(sorted >> 32));
-            const float next = __shfl_down_sync(0xFFFFFFFFu, v, 1);
-            close = __any_sync(0xFFFFFFFFu, lane < p.k && lane + 1 < count && !(v - next > 0x1p-20f * (1.f + fabsf(next))));
-            least = __shfl_sync(0xFFFFFFFFu, v, min(p.k, count) - 1 < 0 ? 0 : min(p.k, count) - 1);
-        }
-    } else {
-        uint32_t before = 0;
+        int mine = -1;
+        float x = 0.f;                                    // its logit
+        // one more: whether the first left out is close; and another, so that the bound lies
+        // below what may be among the chosen (32768 x 256, k = 8: 32 -> 26 us; with k = 16 more
+        // than 32 experts reach it too often: 33 -> 43)
+        const int wanted = p.bias ? p.k + (p.k <= 8 ? 2 : 1) : p.k;
+        // A bound below the last of the wanted keys: that many lanes' largest reach it.
+        uint32_t bound = 1, left = best;
         for (int j = 0; j < wanted; ++j) {
-            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, left);
+            bound = max(m, 1u);
             if (m == 0) break;
-            const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
-            int e = 0;
-            if (lane == owner) {
-                // its first expert with this key goes
-                best = 0;
-                bool found = false;
+            if (left == m) left = 0;
+        }
+        int count = 0;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const bool hit = !found && key[i] == m;
-                    if (hit) {
-                        e = i;
-                        key[i] = 0;
+        for (int i = 0; i < N; ++i) count += key[i] >= bound;
+        count = __reduce_add_sync(0xFFFFFFFFu, count);
+        if (count <= 32) {
+            // The few experts that reach it, one a lane, find their ranks by comparing.
+            int at_mem = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool in = key[i] >= bound;
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+                if (in) {
+                    const int to = at_mem + __popc(who & ((1u << lane) - 1));
+                    // falling order of these: keys, then rising experts
+                    keys[to] = (static_cast<unsigned long long>(key[i]) << 32) | (0xFFFFFFFFu - (lane * N + i));
+                    logits[to] = l[i];
+                }
+                at_mem += __popc(who);
+            }
+            __syncwarp();
+            unsigned long long own = lane < count ? keys[lane] : 0;
+            const float own_l = lane < count ? logits[lane] : 0.f;
+            const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(own));
+            int rank = 0;
+            for (int j = 0; j < count; ++j) rank += keys[j] > own;
+            if (p.bias) {
+                // Neighbours in the order that are closer than their keys' errors, two of less
+                // than 2^-21 (1 + |key|) each (6.25 u for the sigmoid, u |key| for the sum):
+                // keys in 64 bits decide, unless experts below the bound may be among them.
+                if (lane < count) experts[rank] = static_cast<int>(own >> 32);
+                __syncwarp();
+                const float v = key_value(lane < count ? static_cast<uint32_t>(experts[lane]) : 0x80000000u);
+                const float after = __shfl_down_sync(0xFFFFFFFFu, v, 1);
+                const bool close = lane < p.k && lane + 1 < count && !(v - after > 0x1p-20f * (1.f + fabsf(after)));
+                if (__any_sync(0xFFFFFFFFu, close)) {
+                    const float least = __shfl_sync(0xFFFFFFFFu, v, max(0, min(p.k, count) - 1));
+                    const float from = least - 0x1p-20f * (1.f + fabsf(least));
+                    if (bound > 1 && !(key_value(bound) < from)) {
+                        mine = choose_in_64_bits<B16>(p, at, from, lane);
+                        count = -1;
+                    } else {
+                        if (lane < count) {
+                            own = exact_key(own_l, __ldg(p.bias + e));
+                            keys[lane] = own;
+                            experts[lane] = e;
+                        }
+                        __syncwarp();
+                        rank = 0;
+                        for (int j = 0; j < count; ++j) rank += keys[j] > own || (keys[j] == own && experts[j] < e);
                     }
-                    found |= hit;
-                    best = max(best, key[i]);
                 }
             }
-            e = __shfl_sync(0xFFFFFFFFu, e, owner) + owner * N;
-            if (lane == j && j < p.k) mine = e;
-            if (p.bias) {
-                const float v = key_value(m);
-                close |= j > 0 && !(key_value(before) - v > 0x1p-20f * (1.f + fabsf(v)));
-                before = m;
-                if (j < p.k) least = v;
+            __syncwarp();
+            if (count >= 0) {
+                if (lane < count) {
+                    experts[rank] = e;
+                    logits[rank] = own_l;
+                }
+                __syncwarp();
+                if (lane < p.k && lane < count) {
+                    mine = experts[lane];
+                    x = logits[lane];
+                }
             }
+            __syncwarp();
+        } else {
+            count = -1;
+            uint32_t before = 0;
+            bool close = false;
+            float least = -INFINITY;
+            for (int j = 0; j < (p.bias ? p.k + 1 : p.k); ++j) {
+                const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+                if (m == 0) break;
+                const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+                int e = 0;
+                if (lane == owner) {
+                    // its first expert with this key goes
+                    best = 0;
+                    bool found = false;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const bool hit = !found && key[i] == m;
+                        if (hit) {
+                            e = i;
+                            key[i] = 0;
+                        }
+                        found |= hit;
+                        best = max(best, key[i]);
+                    }
+                }
+                e = __shfl_sync(0xFFFFFFFFu, e, owner) + owner * N;
+                if (lane == j && j < p.k) mine = e;
+                if (p.bias) {
+                    const float v = key_value(m);
+                    close |= j > 0 && !(key_value(before) - v > 0x1p-20f * (1.f + fabsf(v)));
+                    before = m;
+                    if (j < p.k) least = v;
+                }
+            }
+            // the least key that may be among the chosen: that of the k-th, less both errors
+            if (close) mine = choose_in_64_bits<B16>(p, at, least - 0x1p-20f * (1.f + fabsf(least)), lane);
         }
-    }
-    // the least key that may be among the chosen: that of the k-th, less both errors
-    if (close) mine = choose_in_64_bits<B16>(p, at, least - 0x1p-20f * (1.f + fabsf(least)), lane);
-    float w = mine >= 0 ? fminf(logit_at<B16>(p.logits, at + mine), FLT_MAX) : 0.f;
-    if (p.sigmoid) {
-        if (p.renormalize) top = warp_max(mine >= 0 ? w : -INFINITY);
-        w = mine < 0 ? 0.f : p.renormalize ? shared_sigmoid(w, top) : sigmoid(w);
-    } else {
-        if (p.renormalize) top = __shfl_sync(0xFFFFFFFFu, w, 0);   // the first chosen is the largest
-        w = mine >= 0 ? expf(w - top) : 0.f;
-    }
-    if (p.renormalize) denominator = warp_allreduce_sum(w);
-    if (p.sigmoid && !p.renormalize) denominator = 1.f;
-    if (lane < p.k) {
-        p.ids[t * p.k + lane] = mine;
-        p.w[t * p.k + lane] = w > 0.f ? p.scale * (w / denominator) : 0.f;
+        if (count < 0 && mine >= 0) x = logit_at<B16>(p.logits, at + mine);
+        float w = mine >= 0 ? fminf(x, FLT_MAX) : 0.f;
+        if (p.sigmoid) {
+            if (p.renormalize) top = warp_max(mine >= 0 ? w : -INFINITY);
+            w = mine < 0 ? 0.f : p.renormalize ? shared_sigmoid(w, top) : sigmoid(w);
+        } else {
+            if (p.renormalize) top = __shfl_sync(0xFFFFFFFFu, w, 0);   // the first chosen is the largest
+            w = mine >= 0 ? expf(w - top) : 0.f;
+        }
+        if (p.renormalize) denominator = warp_allreduce_sum(w);
+        if (p.sigmoid && !p.renormalize) denominator = 1.f;
+        if (lane < p.k) {
+            p.ids[t * p.k + lane] = mine;
+            p.w[t * p.k + lane] = w > 0.f ? p.scale * (w / denominator) : 0.f;
+        }
     }
 }
 
@@ -391,8 +455,9 @@ cudaError_t gate_prepare(int E, int b16) {
     return e == cudaSuccess ? preload(kernel_for(E, b16 != 0, true)) : e;
 }
 
-cudaError_t gate_launch(const GateParams& p, int b16, bool grad, int pdl, cudaStream_t s) {
-    return layer_launch(kernel_for(p.E, b16 != 0, grad), (p.T + kGateWarps - 1) / kGateWarps, 32 * kGateWarps, 0, 1, pdl, s, p);
+cudaError_t gate_launch(const GateParams& p, int b16, bool grad, int sms, int pdl, cudaStream_t s) {
+    const int64_t ctas = (p.T + kGateWarps - 1) / kGateWarps, most = static_cast<int64_t>(sms) * kGateCtas;
+    return layer_launch(kernel_for(p.E, b16 != 0, grad), grad || ctas < most ? ctas : most, 32 * kGateWarps, 0, 1, pdl, s, p);
 }
 
 }  // namespace mfr

@@ -110,16 +110,17 @@ __device__ __forceinline__ bool finishers_well(bool ok) {
     return all != 0;
 }
 
-// A role's wait for another.  It gives up after kWaitCycles, or when another has given up.
-__device__ bool role_wait(int* dead_word, int* status, uint32_t bar, uint32_t parity) {
-    if (mbar_test_parity(bar, parity)) return true;
+// A role's wait for another.  It gives up after p.wait_limit cycles (0: at once, whatever
+// there is), or when another has given up.
+__device__ bool role_wait(int* dead_word, const MoeParams& p, uint32_t bar, uint32_t parity) {
+    if (p.wait_limit > 0 && mbar_test_parity(bar, parity)) return true;
     volatile int* dead = dead_word;
     const long long t0 = clock64();
-    while (!mbar_test_parity(bar, parity)) {
+    while (p.wait_limit == 0 || !mbar_test_parity(bar, parity)) {
         if (*dead) return false;
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 >= p.wait_limit) {
             *dead = 1;
-            atomicOr(status, MFR_STATUS_TIMEOUT);
+            atomicOr(p.status, MFR_STATUS_TIMEOUT);
             return false;
         }
     }
@@ -279,7 +280,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             const int tile = u / M, expert = unpack_entry(entries[u - tile * M]).expert;
             const int c1a = tile * ROWS, c1b = DOWN ? c1a + kMoeRows : I + c1a;
             for (int kb = 0; kb < KB; ++kb, ++i) {
-                if (i >= S) ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p.status, smem_addr(&s->empty[st]), parity));
+                if (i >= S) ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p, smem_addr(&s->empty[st]), parity));
                 if (!ok) break;
                 const uint32_t bar = smem_addr(&s->full[st]), a = ring + st * STAGE;
                 if (elect_lane()) {
@@ -322,7 +323,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             const int gathers = (en.n + 3) >> 2;
             const uint32_t second = ring + 2 * kPanel + (STACKED ? (en.n + 15) & ~15 : NB) * 128;
             for (int kb = 0; kb < KB; ++kb, ++i) {
-                if (i >= S) ok = role_wait(&s->dead, p.status, smem_addr(&s->empty[st]), parity);
+                if (i >= S) ok = role_wait(&s->dead, p, smem_addr(&s->empty[st]), parity);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const uint32_t bar = smem_addr(&s->full[st]), b = ring + st * STAGE + 2 * kPanel;
@@ -347,8 +348,8 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             const uint32_t desc = mma_desc(FP8, STACKED ? 2 * n : n);
             for (int kb = 0; kb < KB; ++kb) {
                 if ((FP8 || kb == 0) && uses > 1)
-                    ok = role_wait(&s->dead, p.status, smem_addr(&s->taken[uses & 1]), ((uses >> 1) - 1) & 1);
-                ok = ok && role_wait(&s->dead, p.status, smem_addr(&s->full[st]), parity);
+                    ok = role_wait(&s->dead, p, smem_addr(&s->taken[uses & 1]), ((uses >> 1) - 1) & 1);
+                ok = ok && role_wait(&s->dead, p, smem_addr(&s->full[st]), parity);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tcgen05_fence_after();
@@ -454,7 +455,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         if (HALF > 32) sx[lane + 32] = f1[step];
                         __syncwarp();
                         const float a0 = sw0[step], a1 = sw1[step];
-                        ok = role_wait(&s->dead, p.status, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
+                        ok = role_wait(&s->dead, p, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         tcgen05_fence_after();
@@ -511,7 +512,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     }
                 }
             } else {
-                ok = role_wait(&s->dead, p.status, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
+                ok = role_wait(&s->dead, p, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
                 ok = finishers_well(ok);
                 if (!ok) break;
                 tcgen05_fence_after();

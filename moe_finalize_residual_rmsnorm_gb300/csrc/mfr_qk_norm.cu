@@ -28,35 +28,67 @@ namespace {
 
 constexpr int kQkWarps = 8;
 
+// Two FP32 values that one instruction works on.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ float2 halves(f2 v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ f2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 swapped(f2 v) {
+    const float2 f = halves(v);
+    return pair(f.y, f.x);
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    const float2 f = halves(v);
+    return f.x + f.y;
+}
+
+// Eight 16-bit values as four pairs, and back.
 template <bool F16>
-__device__ __forceinline__ void widen(uint4 v, float* f) {
-    if constexpr (F16) {
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void widen(uint4 v, f2* f) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F16) {
             const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            f[2 * i] = x.x;
-            f[2 * i + 1] = x.y;
+            f[i] = pair(x.x, x.y);
+        } else {
+            f[i] = pair(bf16_lo(u[i]), bf16_hi(u[i]));
         }
-    } else {
-        f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-        f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
     }
 }
 
 template <bool F16>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+__device__ __forceinline__ uint32_t narrow2(f2 v) {
+    const float2 f = halves(v);
     if constexpr (F16) {
-        const __half2 h = __floats2half2_rn(a, b);
+        const __half2 h = __floats2half2_rn(f.x, f.y);
         return *reinterpret_cast<const uint32_t*>(&h);
     } else {
-        return pack_bf16x2(a, b);
+        return pack_bf16x2(f.x, f.y);
     }
 }
 
 template <bool F16>
-__device__ __forceinline__ uint4 narrow(const float* f) {
-    return make_uint4(narrow2<F16>(f[0], f[1]), narrow2<F16>(f[2], f[3]), narrow2<F16>(f[4], f[5]), narrow2<F16>(f[6], f[7]));
+__device__ __forceinline__ uint4 narrow(const f2* f) {
+    return make_uint4(narrow2<F16>(f[0]), narrow2<F16>(f[1]), narrow2<F16>(f[2]), narrow2<F16>(f[3]));
 }
 
 // Which elements of a head a lane holds: eight from `a` and eight from `b` (-1: none).
@@ -84,29 +116,60 @@ __device__ __forceinline__ Place place_of(int u, int D, int rotary, bool interle
     return p;
 }
 
+// A lane's cosines and sines, as `turn` takes them: for pairs (i, i + rotary / 2) four
+// pairs each of neighbours, for pairs (2 i, 2 i + 1) eight of (cos, cos) and of (-sin, sin).
+template <bool PAIRED>
+struct Angles {
+    f2 c[PAIRED ? 8 : 4], s[PAIRED ? 8 : 4];
+    __device__ __forceinline__ void set(int i, float c0, float c1, float s0, float s1) {      // angles 2 i and 2 i + 1
+        if constexpr (PAIRED) {
+            c[2 * i] = both(c0);
+            c[2 * i + 1] = both(c1);
+            s[2 * i] = pair(-s0, s0);
+            s[2 * i + 1] = pair(-s1, s1);
+        } else {
+            c[i] = pair(c0, c1);
+            s[i] = pair(s0, s1);
+        }
+    }
+};
+
 // The pairs of x turned by the angles, or back.
 template <bool BACK, bool PAIRED>
-__device__ __forceinline__ void turn(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+__device__ __forceinline__ void turn(f2 (&x)[8], const Angles<PAIRED>& t) {
+    const f2 minus = both(-1.f);
+    if constexpr (PAIRED) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int ia = PAIRED ? 2 * i : i, ib = PAIRED ? 2 * i + 1 : i + 8;
-        const float sn = BACK ? -s[i] : s[i], a = x[ia], b = x[ib];
-        x[ia] = a * c[i] - b * sn;
-        x[ib] = a * sn + b * c[i];
+        for (int i = 0; i < 8; ++i) x[i] = fma2(swapped(x[i]), BACK ? mul2(t.s[i], minus) : t.s[i], mul2(x[i], t.c[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f2 a = x[i], b = x[i + 4], less = mul2(BACK ? a : b, minus);
+            x[i] = fma2(BACK ? b : less, t.s[i], mul2(a, t.c[i]));
+            x[i + 4] = fma2(BACK ? less : a, t.s[i], mul2(b, t.c[i]));
+        }
     }
 }
 
+// Sum over a head's lanes: L of them, or (L = 0) `lanes`, not a power of two, from `base` on.
 template <int L>
-__device__ __forceinline__ float head_sum(float v) {
+__device__ __forceinline__ float head_sum(float v, int lanes, int base) {
+    if constexpr (L > 0) {
 #pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    return v;
+        for (int off = L / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+        return v;
+    } else {
+        float sum = 0.f;
+        for (int i = 0; i < lanes; ++i) sum += __shfl_sync(0xFFFFFFFFu, v, base + i);
+        return sum;
+    }
 }
 
 // Units of work: CTA b < blocks_q has queries' units, the others keys'.  A group is HPW =
-// 32 / L heads; a token's per_token groups are `slices` runs of `run` groups, and
+// 32 / lanes heads; a token's per_token groups are `slices` runs of `run` groups, and
 // unit u is run u % slices of token u / slices.  A warp takes every stride-th unit.
 struct QkRuns {
+    int lanes;              // of a head
     int blocks_q;
     int run[2];
     int per_token[2];
@@ -114,49 +177,59 @@ struct QkRuns {
     int64_t stride[2];
 };
 
-// PAIRED: pairs (2 i, 2 i + 1).
+// L: lanes of a head, 0: no power of two.  PAIRED: pairs (2 i, 2 i + 1).
 template <bool F16, int L, bool GRAD, bool PAIRED>
-__global__ void __launch_bounds__(32 * kQkWarps, GRAD ? 2 : 3) qk_kernel(const QkParams p, const QkRuns r) {
-    constexpr int HPW = 32 / L;
-    constexpr int BATCH = GRAD ? 2 : 4;       // groups whose loads are in flight
-    __shared__ float s_gamma[GRAD ? kQkWarps : 1][GRAD ? 16 * L : 1];
+__global__ void __launch_bounds__(32 * kQkWarps, GRAD ? 2 : 3) qk_kernel(const __grid_constant__ QkParams p, const __grid_constant__ QkRuns r) {
+    constexpr int BATCH = 2;                  // groups whose loads are in flight
+    __shared__ float s_gamma[GRAD ? kQkWarps : 1][GRAD ? 32 * 16 : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lanes = L > 0 ? L : r.lanes, heads_a_warp = 32 / lanes;
     const int which = static_cast<int>(blockIdx.x) < r.blocks_q ? 0 : 1;
     const QkSide& side = p.side[which];
     const int per = r.per_token[which], slices = r.slices[which], run = r.run[which];
     const int64_t units = p.T * slices;
-    const Place pl = place_of(lane % L, p.D, p.rotary, PAIRED);
+    const int of_head = lane / lanes, base = of_head * lanes;
+    const bool used = of_head < heads_a_warp;             // lanes behind the last whole head have none
+    const Place pl = place_of(lane - base, p.D, p.rotary, PAIRED);
+    const bool has_a = used && pl.a >= 0, has_b = used && pl.b >= 0;
     const float per_element = 1.f / static_cast<float>(p.D);
     pdl_wait();
     pdl_launch_dependents();
-    float sum[GRAD ? 16 : 1];
     const uint4 none = make_uint4(0, 0, 0, 0);
-    const uint4 gamma_a = pl.a >= 0 ? *reinterpret_cast<const uint4*>(side.gamma + pl.a) : none;
-    const uint4 gamma_b = pl.b >= 0 ? *reinterpret_cast<const uint4*>(side.gamma + pl.b) : none;
+    f2 gamma[8], sum[GRAD ? 8 : 1];
+    widen<F16>(has_a ? *reinterpret_cast<const uint4*>(side.gamma + pl.a) : none, gamma);
+    widen<F16>(has_b ? *reinterpret_cast<const uint4*>(side.gamma + pl.b) : none, gamma + 4);
     if constexpr (GRAD)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = 0.f;
-    for (int64_t unit = (blockIdx.x - (which ? r.blocks_q : 0)) * int64_t(kQkWarps) + warp; unit < units; unit += r.stride[which]) {
-        const int64_t t = unit / slices;
+        for (int i = 0; i < 8; ++i) sum[i] = 0;
+    int64_t unit = (blockIdx.x - (which ? r.blocks_q : 0)) * int64_t(kQkWarps) + warp;
+    int next_pos = unit < units ? p.positions[unit / slices] : 0;
+    for (; unit < units; unit += r.stride[which]) {
+        const int64_t t = unit / slices, next = unit + r.stride[which];
         const int g0 = static_cast<int>(unit - t * slices) * run, g1 = min(g0 + run, per);
-        const int pos = p.positions[t];
-        const uint16_t* xs = side.x + t * side.x_token;
-        const uint16_t* ds = GRAD ? side.d_out + t * side.d_token : nullptr;
-        float c[8], s[8];
+        const int pos = next_pos;
+        if (next < units) next_pos = p.positions[next / slices];      // long before its cosines are asked for
+        const int first = g0 * heads_a_warp + of_head;
+        const uint16_t* xs = side.x + t * side.x_token + first * side.x_head;
+        const uint16_t* ds = GRAD ? side.d_out + t * side.d_token + first * side.d_head : nullptr;
+        uint16_t* os = side.out + t * side.out_token + first * side.out_head;
+        const int64_t x_step = heads_a_warp * side.x_head, d_step = GRAD ? heads_a_warp * side.d_head : 0;
+        const int64_t o_step = heads_a_warp * side.out_head;
+        int heads = side.heads - first;                   // from this lane's first on
+        Angles<PAIRED> angles;
         bool known = false, good = false;
         for (int g = g0; g < g1; g += BATCH) {
             uint4 xa[BATCH], xb[BATCH], da[GRAD ? BATCH : 1], db[GRAD ? BATCH : 1];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
-                const int head = (g + i) * HPW + lane / L;
-                const bool on = g + i < g1 && head < side.heads;
-                const uint16_t* x = xs + head * side.x_head;
-                xa[i] = ld_stream_u4_if(x + pl.a, on && pl.a >= 0);
-                xb[i] = ld_stream_u4_if(x + pl.b, on && pl.b >= 0);
+                const bool on = g + i < g1 && i * heads_a_warp < heads;
+                xa[i] = xb[i] = none;
+                if (on && has_a) xa[i] = ld_stream_u4(xs + i * x_step + pl.a);
+                if (on && has_b) xb[i] = ld_stream_u4(xs + i * x_step + pl.b);
                 if constexpr (GRAD) {
-                    const uint16_t* d = ds + head * side.d_head;
-                    da[i] = ld_stream_u4_if(d + pl.a, on && pl.a >= 0);
-                    db[i] = ld_stream_u4_if(d + pl.b, on && pl.b >= 0);
+                    da[i] = db[i] = none;
+                    if (on && has_a) da[i] = ld_stream_u4(ds + i * d_step + pl.a);
+                    if (on && has_b) db[i] = ld_stream_u4(ds + i * d_step + pl.b);
                 }
             }
             if (!known) {
@@ -169,69 +242,68 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? 2 : 3) qk_kernel(const Q
                 for (int i = 0; i < 2; ++i) {
                     const float4 a = on ? __ldg(row + i) : make_float4(1.f, 1.f, 1.f, 1.f);
                     const float4 b = on ? __ldg(row + p.rotary / 8 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    c[4 * i] = a.x; c[4 * i + 1] = a.y; c[4 * i + 2] = a.z; c[4 * i + 3] = a.w;
-                    s[4 * i] = b.x; s[4 * i + 1] = b.y; s[4 * i + 2] = b.z; s[4 * i + 3] = b.w;
+                    angles.set(2 * i, a.x, a.y, b.x, b.y);
+                    angles.set(2 * i + 1, a.z, a.w, b.z, b.w);
                 }
             }
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 if (g + i >= g1) break;
-                const int head = (g + i) * HPW + lane / L;
-                float x[16], gamma[16];
-                widen<F16>(gamma_a, gamma);
-                widen<F16>(gamma_b, gamma + 8);
+                f2 x[8], square = 0;
                 widen<F16>(xa[i], x);
-                widen<F16>(xb[i], x + 8);
-                float ss = 0.f;
+                widen<F16>(xb[i], x + 4);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-                const float inv = rsqrtf(fmaf(head_sum<L>(ss), per_element, p.eps));
+                for (int e = 0; e < 8; ++e) square = fma2(x[e], x[e], square);
+                const float inv = rsqrtf(fmaf(head_sum<L>(sum2(square), lanes, base), per_element, p.eps));
+                const f2 inv2 = both(inv);
                 if constexpr (!GRAD) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * gamma[e];
-                    if (pl.turns) turn<false, PAIRED>(x, c, s);
+                    for (int e = 0; e < 8; ++e) x[e] = mul2(mul2(x[e], inv2), gamma[e]);
+                    if (pl.turns) turn<false, PAIRED>(x, angles);
                 } else {
-                    float d[16];
+                    f2 d[8], dot2 = 0;
                     widen<F16>(da[i], d);
-                    widen<F16>(db[i], d + 8);
-                    if (pl.turns) turn<true, PAIRED>(d, c, s);
-                    float dot = 0.f;
+                    widen<F16>(db[i], d + 4);
+                    if (pl.turns) turn<true, PAIRED>(d, angles);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        x[e] *= inv;                                  // unit
-                        if (good) sum[e] = fmaf(d[e], x[e], sum[e]);
-                        d[e] *= gamma[e];
-                        dot = fmaf(d[e], x[e], dot);
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = mul2(x[e], inv2);                      // unit
+                        if (good) sum[e] = fma2(d[e], x[e], sum[e]);
+                        d[e] = mul2(d[e], gamma[e]);
+                        dot2 = fma2(d[e], x[e], dot2);
                     }
-                    const float mean = head_sum<L>(dot) * per_element;
+                    const f2 less = both(-(head_sum<L>(sum2(dot2), lanes, base) * per_element));
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = inv * (d[e] - x[e] * mean);
+                    for (int e = 0; e < 8; ++e) x[e] = mul2(inv2, fma2(x[e], less, d[e]));
                 }
-                if (good && head < side.heads) {
-                    uint16_t* o = side.out + t * side.out_token + head * side.out_head;
-                    if (pl.a >= 0) st_stream_u4(o + pl.a, narrow<F16>(x));
-                    if (pl.b >= 0) st_stream_u4(o + pl.b, narrow<F16>(x + 8));
+                if (good && i * heads_a_warp < heads) {
+                    if (has_a) st_stream_u4(os + i * o_step + pl.a, narrow<F16>(x));
+                    if (has_b) st_stream_u4(os + i * o_step + pl.b, narrow<F16>(x + 4));
                 }
             }
+            heads -= BATCH * heads_a_warp;
+            xs += BATCH * x_step;
+            os += BATCH * o_step;
+            if constexpr (GRAD) ds += BATCH * d_step;
         }
     }
     if constexpr (GRAD) {
-        // this warp's heads, then the CTA's warps, in a fixed order
+        // the CTA's warps' heads, in a fixed order
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-#pragma unroll
-            for (int off = L; off < 32; off <<= 1) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], off);
-            if (lane < L) s_gamma[warp][i * L + lane] = sum[i];
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = halves(sum[i]);
+            s_gamma[warp][(2 * i) * 32 + lane] = f.x;
+            s_gamma[warp][(2 * i + 1) * 32 + lane] = f.y;
         }
         __syncthreads();
-        for (int j = threadIdx.x; j < 16 * L; j += 32 * kQkWarps) {
-            const int i = j / L;
-            const Place q = place_of(j % L, p.D, p.rotary, PAIRED);
+        for (int j = threadIdx.x; j < 16 * lanes; j += 32 * kQkWarps) {
+            const int i = j / lanes, u = j % lanes;
+            const Place q = place_of(u, p.D, p.rotary, PAIRED);
             const int at = i < 8 ? q.a : q.b;
             if (at < 0) continue;
             float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kQkWarps; ++w) v += s_gamma[w][j];
+            for (int w = 0; w < kQkWarps; ++w)
+                for (int h = 0; h < heads_a_warp; ++h) v += s_gamma[w][i * 32 + h * lanes + u];
             p.partial[static_cast<int64_t>(blockIdx.x) * p.D + at + (i & 7)] = v;
         }
     }
@@ -246,13 +318,17 @@ __global__ void __launch_bounds__(32 * kSumWarps) qk_gamma_kernel(const QkParams
     pdl_wait();
     pdl_launch_dependents();
     const int first = which ? r.blocks_q : 0, last = which ? blocks : r.blocks_q;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};                // four rows in flight
+    float sum = 0.f;
     if (col < p.D)
-        for (int b = first + warp; b < last; b += 4 * kSumWarps)
+        for (int b = first + warp; b < last; b += 8 * kSumWarps) {
+            float v[8];                               // eight rows in flight
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (b + i * kSumWarps < last) v[i] += __ldcg(p.partial + static_cast<int64_t>(b + i * kSumWarps) * p.D + col);
-    s_sum[warp][lane] = (v[0] + v[1]) + (v[2] + v[3]);
+            for (int i = 0; i < 8; ++i)
+                v[i] = b + i * kSumWarps < last ? __ldcg(p.partial + static_cast<int64_t>(b + i * kSumWarps) * p.D + col) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += v[i];
+        }
+    s_sum[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && col < p.D) {
         float total = 0.f;
@@ -263,11 +339,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) qk_gamma_kernel(const QkParams
 
 using Kernel = void (*)(const QkParams, const QkRuns);
 
-int lanes_for(int D) {
-    int l = 1;
-    while (l * 16 < D) l *= 2;
-    return l;
-}
+int lanes_for(int D) { return (D + 15) / 16; }
 
 template <bool F16, bool GRAD, bool PAIRED>
 Kernel kernel_of(int D) {
@@ -277,7 +349,8 @@ Kernel kernel_of(int D) {
         case 4: return qk_kernel<F16, 4, GRAD, PAIRED>;
         case 8: return qk_kernel<F16, 8, GRAD, PAIRED>;
         case 16: return qk_kernel<F16, 16, GRAD, PAIRED>;
-        default: return qk_kernel<F16, 32, GRAD, PAIRED>;
+        case 32: return qk_kernel<F16, 32, GRAD, PAIRED>;
+        default: return qk_kernel<F16, 0, GRAD, PAIRED>;
     }
 }
 
@@ -293,8 +366,9 @@ Kernel kernel_for(const QkShape& s, bool grad) { return grad ? kernel_of<true>(s
 // SMs without work.  The gradient's warps stay for several units, two CTAs an SM, so
 // that there are few partial sums of d_gamma.
 QkRuns runs_for(const QkShape& s, int64_t T, bool grad, int sms, int* blocks) {
-    const int hpw = 32 / lanes_for(s.D), heads[2] = {s.heads_q, s.heads_k};
     QkRuns r;
+    r.lanes = lanes_for(s.D);
+    const int hpw = 32 / r.lanes, heads[2] = {s.heads_q, s.heads_k};
     int64_t units[2];
     for (int i = 0; i < 2; ++i) {
         const int per = (heads[i] + hpw - 1) / hpw;
@@ -305,13 +379,15 @@ QkRuns runs_for(const QkShape& s, int64_t T, bool grad, int sms, int* blocks) {
         r.slices[i] = (per + run - 1) / run;
         units[i] = T * r.slices[i];
     }
-    const int64_t all = units[0] * r.run[0] + units[1] * r.run[1], most = static_cast<int64_t>(sms) * 2;
+    // a unit's work: its groups, and about two more for its first loads, which nothing covers
+    const int64_t work[2] = {units[0] * (r.run[0] + 2), units[1] * (r.run[1] + 2)};
+    const int64_t all = work[0] + work[1], most = static_cast<int64_t>(sms) * 2;
     int64_t b[2];
     for (int i = 0; i < 2; ++i) {
         b[i] = (units[i] + kQkWarps - 1) / kQkWarps;
         if (grad && all > 0) {
             // shares of the CTAs in the proportion of the work
-            int64_t share = most * (units[i] * r.run[i]) / all;
+            int64_t share = most * work[i] / all;
             if (share < 1) share = 1;
             if (b[i] > share) b[i] = share;
         }

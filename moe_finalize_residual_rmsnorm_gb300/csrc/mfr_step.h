@@ -51,6 +51,7 @@ struct MoeParams {
     int entries;
     int stages;
     int sentinel;
+    long long wait_limit;     // cycles after which a wait gives up: kWaitCycles, or less to test that
 };
 
 // Fills the launch geometry and the workspace's layout from T .. fp8.
@@ -87,7 +88,7 @@ struct GateParams {
 };
 
 cudaError_t gate_prepare(int E, int b16);
-cudaError_t gate_launch(const GateParams& p, int b16, bool grad, int pdl, cudaStream_t s);
+cudaError_t gate_launch(const GateParams& p, int b16, bool grad, int sms, int pdl, cudaStream_t s);
 
 // ---- norms of query and key heads with the rotation (mfr_qk_norm.cu) -----------------------
 struct QkShape {

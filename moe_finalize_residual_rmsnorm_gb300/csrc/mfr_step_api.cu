@@ -115,6 +115,7 @@ int moe_small_layer_plan(moe_op_t* op, int64_t T, int64_t H, int64_t I, int E, i
     p->H = H;
     p->k = k;
     p->E = E;
+    p->wait_limit = kWaitCycles;
     if (T == 0) return MFR_OK;
     MoeLayerShape& s = p->layer;
     s.T = static_cast<int>(T);
@@ -126,6 +127,15 @@ int moe_small_layer_plan(moe_op_t* op, int64_t T, int64_t H, int64_t I, int E, i
     moe_layer_choose(s, p->sms);
     p->workspace = s.bytes;
     return prepared(op, moe_layer_encoder() ? moe_layer_prepare(s) : cudaErrorNotSupported);
+}
+
+int moe_small_layer_set_wait_limit(moe_op_t op, int64_t limit_cycles) {
+    const int rc = check_op(op, kMoeLayer);
+    if (rc != MFR_OK) return rc;
+    if (limit_cycles < 0 || limit_cycles > kWaitCycles)
+        return MFR_FAIL(MFR_ERR_INVALID_ARG, "limit_cycles must be in [0, %lld] (got %lld)", kWaitCycles, (long long)limit_cycles);
+    op->wait_limit = limit_cycles;
+    return MFR_OK;
 }
 
 int moe_small_layer_run(moe_op_t op, const void* x, const float* x_sf, const int32_t* expert_ids,
@@ -169,6 +179,7 @@ int moe_small_layer_run(moe_op_t op, const void* x, const float* x_sf, const int
     p.entries = s.entries;
     p.stages = s.stages;
     p.sentinel = op->opt.sentinel_skip ? 1 : 0;
+    p.wait_limit = op->wait_limit;
     const DebugTurn turn(op->status, op->opt.debug_checks != 0);
     return finish(op, moe_layer_launch(s, p, x, w13, w2, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
@@ -227,7 +238,7 @@ int moe_gate_run(moe_op_t op, const void* logits, const float* bias, int32_t* ex
     p.ids = expert_ids;
     p.w = topk_weights;
     const DebugTurn turn(op->status, op->opt.debug_checks != 0);
-    return finish(op, gate_launch(p, op->gate.b16, false, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
+    return finish(op, gate_launch(p, op->gate.b16, false, op->sms, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
 int moe_gate_grad_run(moe_op_t op, const float* d_topk_weights, const void* logits, const int32_t* expert_ids, void* d_logits,
@@ -249,7 +260,7 @@ int moe_gate_grad_run(moe_op_t op, const float* d_topk_weights, const void* logi
     p.d_w = d_topk_weights;
     p.d_logits = d_logits;
     const DebugTurn turn(op->status, op->opt.debug_checks != 0);
-    return finish(op, gate_launch(p, op->gate.b16, true, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
+    return finish(op, gate_launch(p, op->gate.b16, true, op->sms, op->opt.enable_pdl ? 1 : 0, static_cast<cudaStream_t>(stream)), stream);
 }
 
 // ---- norms of query and key heads with the rotation -----------------------------------------

@@ -258,6 +258,33 @@ def test_the_c_side_refuses():
     assert plan.get_status() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 128, 128, 1, 1), (3, 4096, 256, 8, 4), (130, 1040, 384, 5, 3)])
+def test_waits_that_run_out_end_and_report_it(T, H, I, E, k, fp8):
+    """With a limit of nothing the first stage's wait gives up: the run ends, says so, and the
+    plan's next run with the usual limit is as if nothing had been."""
+    layer, i = Layer(T, H, I, E, k, fp8), inputs(T, H, I, E, k, fp8)
+    layer.run(i)
+    layer.check(i)
+    want = layer.out.t.clone()
+    for limit in (0, 100, 0, 3000):
+        layer.plan.set_wait_limit(limit)
+        layer.run(i)
+        torch.cuda.synchronize()
+        st = layer.plan.get_status()
+        assert st == mfr.STATUS_TIMEOUT or (limit > 0 and st == 0 and torch.equal(layer.out.t, want))
+        layer.ws.check()
+        layer.out.check()
+        layer.plan.set_wait_limit(4_000_000_000)
+        layer.run(i)
+        torch.cuda.synchronize()
+        assert layer.plan.get_status() == 0 and torch.equal(layer.out.check(), want)
+    with pytest.raises(mfr.MFRError):
+        layer.plan.set_wait_limit(-1)
+    with pytest.raises(mfr.MFRError):
+        layer.plan.set_wait_limit(4_000_000_001)
+
+
 def test_many_calls_without_a_wait_that_runs_out():
     for T, H, I, E, k in [(1, 2048, 1024, 8, 4), (130, 256, 128, 3, 2), (16, 520, 520, 32, 8)]:
         layer, i = Layer(T, H, I, E, k), inputs(T, H, I, E, k)

@@ -198,6 +198,28 @@ def test_a_layer_for_bf16_takes_no_scales():
         plan.run(**args, w2_sf=_z(8, 2, 1))
 
 
+def test_clip_refuses_each_wrong_tensor():
+    plan = _plan(mfr.GradClipPlan, numels=[5, 8], dtypes=[F32, B16], _need=8, _pointers=ctypes.c_void_p * 2)
+    good = [_z(5), _z(8, dtype=B16)]
+    args = dict(max_norm=1.0, norm=_z(1), workspace=_z(8, dtype=torch.uint8))
+    for name in ("grads", "out"):
+        for i, wrong in ((0, _z(4)), (0, _z(5, dtype=B16)), (1, 5), (1, None), (1, _z(16, dtype=B16)[::2])):
+            bad = list(good)
+            bad[i] = wrong
+            with pytest.raises(ValueError, match=rf"{name}\[{i}\]"):
+                plan.run(**{"grads": good, **args, name: bad})
+        with pytest.raises(ValueError, match=name):
+            plan.run(**{"grads": good, **args, name: good[:1]})
+    for name, wrong in (("norm", _z(2)), ("norm", _z(1, dtype=B16)), ("workspace", _z(7, dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="norm|workspace"):
+            plan.run(good, **{**args, name: wrong})
+    with pytest.raises(AssertionError, match="reached"):
+        plan.run(good, **args, stream=0)
+    plan.device = torch.device("cuda", 0)
+    with pytest.raises(ValueError, match="device"):
+        plan.run(good, **args, stream=0)
+
+
 def test_a_bias_needs_sigmoid_scores():
     plan, args, _ = _gate(False)
     plan.score = mfr.SCORE_SOFTMAX
