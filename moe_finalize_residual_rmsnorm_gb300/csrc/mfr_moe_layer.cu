@@ -25,12 +25,21 @@
 //                  before it waits for the first launch
 //   then the pairs of every token are added in slot order, by a small third launch:
 //                  no atomics, the same bits in every call
+// Measured on GB300 (4096 x 1024 weights an expert, bf16, copy rate 6782 GB/s): 16 tokens
+// of 128 experts 309 us (0.99 of the copy rate), 64 of 64 experts 248 us (0.96), one
+// token of 64 experts 39 us (0.75: two launches' starts, sorts and first loads, 10 us); 128
+// tokens of 64 experts of 8192 x 1024 in E4M3 278 us (0.86: 512 units are 3.4 turns of the
+// SMs).  With units for few SMs one SM takes 60-70 GB/s: a stage's eight products are
+// 330 cycles whatever their columns (the weights are read from shared memory for each), and
+// hand-overs 200 more.
 // Not taken: dividing the steps along K evenly over the CTAs, with partial sums put
 // together by the last to arrive (every piece's end is a fence, an atomic and a round
 // trip: one token 54 us that way and 42 this, 37 tokens 85 and 51, 128 in E4M3 378 and
 // 289); adding the pairs in the second launch by the last CTA of a tile (128 tokens: 50
 // us at its end); two CTAs an SM, so that the launches overlap (half the ring each: one
-// token 52 us); fetching w2 to L2 at the first launch's end (no difference).
+// token 52 us); fetching w2 to L2 at the first launch's end (no difference); units of 32
+// or 64 columns of h and 128 rows of D, in E4M3 with clusters that share a group's
+// largest magnitude (25 shapes 5 % slower: more copies, and in E4M3 more steps, a byte).
 //
 // bf16: h is kept as the sum of two bf16 values (16 bits of it), two products of the
 // same weights, which cost nothing where bytes bound it; rounded once it alone would
@@ -68,12 +77,18 @@ constexpr int accumulators() { return FP8 || DOWN ? 2 : 1; }
 template <bool FP8, bool DOWN, int NB>
 constexpr bool stacked() { return DOWN && !FP8 && NB <= 64; }
 
-// Columns of an accumulator, and of two units' accumulators.
+// Accumulators in turn: two units', in E4M3 four steps' where tensor memory holds them
+// (128 tokens of 64 experts 287 -> 278 us).
+constexpr int kMaxTurns = 4;
+template <bool FP8, int NB>
+constexpr int turns() { return FP8 && NB <= 64 ? 4 : 2; }
+
+// Columns of an accumulator, and of all.
 template <bool FP8, bool DOWN, int NB>
 constexpr int columns() { return stacked<FP8, DOWN, NB>() ? 2 * NB : NB; }
 template <bool FP8, bool DOWN, int NB>
 constexpr uint32_t tmem_columns() {
-    constexpr int n = 2 * accumulators<FP8, DOWN>() * columns<FP8, DOWN, NB>();
+    constexpr int n = turns<FP8, NB>() * accumulators<FP8, DOWN>() * columns<FP8, DOWN, NB>();
     return n < 32 ? 32 : n;
 }
 
@@ -81,7 +96,7 @@ constexpr uint32_t tmem_columns() {
 template <int NB>
 struct Shared {
     uint64_t full[kRingStages], empty[kRingStages];
-    uint64_t done[2], taken[2];       // an accumulator is complete; its values are in registers
+    uint64_t done[kMaxTurns], taken[kMaxTurns];       // an accumulator is complete; its values are in registers
     uint64_t drain;
     uint32_t tmem;
     int dead;                         // a wait ran out: every role leaves
@@ -142,7 +157,8 @@ __device__ __forceinline__ bool valid_expert(int id, int E) { return static_cast
 
 // Stable counting sort of the pairs by expert, the same in every CTA: `list` gets
 // the pairs, `entries` the chunks of at most NB of them; returns their number.
-// `hist`: [kWarps + 1][E], and the ids behind it.  All threads call it.
+// `hist`: [kWarps + 1][E], and behind it the pairs' ids and their places among their
+// warp's pairs of the same expert.  All threads call it.
 template <int NB>
 __device__ int sort_pairs(const MoeParams& p, Shared<NB>* s, uint16_t* list, uint32_t* entries, int* hist, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -150,6 +166,7 @@ __device__ int sort_pairs(const MoeParams& p, Shared<NB>* s, uint16_t* list, uin
     const int seg = ((P + kWarps - 1) / kWarps + 31) & ~31, first = warp * seg, last = min(P, first + seg);
     const int warps = (P + seg - 1) / seg;            // that have pairs
     int* ids = hist + (kWarps + 1) * E;
+    uint16_t* place = reinterpret_cast<uint16_t*>(ids + P);
     for (int i = tid; i < P; i += kMoeThreads) ids[i] = __ldg(p.ids + i);
     for (int i = tid; i < warps * E; i += kMoeThreads) hist[i] = 0;
     __syncthreads();
@@ -157,11 +174,11 @@ __device__ int sort_pairs(const MoeParams& p, Shared<NB>* s, uint16_t* list, uin
     for (int i0 = first; i0 < last; i0 += 32) {
         const int i = i0 + lane, e = i < last ? ids[i] : -1;
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        if (valid_expert(e, E)) {
-            if (lane == __ffs(same) - 1) hist[warp * E + e] += __popc(same);
-        } else {
-            bad |= i < last && !(p.sentinel && e < 0);
-        }
+        const bool ok = valid_expert(e, E);
+        if (ok) place[i] = static_cast<uint16_t>(hist[warp * E + e] + __popc(same & ((1u << lane) - 1)));
+        else bad |= i < last && !(p.sentinel && e < 0);
+        __syncwarp();
+        if (ok && lane == __ffs(same) - 1) hist[warp * E + e] += __popc(same);
         __syncwarp();
     }
     if (report && bad) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
@@ -201,15 +218,8 @@ __device__ int sort_pairs(const MoeParams& p, Shared<NB>* s, uint16_t* list, uin
         at += n;
     }
     __syncthreads();
-    for (int i0 = first; i0 < last; i0 += 32) {
-        const int i = i0 + lane, e = i < last ? ids[i] : -1;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        const bool ok = valid_expert(e, E);
-        if (ok) list[hist[warp * E + e] + __popc(same & ((1u << lane) - 1))] = static_cast<uint16_t>(i);
-        __syncwarp();
-        if (ok && lane == __ffs(same) - 1) hist[warp * E + e] += __popc(same);
-        __syncwarp();
-    }
+    for (int i = first + lane; i < last; i += 32)
+        if (valid_expert(ids[i], E)) list[hist[warp * E + ids[i]] + place[i]] = static_cast<uint16_t>(i);
     return static_cast<int>(all >> 16);               // the caller's barrier ends it
 }
 
@@ -227,6 +237,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
     constexpr int COLS = columns<FP8, DOWN, NB>();   // of an accumulator
     constexpr int ACC = accumulators<FP8, DOWN>() * COLS;
     constexpr int STAGE = stage_bytes<FP8, NB>();
+    constexpr int TURNS = turns<FP8, NB>();
     constexpr int ROWS = GATES ? kMoeRows / 2 : DOWN ? 2 * kMoeRows : kMoeRows;     // of a tile
     extern __shared__ unsigned char raw[];
     const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
@@ -243,7 +254,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             mbar_init(smem_addr(&s->full[i]), 2);
             mbar_init(smem_addr(&s->empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kMaxTurns; ++i) {
             mbar_init(smem_addr(&s->done[i]), 1);
             mbar_init(smem_addr(&s->taken[i]), kFinishWarps);
         }
@@ -347,15 +358,15 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             const int n = (unpack_entry(entries[u % M]).n + 15) & ~15;
             const uint32_t desc = mma_desc(FP8, STACKED ? 2 * n : n);
             for (int kb = 0; kb < KB; ++kb) {
-                if ((FP8 || kb == 0) && uses > 1)
-                    ok = role_wait(&s->dead, p, smem_addr(&s->taken[uses & 1]), ((uses >> 1) - 1) & 1);
-                ok = ok && role_wait(&s->dead, p, smem_addr(&s->full[st]), parity);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                // the stage is full, and (lane 1) the accumulator's values are in registers
+                const bool again = lane == 1 && (FP8 || kb == 0) && uses >= TURNS;
+                ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p, again ? smem_addr(&s->taken[uses % TURNS]) : smem_addr(&s->full[st]),
+                                                       again ? (uses / TURNS - 1) & 1 : parity));
                 if (!ok) break;
                 tcgen05_fence_after();
                 const bool last = FP8 || kb == KB - 1;
                 if (elect_lane()) {
-                    const uint32_t a = ring + st * STAGE, d = tmem + (uses & 1) * ACC;
+                    const uint32_t a = ring + st * STAGE, d = tmem + uses % TURNS * ACC;
                     const uint64_t da = operand_desc(a), db = operand_desc(a + 2 * kPanel);
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
@@ -368,7 +379,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                                 mma_issue<FP8>(d + half * COLS, from, db + (NB * 128 >> 4) + i * 2, desc, true);
                         }
                     mma_commit(smem_addr(&s->empty[st]));
-                    if (last) mma_commit(smem_addr(&s->done[uses & 1]));
+                    if (last) mma_commit(smem_addr(&s->done[uses % TURNS]));
                 }
                 __syncwarp();
                 if (last) ++uses;
@@ -455,11 +466,11 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         if (HALF > 32) sx[lane + 32] = f1[step];
                         __syncwarp();
                         const float a0 = sw0[step], a1 = sw1[step];
-                        ok = role_wait(&s->dead, p, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
+                        ok = role_wait(&s->dead, p, smem_addr(&s->done[uses % TURNS]), uses / TURNS & 1);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         tcgen05_fence_after();
-                        const uint32_t acc = lanes + (uses & 1) * ACC;
+                        const uint32_t acc = lanes + uses % TURNS * ACC;
 #pragma unroll
                         for (int q = 0; q < NB / 16; ++q) {
                             if (q >= groups) break;
@@ -476,7 +487,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         }
                         tcgen05_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses & 1]));
+                        if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses % TURNS]));
                         ++uses;
                     }
                 }
@@ -512,11 +523,11 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     }
                 }
             } else {
-                ok = role_wait(&s->dead, p, smem_addr(&s->done[uses & 1]), (uses >> 1) & 1);
+                ok = role_wait(&s->dead, p, smem_addr(&s->done[uses % TURNS]), uses / TURNS & 1);
                 ok = finishers_well(ok);
                 if (!ok) break;
                 tcgen05_fence_after();
-                const uint32_t acc = lanes + (uses & 1) * ACC;
+                const uint32_t acc = lanes + uses % TURNS * ACC;
 #pragma unroll 1
                 for (int q = 0; q < groups; ++q) {
                     const int c0 = q * 16 + side * 8;
@@ -569,7 +580,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                 }
                 tcgen05_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses & 1]));
+                if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses % TURNS]));
                 ++uses;
             }
         }
