@@ -40,7 +40,7 @@ extern "C" {
  * sentinel_skip.  +infinity counts as the largest FP32 value.  The choice is that
  * of exact keys: FP32 ones that lie too close are compared in 64 bits.
  *  bf16_logits   0: logits FP32 [T, E]; 1: bf16
- *  bias          FP32 [E], finite or -infinity, MFR_SCORE_SIGMOID only; or NULL
+ *  bias          FP32 [E], MFR_SCORE_SIGMOID only; or NULL
  *  expert_ids    int32 [T, k];  topk_weights FP32 [T, k]
  * Needs 1 <= k <= 16, k <= E <= 1024, scale finite and > 0.  logits 16-byte aligned,
  * the others 4-byte.  Outputs overlap nothing. */

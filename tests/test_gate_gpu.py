@@ -92,6 +92,19 @@ def test_masked_experts(E, k, score, renorm):
         check(logits, k, 1, renorm, bias=torch.where(torch.arange(E, device="cuda") == 3, -INF, 0.1).float())
 
 
+@pytest.mark.parametrize("E", [40, 200])
+@pytest.mark.parametrize("many", [2, 4, 9, 36])
+def test_biases_that_are_not_finite(E, many):
+    """Infinite ones come first, the lower index before the higher; an expert with a NaN is not chosen."""
+    bias = randn((E,), 11, F32)
+    bias[E - many:] = INF
+    bias[1] = NAN
+    for k in (4, 16):
+        _, ids, _ = check(randn((9, E), 12, F32), k, 1, True, bias=bias)
+        n = min(k, many)
+        assert ids[:, :n].tolist() == [list(range(E - many, E - many + n))] * 9 and not (ids == 1).any()
+
+
 def test_infinity_counts_as_the_largest_value():
     logits = randn((2, 64), 10, F32)
     logits[0, 5] = INF
