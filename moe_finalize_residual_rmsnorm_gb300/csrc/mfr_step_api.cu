@@ -44,6 +44,9 @@ int check_heads(const Heads& a, int64_t T, int D, bool output) {
     const int64_t most = int64_t(1) << 40;
     if (a.h->token_stride < 0 || a.h->head_stride < 0 || a.h->token_stride > most || a.h->head_stride > most)
         return MFR_FAIL(MFR_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40]", a.name);
+    // no address space holds more, and the extents below stay within 64 bits
+    if (T > 1 && a.h->token_stride > (int64_t(1) << 56) / T)
+        return MFR_FAIL(MFR_ERR_INVALID_ARG, "%s: its tokens span more than 2^56 elements", a.name);
     // heads within a token, or tokens within a head's row
     const bool apart = (a.heads == 1 || a.h->head_stride >= D) && (T == 1 || a.h->token_stride >= row_extent(a, D));
     const bool across = (T == 1 || a.h->token_stride >= D) && (a.heads == 1 || a.h->head_stride >= (T - 1) * a.h->token_stride + D);

@@ -278,3 +278,8 @@ def test_refusals():
     torch.cuda.synchronize()
     with pytest.raises(ValueError, match="lie together"):
         plan.run(c.q.transpose(1, 2).contiguous().transpose(1, 2), c.k, c.gq, c.gk, EPS, c.table, c.pos, qo, ko)
+    # tokens that span more than there are addresses
+    large = mfr.QkNormRopePlan(1 << 26, hq, hk, D, max_positions=c.table.shape[0])
+    far = heads(c.q, token=1 << 40)
+    assert lib.moe_qk_norm_rope_run(large._h, far, far, c.gq.data_ptr(), c.gk.data_ptr(), EPS, c.table.data_ptr(), c.pos.data_ptr(),
+                                    far, far, torch.cuda.current_stream().cuda_stream) == 1
