@@ -152,8 +152,8 @@ int moe_qk_norm_rope_grad_run(moe_op_t op, const moe_heads_t* d_q_out, const moe
  *             to its element, fastest where in[i] and out[i] lie alike towards 16
  *             bytes; NULL where numel[i] is 0
  *  workspace  moe_op_workspace_bytes(op) bytes, 16-byte aligned
- * 0 <= n <= 65536, numel[i] < 2^40.  Outputs overlap nothing but their own input (the
- * call checks each against its own input only). */
+ * 0 <= n <= 65536, numel[i] < 2^40.  Outputs overlap nothing but their own input, which
+ * is then the same tensor: the same tensor twice in place is refused. */
 #define MFR_GRAD_F32  0
 #define MFR_GRAD_BF16 1
 #define MFR_GRAD_F16  2

@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/moe_step_ops.h: argument checks,
 // launch geometry.
+#include <algorithm>
 #include <cstdlib>
 
 #include "moe_step_ops.h"
@@ -93,6 +94,25 @@ int check_qk(const QkShape& s, const void* gamma_q, const void* gamma_k, float e
     if (!aligned(gamma_q, 16) || !aligned(gamma_k, 16) || !aligned(cos_sin, 16) || !aligned(positions, 4))
         return MFR_FAIL(MFR_ERR_MISALIGNED, "gammas and cos_sin must be 16-byte aligned, positions 4-byte");
     return MFR_OK;
+}
+
+// The bytes of a tensor of moe_grad_clip_run.
+struct Extent {
+    uintptr_t from, to;
+    bool written;
+};
+
+// Whether a written one shares a byte with any other; sorts them.
+bool written_meet(Extent* e, int n) {
+    const auto before = [](const Extent& a, const Extent& b) { return a.from < b.from; };
+    if (!std::is_sorted(e, e + n, before)) std::sort(e, e + n, before);
+    uintptr_t read = 0, written = 0;          // how far those before reach
+    for (int i = 0; i < n; ++i) {
+        if (e[i].from < written || (e[i].written && e[i].from < read)) return true;
+        uintptr_t& end = e[i].written ? written : read;
+        end = std::max(end, e[i].to);
+    }
+    return false;
 }
 
 }  // namespace
@@ -417,16 +437,33 @@ int moe_grad_clip_run(moe_op_t op, const void* const* in, void* const* out, floa
     if (!aligned(norm, 4)) return MFR_FAIL(MFR_ERR_MISALIGNED, "norm must be 4-byte aligned");
     if ((rc = check_workspace(op, workspace, workspace_bytes)) != MFR_OK) return rc;
     const Span mine[] = {{norm, 4}, {workspace, op->workspace}};
-    if (meet(mine[0], mine[1])) return MFR_FAIL(MFR_ERR_INVALID_ARG, "norm lies in the workspace");
-    for (int i = 0; i < s.n; ++i) {
+    // room for a few on the stack
+    Extent few[2 * kClipFew + 2], *e = few;
+    if (s.n > kClipFew && !(e = static_cast<Extent*>(std::malloc(sizeof(Extent) * (2 * static_cast<size_t>(s.n) + 2)))))
+        return MFR_FAIL(MFR_ERR_CUDA, "out of host memory");
+    int count = 0;
+    const auto add = [&](const void* p, int64_t bytes, bool written) {
+        const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+        e[count++] = {from, from + static_cast<uintptr_t>(bytes), written};
+    };
+    rc = MFR_OK;
+    for (int i = 0; i < s.n && rc == MFR_OK; ++i) {
         if (s.numel[i] == 0) continue;
         const int size = s.type[i] == MFR_GRAD_F32 ? 4 : 2;
-        if (!in[i] || !out[i]) return MFR_FAIL(MFR_ERR_INVALID_ARG, "tensor %d is NULL", i);
-        if (!aligned(in[i], size) || !aligned(out[i], size)) return MFR_FAIL(MFR_ERR_MISALIGNED, "tensor %d is not aligned to its element", i);
-        const Span a{in[i], s.numel[i] * size}, b{out[i], s.numel[i] * size};
-        if ((in[i] != out[i] && meet(a, b)) || meet(mine[0], a) || meet(mine[0], b) || meet(mine[1], a) || meet(mine[1], b))
-            return MFR_FAIL(MFR_ERR_INVALID_ARG, "tensor %d overlaps its output, norm or the workspace", i);
+        if (!in[i] || !out[i]) {
+            rc = MFR_FAIL(MFR_ERR_INVALID_ARG, "tensor %d is NULL", i);
+        } else if (!aligned(in[i], size) || !aligned(out[i], size)) {
+            rc = MFR_FAIL(MFR_ERR_MISALIGNED, "tensor %d is not aligned to its element", i);
+        } else {
+            add(out[i], s.numel[i] * size, true);
+            if (in[i] != out[i]) add(in[i], s.numel[i] * size, false);
+        }
     }
+    for (const Span& m : mine) add(m.p, m.bytes, true);
+    if (rc == MFR_OK && written_meet(e, count))
+        rc = MFR_FAIL(MFR_ERR_INVALID_ARG, "an output, norm or the workspace overlaps another argument");
+    if (e != few) std::free(e);
+    if (rc != MFR_OK) return rc;
     if ((rc = check_place(op, stream)) != MFR_OK) return rc;
     ClipParams p{};
     p.partial = static_cast<double*>(workspace);

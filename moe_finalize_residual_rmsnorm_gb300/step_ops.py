@@ -5,6 +5,7 @@ Argument marshalling only, with the checks and the conventions of layer_ops.py.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Optional
 
 import torch
@@ -183,17 +184,16 @@ class GradClipPlan(_OpPlan):
         self._make("moe_grad_clip_plan", n, (ctypes.c_int64 * n)(*self.numels),
                    (ctypes.c_int * n)(*[_GRAD_TYPES[d] for d in self.dtypes]), enable_pdl=enable_pdl,
                    debug_checks=debug_checks)
-        self._pointers = ctypes.c_void_p * n
         self._need = self.workspace_bytes()
 
-    def _addresses(self, name: str, tensors):
+    def _addresses(self, name: str, tensors) -> array:
         if len(tensors) != len(self.numels):
             raise ValueError(f"{name}: expected {len(self.numels)} tensors, got {len(tensors)}")
         T, dev = torch.Tensor, self.device
         try:        # all at once: a quarter of the time of looking at them one by one
             if list(map(T.numel, tensors)) == self.numels and [t.dtype for t in tensors] == self.dtypes and \
                     all(map(T.is_contiguous, tensors)) and {*map(T.get_device, tensors)} <= {-1 if dev.index is None else dev.index}:
-                return self._pointers(*map(T.data_ptr, tensors))
+                return array("Q", map(T.data_ptr, tensors))
         except TypeError:
             pass    # one of them is no tensor
         for i, (t, n, dt) in enumerate(zip(tensors, self.numels, self.dtypes)):
@@ -210,5 +210,6 @@ class GradClipPlan(_OpPlan):
         src = self._addresses("grads", grads)
         dst = src if out is None else self._addresses("out", out)
         ws, ws_bytes = _workspace(workspace, self._need, dev)
-        _check(self._lib.moe_grad_clip_run(self._h, src, dst, max_norm, eps, _tensor("norm", norm, torch.float32, (1,), dev),
-                                           ws, ws_bytes, self._stream(stream)), "moe_grad_clip_run")
+        _check(self._lib.moe_grad_clip_run(self._h, src.buffer_info()[0], dst.buffer_info()[0], max_norm, eps,
+                                           _tensor("norm", norm, torch.float32, (1,), dev), ws, ws_bytes,
+                                           self._stream(stream)), "moe_grad_clip_run")

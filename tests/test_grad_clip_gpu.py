@@ -191,3 +191,20 @@ def test_refusals():
         plan.run([grads[0], grads[0]], 1.0, norm, ws)
     with pytest.raises(ValueError, match=r"out\[0\]"):
         plan.run(grads, 1.0, norm, ws, [grads[0].cpu(), grads[1]])
+
+
+@pytest.mark.parametrize("n", [3, 100])
+def test_tensors_that_meet_are_refused(n):
+    """The same tensor twice, or an output on another one's input, is a race; inputs may meet."""
+    flat = torch.ones(n * 64 + 64, device="cuda")
+    grads = [flat[i * 64:(i + 1) * 64] for i in range(n)]
+    plan, ws, norm = plan_for(grads)
+    plan.run(grads, 1.0, norm, ws)                                       # neighbours
+    plan.run(grads[::-1], 1.0, norm, ws)
+    others = [torch.zeros(64, device="cuda") for _ in range(n)]
+    plan.run([grads[0]] * n, 1.0, norm, ws, others)                      # an input n times
+    for src, dst in ((grads[:-1] + [grads[0]], None), (grads[:-1] + [flat[32:96]], None),
+                     (grads, others[:-1] + [others[0]]), (grads, [others[0], grads[0]] + others[2:])):
+        with pytest.raises(mfr.MFRError, match="overlaps"):
+            plan.run(src, 1.0, norm, ws, dst)
+    torch.cuda.synchronize()
