@@ -16,7 +16,8 @@
 // unit while the next one is multiplied.
 //
 // Each CTA sorts the pairs by expert itself (at most 4096, from L2), so that no
-// launch before it is needed.  A unit is (tile of weight rows, chunk of an expert's
+// launch before it is needed; up to 32 of them are one warp's, which asks for its first
+// weights before the others are ready (5 tokens of 384 x 368: 11.7 -> 10.9 us).  A unit is (tile of weight rows, chunk of an expert's
 // pairs) over all of K, in turns over persistent CTAs; chunks of one expert are
 // neighbours, so that its weights come from DRAM once.
 //   first launch:  64 rows of G and the same 64 of U (E4M3: 128 and 128, a group of
@@ -27,8 +28,8 @@
 //                  no atomics, the same bits in every call
 // Measured on GB300 (4096 x 1024 weights an expert, bf16, copy rate 6782 GB/s): 16 tokens
 // of 128 experts 309 us (0.99 of the copy rate), 64 of 64 experts 248 us (0.96), one
-// token of 64 experts 39 us (0.75: two launches' starts, sorts and first loads, 10 us); 128
-// tokens of 64 experts of 8192 x 1024 in E4M3 278 us (0.86: 512 units are 3.4 turns of the
+// token of 64 experts 38 us (0.78: two launches' starts, sorts and first loads, 8 us); 128
+// tokens of 64 experts of 8192 x 1024 in E4M3 273 us (0.87: 512 units are 3.4 turns of the
 // SMs).  With units for few SMs one SM takes 60-70 GB/s: a stage's eight products are
 // 330 cycles whatever their columns (the weights are read from shared memory for each), and
 // hand-overs 200 more.
@@ -47,6 +48,7 @@
 // E4M3: products of 128 columns of K are one accumulation in tensor memory, which
 // the finishing warps scale and add in FP32 registers.
 #include <cfloat>
+#include <climits>
 #include <mutex>
 
 #include "moe_step_ops.h"
@@ -112,6 +114,7 @@ struct Shared {
 };
 
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void shared_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void group_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
@@ -223,6 +226,32 @@ __device__ int sort_pairs(const MoeParams& p, Shared<NB>* s, uint16_t* list, uin
     return static_cast<int>(all >> 16);               // the caller's barrier ends it
 }
 
+// The same for at most 32 pairs by one warp, which needs no other.
+template <int NB>
+__device__ __forceinline__ int sort_few(const MoeParams& p, uint16_t* list, uint32_t* entries, bool report) {
+    const int lane = threadIdx.x & 31, P = p.T * p.k;
+    const int id = lane < P ? __ldg(p.ids + lane) : -1;
+    const bool ok = valid_expert(id, p.E);
+    if (report && lane < P && !ok && !(p.sentinel && id < 0)) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
+    const int key = ok ? id : kMaxExperts;            // pairs without an expert come last
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, key);
+    const int before = __popc(same & ((1u << lane) - 1)), total = __popc(same);
+    const bool leads = ok && before % NB == 0;        // a chunk
+    const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+    int rank = 0, chunk = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const int other = __shfl_sync(0xFFFFFFFFu, key, j);
+        const bool first = other < key || (other == key && j < lane);
+        rank += first;
+        chunk += first && (leaders >> j & 1u);
+    }
+    if (ok) list[rank] = static_cast<uint16_t>(lane);
+    if (leads) entries[chunk] = pack_entry(id, rank, min(NB, total - before));
+    __syncwarp();
+    return __popc(leaders);
+}
+
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
 // One launch of products.  DOWN: the second one.
@@ -272,47 +301,70 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
         pdl_wait();
         pdl_launch_dependents();
     }
-    const int M = sort_pairs<NB>(p, s, list, entries, hist, !DOWN && blockIdx.x == 0);
-    proxy_fence();                    // the ring's memory held the counts
-    tcgen05_fence_before();
-    __syncthreads();
-    tcgen05_fence_after();
-    const uint32_t tmem = s->tmem;
-
     const int H = p.H, I = p.I, K = DOWN ? I : H, P = p.T * p.k;
     const int KB = (K + KS - 1) / KS;                // stages of a unit
-    const int units = M * (((DOWN ? H : I) + ROWS - 1) / ROWS);
     const int G = gridDim.x;
 
-    if (warp == 0) {                  // the weights
-        bool ok = true;
-        int i = 0, st = 0, parity = 1;
-        for (int u = blockIdx.x; ok && u < units; u += G) {
-            const int tile = u / M, expert = unpack_entry(entries[u - tile * M]).expert;
+    // The weights: stages up to number `until`, from where the last call ended.
+    struct {
+        int u, kb, i, st, parity;
+        bool ok;
+    } feed{static_cast<int>(blockIdx.x), 0, 0, 0, 1, true};
+    auto load_weights = [&](int M, int units, int until) {
+        for (; feed.u < units; feed.u += G) {
+            const int tile = feed.u / M, expert = unpack_entry(entries[feed.u - tile * M]).expert;
             const int c1a = tile * ROWS, c1b = DOWN ? c1a + kMoeRows : I + c1a;
-            for (int kb = 0; kb < KB; ++kb, ++i) {
-                if (i >= S) ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p, smem_addr(&s->empty[st]), parity));
-                if (!ok) break;
-                const uint32_t bar = smem_addr(&s->full[st]), a = ring + st * STAGE;
+            for (; feed.kb < KB; ++feed.kb, ++feed.i) {
+                if (feed.i == until) return;
+                if (feed.i >= S) feed.ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p, smem_addr(&s->empty[feed.st]), feed.parity));
+                if (!feed.ok) return;
+                const uint32_t bar = smem_addr(&s->full[feed.st]), a = ring + feed.st * STAGE;
+                const int c0 = feed.kb * KS;
                 if (elect_lane()) {
                     mbar_arrive_expect_tx(bar, 2 * kPanel);
-                    map_load3(a, &weights, kb * KS, c1a, expert, bar);
+                    map_load3(a, &weights, c0, c1a, expert, bar);
                     if constexpr (GATES) {           // 64 rows a box; a box behind the end of K reads zeros
-                        map_load3(a + kPanel / 2, &weights, kb * KS, c1b, expert, bar);
-                        map_load3(a + kPanel, &weights, kb * KS + KE, c1a, expert, bar);
-                        map_load3(a + kPanel + kPanel / 2, &weights, kb * KS + KE, c1b, expert, bar);
+                        map_load3(a + kPanel / 2, &weights, c0, c1b, expert, bar);
+                        map_load3(a + kPanel, &weights, c0 + KE, c1a, expert, bar);
+                        map_load3(a + kPanel + kPanel / 2, &weights, c0 + KE, c1b, expert, bar);
                     } else {
-                        map_load3(a + kPanel, &weights, kb * KS, c1b, expert, bar);
+                        map_load3(a + kPanel, &weights, c0, c1b, expert, bar);
                     }
                 }
                 __syncwarp();
-                if (++st == S) {
-                    st = 0;
-                    parity ^= 1;
+                if (++feed.st == S) {
+                    feed.st = 0;
+                    feed.parity ^= 1;
                 }
             }
+            feed.kb = 0;
         }
-        if (lane == 0) s->issued[0] = i;
+    };
+
+    const int tiles = ((DOWN ? H : I) + ROWS - 1) / ROWS;
+    const bool report = !DOWN && blockIdx.x == 0;
+    int M;
+    if (P <= 32) {
+        // nothing of the ring is in use, so that the first stages are asked for at once
+        if (warp == 0) {
+            M = sort_few<NB>(p, list, entries, report);
+            if (lane == 0) s->scan[0] = M;
+            load_weights(M, M * tiles, S);
+        }
+    } else {
+        M = sort_pairs<NB>(p, s, list, entries, hist, report);
+        shared_proxy_fence();         // the ring's memory held the counts
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    if (P <= 32) M = s->scan[0];
+    const uint32_t tmem = s->tmem;
+    const int units = M * tiles;
+
+    if (warp == 0) {
+        load_weights(M, units, INT_MAX);
+        if (lane == 0) s->issued[0] = feed.i;
     } else if (warp == kWarps - 1) {  // the pairs' rows
         if (DOWN) {
             pdl_wait();
