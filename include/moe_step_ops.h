@@ -33,7 +33,8 @@ extern "C" {
  *   expert_ids[t, :]    the k experts with the largest keys, in falling order; among
  *                       equal keys the lower index first.  The key is the logit, or
  *                       with a bias sigmoid(logit) + bias[e]
- *   topk_weights[t, j]  = scale * p_j / (renormalize ? p_1 + .. + p_k : 1)   (p of the chosen)
+ *   topk_weights[t, j]  = scale * p_j / (renormalize ? p_1 + .. + p_k : 1)   (p of the chosen;
+ *                       quotients below 2^-126 may be 0)
  * An expert whose logit is -infinity or NaN (or whose key is) is never chosen and
  * does not count for the softmax.  A token with fewer than k others gets id -1 and
  * weight 0 in its last slots; moe_route_plan and the finalize take those with

@@ -14,7 +14,7 @@
 // token in a thousand) are chosen once more by keys in 64 bits.
 //
 // Bytes would bound both directions (32768 x 256: 5 us), but the choice's instructions
-// do: 27 us with a bias, 19 without (k = 8; taking the k experts one by one: 50).  The
+// do: 22 us with a bias, 17 without (k = 8; taking the k experts one by one: 50).  The
 // gradient of renormalised softmax weights reads the chosen logits alone (16385 x 128:
 // 6.3 us, 2.6 of bytes, bound by its instructions as well).
 #include <cfloat>
@@ -28,13 +28,18 @@ namespace mfr {
 namespace {
 
 constexpr int kGateWarps = 4;
-constexpr int kGateCtas = 8;           // an SM, of the choice
+constexpr int kGateCtas = 8;           // an SM, of the choice (10 or 12 spill registers: 25, 29 us)
 
 // Rises with f; 0 for -infinity and NaN, which are never chosen.
 __device__ __forceinline__ uint32_t order_key(float f) {
     f += 0.f;                                             // -0 counts as 0
     const uint32_t u = __float_as_uint(f);
     return f > -INFINITY ? u ^ ((static_cast<int32_t>(u) >> 31) | 0x80000000u) : 0u;
+}
+// That of a key with a bias.
+__device__ __forceinline__ uint32_t order_key(float l, float key) {
+    const uint32_t u = __float_as_uint(key);              // never -0: a sigmoid is not
+    return l > -INFINITY && key > -INFINITY ? u ^ ((static_cast<int32_t>(u) >> 31) | 0x80000000u) : 0u;
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
@@ -70,16 +75,22 @@ __device__ __forceinline__ void load_row(const void* l, int64_t at, int E, int l
     }
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+// Off by 2^-23 (one ulp); 0 from 2^126 on, where 1 / v is no normal number.
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float sigmoid(float l) { return reciprocal(1.f + expf(-l)); }
 
 // For keys, off by less than 6.25 u (u = 2^-24): ex2.approx is off by 2^-22 and its
 // rounded argument by 2 u |l|, which the sigmoid's slope makes 1.25 u at most (where
 // |l| is large it is flat); the sum by u, rcp.approx by 2^-23.
 __device__ __forceinline__ float near_sigmoid(float l) {
-    float e, r;
+    float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
+    return reciprocal(1.f + e);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -90,7 +101,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // sigmoid(l) times a factor that the token's chosen logits share (top: the largest),
 // 1 where one of them is positive: far negative ones still have their proportions.
 __device__ __forceinline__ float shared_sigmoid(float l, float top) {
-    return top > 0.f ? sigmoid(l) : expf(l - fmaxf(top, -FLT_MAX)) / (1.f + expf(l));
+    return top > 0.f ? sigmoid(l) : expf(l - fmaxf(top, -FLT_MAX)) * reciprocal(1.f + expf(l));
 }
 
 // Rises with f, a double that is no NaN; above 0.
@@ -152,18 +163,20 @@ __device__ __noinline__ int choose_in_64_bits(const GateParams& p, int64_t at, f
 // A warp's tokens are t, t + all warps, ...: the next one's logits are on their way
 // while this one's experts are chosen.
 template <bool B16, int V, int N>
-__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams p) {
-    __shared__ unsigned long long s_key[kGateWarps][32];
-    __shared__ float s_logit[kGateWarps][32];
-    __shared__ int s_expert[kGateWarps][32];
+__global__ void __launch_bounds__(32 * kGateWarps, N <= 8 ? kGateCtas : 1) gate_kernel(const GateParams p) {
+    constexpr bool KEPT = N <= 8;                         // biases in registers
+    __shared__ __align__(16) unsigned long long s_key[kGateWarps][36], s_sorted[kGateWarps][32];
     const int lane = threadIdx.x & 31;
     unsigned long long* keys = s_key[threadIdx.x >> 5];
-    float* logits = s_logit[threadIdx.x >> 5];
-    int* experts = s_expert[threadIdx.x >> 5];
+    unsigned long long* sorted = s_sorted[threadIdx.x >> 5];
     const int64_t warps = static_cast<int64_t>(gridDim.x) * kGateWarps;
     int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_dependents();
+    float bias[KEPT ? N : 1];
+    if constexpr (KEPT)
+#pragma unroll
+        for (int i = 0; i < N; ++i) bias[i] = p.bias && lane * N + i < p.E ? __ldg(p.bias + lane * N + i) : 0.f;
     float next[N];
     if (t < p.T) load_row<B16, V, N>(p.logits, t * p.E, p.E, lane, next);
     for (; t < p.T; t += warps) {
@@ -187,92 +200,92 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams 
         uint32_t key[N], best = 0;                        // this lane's largest
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float k = l[i];
-            if (p.bias) k = k > -INFINITY ? near_sigmoid(k) + __ldg(p.bias + lane * N + i) : -INFINITY;
-            key[i] = order_key(k);
+            if (p.bias) {
+                float b;
+                if constexpr (KEPT) b = bias[i];
+                else b = lane * N + i < p.E ? __ldg(p.bias + lane * N + i) : 0.f;
+                key[i] = order_key(l[i], near_sigmoid(l[i]) + b);
+            } else {
+                key[i] = order_key(l[i]);
+            }
             best = max(best, key[i]);
         }
         int mine = -1;
         float x = 0.f;                                    // its logit
         // one more: whether the first left out is close; and another, so that the bound lies
-        // below what may be among the chosen (32768 x 256, k = 8: 32 -> 26 us; with k = 16 more
+        // below what may be among the chosen (32768 x 256, k = 8: 32 -> 26 us then; with k = 16 more
         // than 32 experts reach it too often: 33 -> 43)
         const int wanted = p.bias ? p.k + (p.k <= 8 ? 2 : 1) : p.k;
         // A bound below the last of the wanted keys: that many lanes' largest reach it.
-        uint32_t bound = 1, left = best;
+        uint32_t bound = 0, left = best;
         for (int j = 0; j < wanted; ++j) {
-            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, left);
-            bound = max(m, 1u);
-            if (m == 0) break;
-            if (left == m) left = 0;
+            bound = __reduce_max_sync(0xFFFFFFFFu, left);
+            if (left == bound) left = 0;
         }
-        int count = 0;
+        bound = max(bound, 1u);
+        int own_count = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) count += key[i] >= bound;
-        count = __reduce_add_sync(0xFFFFFFFFu, count);
+        for (int i = 0; i < N; ++i) own_count += key[i] >= bound;
+        int upto = own_count;                             // of the lanes to this one
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+            if (lane >= off) upto += v;
+        }
+        const int count = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        bool known = false;                               // x is
         if (count <= 32) {
             // The few experts that reach it, one a lane, find their ranks by comparing.
-            int at_mem = 0;
+            int to = upto - own_count;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const bool in = key[i] >= bound;
-                const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-                if (in) {
-                    const int to = at_mem + __popc(who & ((1u << lane) - 1));
-                    // falling order of these: keys, then rising experts
-                    keys[to] = (static_cast<unsigned long long>(key[i]) << 32) | (0xFFFFFFFFu - (lane * N + i));
-                    logits[to] = l[i];
-                }
-                at_mem += __popc(who);
-            }
+            for (int i = 0; i < N; ++i)
+                // falling order of these: keys, then rising experts
+                if (key[i] >= bound) keys[to++] = (static_cast<unsigned long long>(key[i]) << 32) | (0xFFFFFFFFu - (lane * N + i));
+            if (lane < 4) keys[count + lane] = 0;         // four are compared at a time
             __syncwarp();
-            unsigned long long own = lane < count ? keys[lane] : 0;
-            const float own_l = lane < count ? logits[lane] : 0.f;
-            const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(own));
+            const unsigned long long own = lane < count ? keys[lane] : 0;
             int rank = 0;
-            for (int j = 0; j < count; ++j) rank += keys[j] > own;
-            if (p.bias) {
+            for (int j = 0; j < count; j += 4) {
+                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(keys + j), b = *reinterpret_cast<const ulonglong2*>(keys + j + 2);
+                rank += (a.x > own) + (a.y > own) + (b.x > own) + (b.y > own);
+            }
+            if (lane < count) sorted[rank] = own;
+            __syncwarp();
+            const unsigned long long at_rank = lane < count ? sorted[lane] : 0x8000000000000000ull;
+            const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(at_rank));
+            const float v = key_value(static_cast<uint32_t>(at_rank >> 32));
+            if (lane < min(p.k, count)) mine = e;
+            if (!p.bias) {
+                x = v;
+                known = true;
+            } else {
                 // Neighbours in the order that are closer than their keys' errors, two of less
                 // than 2^-21 (1 + |key|) each (6.25 u for the sigmoid, u |key| for the sum):
                 // keys in 64 bits decide, unless experts below the bound may be among them.
-                if (lane < count) experts[rank] = static_cast<int>(own >> 32);
-                __syncwarp();
-                const float v = key_value(lane < count ? static_cast<uint32_t>(experts[lane]) : 0x80000000u);
                 const float after = __shfl_down_sync(0xFFFFFFFFu, v, 1);
                 const bool close = lane < p.k && lane + 1 < count && !(v - after > 0x1p-20f * (1.f + fabsf(after)));
                 if (__any_sync(0xFFFFFFFFu, close)) {
-                    const float least = __shfl_sync(0xFFFFFFFFu, v, max(0, min(p.k, count) - 1));
-                    const float from = reach(least);
+                    const float from = reach(__shfl_sync(0xFFFFFFFFu, v, max(0, min(p.k, count) - 1)));
                     if (bound > 1 && !(key_value(bound) < from)) {
                         mine = choose_in_64_bits<B16>(p, at, from, lane);
-                        count = -1;
                     } else {
-                        if (lane < count) {
-                            own = exact_key(own_l, __ldg(p.bias + e));
-                            keys[lane] = own;
-                            experts[lane] = e;
-                        }
+                        unsigned long long exact = 0;
+                        if (lane < count) keys[lane] = exact = exact_key(logit_at<B16>(p.logits, at + e), __ldg(p.bias + e));
                         __syncwarp();
                         rank = 0;
-                        for (int j = 0; j < count; ++j) rank += keys[j] > own || (keys[j] == own && experts[j] < e);
+                        for (int j = 0; j < count; ++j) {
+                            // equal ones: the lower expert, of which the FP32 order tells nothing
+                            const int other = __shfl_sync(0xFFFFFFFFu, e, j);
+                            rank += keys[j] > exact || (keys[j] == exact && other < e);
+                        }
+                        if (lane < count) sorted[rank] = static_cast<unsigned long long>(e);
+                        __syncwarp();
+                        if (lane < min(p.k, count)) mine = static_cast<int>(sorted[lane]);
                     }
                 }
             }
             __syncwarp();
-            if (count >= 0) {
-                if (lane < count) {
-                    experts[rank] = e;
-                    logits[rank] = own_l;
-                }
-                __syncwarp();
-                if (lane < p.k && lane < count) {
-                    mine = experts[lane];
-                    x = logits[lane];
-                }
-            }
-            __syncwarp();
         } else {
-            count = -1;
             uint32_t before = 0;
             bool close = false;
             float least = -INFINITY;
@@ -308,20 +321,27 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateParams 
             // the least key that may be among the chosen: that of the k-th, less both errors
             if (close) mine = choose_in_64_bits<B16>(p, at, reach(least), lane);
         }
-        if (count < 0 && mine >= 0) x = logit_at<B16>(p.logits, at + mine);
+        if (!known && mine >= 0) x = logit_at<B16>(p.logits, at + mine);
         float w = mine >= 0 ? fminf(x, FLT_MAX) : 0.f;
         if (p.sigmoid) {
-            if (p.renormalize) top = warp_max(mine >= 0 ? w : -INFINITY);
-            w = mine < 0 ? 0.f : p.renormalize ? shared_sigmoid(w, top) : sigmoid(w);
+            if (!p.renormalize || __any_sync(0xFFFFFFFFu, w > 0.f)) {
+                w = mine >= 0 ? sigmoid(w) : 0.f;
+            } else {
+                top = warp_max(mine >= 0 ? w : -INFINITY);
+                w = mine >= 0 ? shared_sigmoid(w, top) : 0.f;
+            }
         } else {
             if (p.renormalize) top = __shfl_sync(0xFFFFFFFFu, w, 0);   // the first chosen is the largest
             w = mine >= 0 ? expf(w - top) : 0.f;
         }
-        if (p.renormalize) denominator = warp_allreduce_sum(w);
-        if (p.sigmoid && !p.renormalize) denominator = 1.f;
+        if (p.renormalize) {
+            denominator = w;                              // of the 16 lanes that may have one
+#pragma unroll
+            for (int off = kMaxK / 2; off > 0; off >>= 1) denominator += __shfl_xor_sync(0xFFFFFFFFu, denominator, off);
+        }
         if (lane < p.k) {
             p.ids[t * p.k + lane] = mine;
-            p.w[t * p.k + lane] = w > 0.f ? p.scale * (w / denominator) : 0.f;
+            p.w[t * p.k + lane] = w > 0.f ? p.scale * (w * reciprocal(denominator)) : 0.f;
         }
     }
 }
