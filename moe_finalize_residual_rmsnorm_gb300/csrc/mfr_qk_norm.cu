@@ -19,13 +19,14 @@
 // Queries and keys belong to different CTAs, so that a lane's gamma and its running sum
 // of d_gamma stay where they are; the gradient's warps stay for several units, and a
 // second launch adds their sums in a fixed order.
-// Measured on GB300, of the copy rate: 16384 x 40 heads x 128 out of a packed tensor 61
-// us (0.83), its gradient at 8192 tokens 50 us (0.75); 4097 x 28 x 80 gradient 23.5
-// us (0.35: 2.5 units a warp, whose first loads nothing covers, and 3 us for the second
-// launch).  Loads wait: 22 warps an SM have 24 KB in flight.  Three or four groups at a
-// time (64, 67 us), more warps of fewer registers (67), refilling a group's
-// registers as soon as it is in use (63) and copies into shared memory four groups
-// ahead (80) were no faster.
+// Measured on GB300, of the copy rate: 16384 x 40 heads x 128 out of a packed tensor 58.5
+// us (0.87; 61 without the prefetch to L2), its gradient at 8192 tokens 48.5 us (0.78); 4097
+// x 28 x 80 gradient 21 us (0.39: 2.5 units a warp, whose first loads nothing covers, 500
+// instructions a group of heads, and 3 us for the second launch).  Loads wait: 22 warps an
+// SM have 24 KB in flight in registers.  Three or four groups at a time (64, 67 us), more
+// warps of fewer registers (67), refilling a group's registers as soon as it is in use
+// (63) and copies into shared memory four groups ahead (80) were no faster, nor was
+// prefetching in the gradient (50, and 24 for 23.5).
 #include "moe_step_ops.h"
 #include "mfr_device.cuh"
 #include "mfr_layer.h"
@@ -100,6 +101,8 @@ __device__ __forceinline__ uint4 narrow(const f2* f) {
     return make_uint4(narrow2<F16>(f[0]), narrow2<F16>(f[1]), narrow2<F16>(f[2]), narrow2<F16>(f[3]));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+
 // Which elements of a head a lane holds: eight from `a` and eight from `b` (-1: none).
 struct Place {
     int a, b;
@@ -126,16 +129,17 @@ __device__ __forceinline__ Place place_of(int u, int D, int rotary, bool interle
 }
 
 // A lane's cosines and sines, as `turn` takes them: for pairs (i, i + rotary / 2) four
-// pairs each of neighbours, for pairs (2 i, 2 i + 1) eight of (cos, cos) and of (-sin, sin).
-template <bool PAIRED>
+// pairs each of neighbours, for pairs (2 i, 2 i + 1) eight of (cos, cos) and of (-sin, sin),
+// or back (sin, -sin).
+template <bool BACK, bool PAIRED>
 struct Angles {
     f2 c[PAIRED ? 8 : 4], s[PAIRED ? 8 : 4];
     __device__ __forceinline__ void set(int i, float c0, float c1, float s0, float s1) {      // angles 2 i and 2 i + 1
         if constexpr (PAIRED) {
             c[2 * i] = both(c0);
             c[2 * i + 1] = both(c1);
-            s[2 * i] = pair(-s0, s0);
-            s[2 * i + 1] = pair(-s1, s1);
+            s[2 * i] = BACK ? pair(s0, -s0) : pair(-s0, s0);
+            s[2 * i + 1] = BACK ? pair(s1, -s1) : pair(-s1, s1);
         } else {
             c[i] = pair(c0, c1);
             s[i] = pair(s0, s1);
@@ -145,12 +149,12 @@ struct Angles {
 
 // The pairs of x turned by the angles, or back.
 template <bool BACK, bool PAIRED>
-__device__ __forceinline__ void turn(f2 (&x)[8], const Angles<PAIRED>& t) {
-    const f2 minus = both(-1.f);
+__device__ __forceinline__ void turn(f2 (&x)[8], const Angles<BACK, PAIRED>& t) {
     if constexpr (PAIRED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fma2(swapped(x[i]), BACK ? mul2(t.s[i], minus) : t.s[i], mul2(x[i], t.c[i]));
+        for (int i = 0; i < 8; ++i) x[i] = fma2(swapped(x[i]), t.s[i], mul2(x[i], t.c[i]));
     } else {
+        const f2 minus = both(-1.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const f2 a = x[i], b = x[i + 4], less = mul2(BACK ? a : b, minus);
@@ -160,33 +164,40 @@ __device__ __forceinline__ void turn(f2 (&x)[8], const Angles<PAIRED>& t) {
     }
 }
 
-// Sum over a head's lanes: L of them, or (L = 0) `lanes`, not a power of two, from `base` on.
+// Sum over a head's lanes, L or (L = 0) `lanes` of them from `base` on.
 template <int L>
 __device__ __forceinline__ float head_sum(float v, int lanes, int base) {
-    if constexpr (L > 0) {
+    if constexpr (L > 0 && (L & (L - 1)) == 0) {
 #pragma unroll
         for (int off = L / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
         return v;
     } else {
         float sum = 0.f;
-        for (int i = 0; i < lanes; ++i) sum += __shfl_sync(0xFFFFFFFFu, v, base + i);
+        if constexpr (L > 0) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) sum += __shfl_sync(0xFFFFFFFFu, v, base + i);
+        } else {
+            for (int i = 0; i < lanes; ++i) sum += __shfl_sync(0xFFFFFFFFu, v, base + i);
+        }
         return sum;
     }
 }
 
 // Units of work: CTA b < blocks_q has queries' units, the others keys'.  A group is HPW =
 // 32 / lanes heads; a token's per_token groups are `slices` runs of `run` groups, and
-// unit u is run u % slices of token u / slices.  A warp takes every stride-th unit.
+// unit u is run u % slices of token u / slices.  A warp takes every stride-th unit:
+// step_t tokens and step_s runs further.
 struct QkRuns {
     int lanes;              // of a head
     int blocks_q;
     int run[2];
     int per_token[2];
     int slices[2];
-    int64_t stride[2];
+    int step_t[2];
+    int step_s[2];
 };
 
-// L: lanes of a head, 0: no power of two.  PAIRED: pairs (2 i, 2 i + 1).
+// L: lanes of a head, 0: as many as r says.  PAIRED: pairs (2 i, 2 i + 1).
 template <bool F16, int L, bool GRAD, bool PAIRED>
 __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) qk_kernel(const __grid_constant__ QkParams p, const __grid_constant__ QkRuns r) {
     constexpr int BATCH = 2;                  // groups whose loads are in flight
@@ -196,7 +207,6 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
     const int which = static_cast<int>(blockIdx.x) < r.blocks_q ? 0 : 1;
     const QkSide& side = p.side[which];
     const int per = r.per_token[which], slices = r.slices[which], run = r.run[which];
-    const int64_t units = p.T * slices;
     const int of_head = lane / lanes, base = of_head * lanes;
     const bool used = of_head < heads_a_warp;             // lanes behind the last whole head have none
     const Place pl = place_of(lane - base, p.D, p.rotary, PAIRED);
@@ -211,13 +221,21 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
     if constexpr (GRAD)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = 0;
-    int64_t unit = (blockIdx.x - (which ? r.blocks_q : 0)) * int64_t(kQkWarps) + warp;
-    int next_pos = unit < units ? p.positions[unit / slices] : 0;
-    for (; unit < units; unit += r.stride[which]) {
-        const int64_t t = unit / slices, next = unit + r.stride[which];
-        const int g0 = static_cast<int>(unit - t * slices) * run, g1 = min(g0 + run, per);
+    // T * slices is the number of 16 heads at most that an output holds: far below 2^32
+    const uint32_t unit = (blockIdx.x - (which ? r.blocks_q : 0)) * kQkWarps + warp;
+    int64_t t = unit / static_cast<uint32_t>(slices);
+    int slice = static_cast<int>(unit - static_cast<uint32_t>(t) * slices);
+    int next_pos = t < p.T ? p.positions[t] : 0;
+    while (t < p.T) {
+        int next_slice = slice + r.step_s[which];
+        int64_t next = t + r.step_t[which];
+        if (next_slice >= slices) {
+            next_slice -= slices;
+            ++next;
+        }
+        const int g0 = slice * run, g1 = min(g0 + run, per);
         const int pos = next_pos;
-        if (next < units) next_pos = p.positions[next / slices];      // long before its cosines are asked for
+        if (next < p.T) next_pos = p.positions[next];     // long before its cosines are asked for
         const int first = g0 * heads_a_warp + of_head;
         const uint16_t* xs = side.x + t * side.x_token + first * side.x_head;
         const uint16_t* ds = GRAD ? side.d_out + t * side.d_token + first * side.d_head : nullptr;
@@ -225,7 +243,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
         const int64_t x_step = heads_a_warp * side.x_head, d_step = GRAD ? heads_a_warp * side.d_head : 0;
         const int64_t o_step = heads_a_warp * side.out_head;
         int heads = side.heads - first;                   // from this lane's first on
-        Angles<PAIRED> angles;
+        Angles<GRAD, PAIRED> angles;
         bool known = false, good = false;
         for (int g = g0; g < g1; g += BATCH) {
             uint4 xa[BATCH], xb[BATCH], da[GRAD ? BATCH : 1], db[GRAD ? BATCH : 1];
@@ -243,6 +261,13 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
             }
             if (!known) {
                 known = true;
+                // the rest of the run to L2: more bytes in flight than registers hold
+                if constexpr (!GRAD)
+                    for (int i = BATCH; i < g1 - g0; ++i) {
+                        const bool on = i * heads_a_warp < heads;
+                        if (on && has_a) prefetch_l2(xs + i * x_step + pl.a);
+                        if (on && has_b) prefetch_l2(xs + i * x_step + pl.b);
+                    }
                 good = static_cast<uint32_t>(pos) < static_cast<uint32_t>(p.max_positions);
                 if (!good && lane == 0) atomicOr(p.status, MFR_STATUS_BAD_INDEX);
                 const float4* row = reinterpret_cast<const float4*>(p.table + static_cast<int64_t>(pos) * p.rotary + 8 * pl.u);
@@ -295,6 +320,8 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
             os += BATCH * o_step;
             if constexpr (GRAD) ds += BATCH * d_step;
         }
+        t = next;
+        slice = next_slice;
     }
     if constexpr (GRAD) {
         // the CTA's warps' heads, in a fixed order
@@ -350,12 +377,18 @@ using Kernel = void (*)(const QkParams, const QkRuns);
 
 int lanes_for(int D) { return (D + 15) / 16; }
 
+// A head's lanes are known to the kernel up to 8 and for powers of two (4097 x 28 heads of 80,
+// gradient: 23.5 us with a loop over them, 21 so).
 template <bool F16, bool GRAD, bool PAIRED>
 Kernel kernel_of(int D) {
     switch (lanes_for(D)) {
         case 1: return qk_kernel<F16, 1, GRAD, PAIRED>;
         case 2: return qk_kernel<F16, 2, GRAD, PAIRED>;
+        case 3: return qk_kernel<F16, 3, GRAD, PAIRED>;
         case 4: return qk_kernel<F16, 4, GRAD, PAIRED>;
+        case 5: return qk_kernel<F16, 5, GRAD, PAIRED>;
+        case 6: return qk_kernel<F16, 6, GRAD, PAIRED>;
+        case 7: return qk_kernel<F16, 7, GRAD, PAIRED>;
         case 8: return qk_kernel<F16, 8, GRAD, PAIRED>;
         case 16: return qk_kernel<F16, 16, GRAD, PAIRED>;
         case 32: return qk_kernel<F16, 32, GRAD, PAIRED>;
@@ -400,7 +433,8 @@ QkRuns runs_for(const QkShape& s, int64_t T, bool grad, int sms, int* blocks) {
             if (share < 1) share = 1;
             if (b[i] > share) b[i] = share;
         }
-        r.stride[i] = b[i] * kQkWarps;
+        r.step_t[i] = static_cast<int>(b[i] * kQkWarps / r.slices[i]);
+        r.step_s[i] = static_cast<int>(b[i] * kQkWarps % r.slices[i]);
     }
     r.blocks_q = static_cast<int>(b[0]);
     *blocks = static_cast<int>(b[0] + b[1]);
