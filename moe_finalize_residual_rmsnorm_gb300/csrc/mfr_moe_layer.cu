@@ -17,19 +17,20 @@
 //
 // Each CTA sorts the pairs by expert itself (at most 4096, from L2), so that no
 // launch before it is needed; up to 32 of them are one warp's, which asks for its first
-// weights before the others are ready (5 tokens of 384 x 368: 11.7 -> 10.9 us).  A unit is (tile of weight rows, chunk of an expert's
-// pairs) over all of K, in turns over persistent CTAs; chunks of one expert are
-// neighbours, so that its weights come from DRAM once.
+// weights before the others are ready (5 tokens of 384 x 368: 11.7 -> 10.9 us).  A unit is
+// (tile of weight rows, chunk of an expert's pairs) over all of K, in turns over persistent
+// CTAs; chunks of one expert are neighbours, so that its weights come from DRAM once.
 //   first launch:  64 rows of G and the same 64 of U (E4M3: 128 and 128, a group of
 //                  h's scales), h to the workspace
 //   second launch: 256 rows of D, products to y[pair] in FP32; it loads weights
 //                  before it waits for the first launch
 //   then the pairs of every token are added in slot order, by a small third launch:
 //                  no atomics, the same bits in every call
+// Where units are few and long, the CTAs of a cluster take a part of K each.
 // Measured on GB300 (4096 x 1024 weights an expert, bf16, copy rate 6782 GB/s): 16 tokens
-// of 128 experts 309 us (0.99 of the copy rate), 64 of 64 experts 248 us (0.96), one
+// of 128 experts 304 us (1.0 of the copy rate), 64 of 64 experts 244 us (0.97), one
 // token of 64 experts 38 us (0.78: two launches' starts, sorts and first loads, 8 us); 128
-// tokens of 64 experts of 8192 x 1024 in E4M3 273 us (0.87: 512 units are 3.4 turns of the
+// tokens of 64 experts of 8192 x 1024 in E4M3 274 us (0.87: 512 units are 3.4 turns of the
 // SMs).  With units for few SMs one SM takes 60-70 GB/s: a stage's eight products are
 // 330 cycles whatever their columns (the weights are read from shared memory for each), and
 // hand-overs 200 more.
@@ -40,13 +41,15 @@
 // us at its end); two CTAs an SM, so that the launches overlap (half the ring each: one
 // token 52 us); fetching w2 to L2 at the first launch's end (no difference); units of 32
 // or 64 columns of h and 128 rows of D, in E4M3 with clusters that share a group's
-// largest magnitude (25 shapes 5 % slower: more copies, and in E4M3 more steps, a byte).
+// largest magnitude (25 shapes 5 % slower: more copies, and in E4M3 more steps, a byte);
+// clusters of two for every call, which divide the last, partial turn (3 % slower).
 //
 // bf16: h is kept as the sum of two bf16 values (16 bits of it), two products of the
 // same weights, which cost nothing where bytes bound it; rounded once it alone would
 // put the output 1.4 times as far from the exact one as its own rounding does.
 // E4M3: products of 128 columns of K are one accumulation in tensor memory, which
 // the finishing warps scale and add in FP32 registers.
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 #include <mutex>
@@ -100,6 +103,7 @@ struct Shared {
     uint64_t full[kRingStages], empty[kRingStages];
     uint64_t done[kMaxTurns], taken[kMaxTurns];       // an accumulator is complete; its values are in registers
     uint64_t drain;
+    uint64_t parts[kFinishWarps];     // the other parts' sums of this warp's values are in the workspace
     uint32_t tmem;
     int dead;                         // a wait ran out: every role leaves
     int issued[2];                    // stages that the loading warps have begun
@@ -130,11 +134,13 @@ __device__ __forceinline__ bool finishers_well(bool ok) {
 
 // A role's wait for another.  It gives up after p.wait_limit cycles (0: at once, whatever
 // there is), or when another has given up.
+template <bool CLUSTER = false>
 __device__ bool role_wait(int* dead_word, const MoeParams& p, uint32_t bar, uint32_t parity) {
-    if (p.wait_limit > 0 && mbar_test_parity(bar, parity)) return true;
+    auto test = [&] { return CLUSTER ? mbar_test_cluster(bar, parity) : mbar_test_parity(bar, parity); };
+    if (p.wait_limit > 0 && test()) return true;
     volatile int* dead = dead_word;
     const long long t0 = clock64();
-    while (p.wait_limit == 0 || !mbar_test_parity(bar, parity)) {
+    while (p.wait_limit == 0 || !test()) {
         if (*dead) return false;
         if (clock64() - t0 >= p.wait_limit) {
             *dead = 1;
@@ -254,8 +260,9 @@ __device__ __forceinline__ int sort_few(const MoeParams& p, uint16_t* list, uint
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
-// One launch of products.  DOWN: the second one.
-template <bool FP8, bool DOWN, int NB>
+// One launch of products.  DOWN: the second one.  JOINT: the CTAs of a cluster have one
+// unit, a part of K each, and the first adds the others' sums to its own.
+template <bool FP8, bool DOWN, int NB, bool JOINT>
 __global__ void __launch_bounds__(kMoeThreads, 1)
 moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights, const __grid_constant__ CUtensorMap rows) {
     constexpr bool GATES = !FP8 && !DOWN;            // gate and up rows in one accumulator, two steps of K a stage
@@ -288,6 +295,8 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             mbar_init(smem_addr(&s->taken[i]), kFinishWarps);
         }
         mbar_init(smem_addr(&s->drain), 1);
+        if (JOINT)
+            for (int i = 0; i < kFinishWarps; ++i) mbar_init(smem_addr(&s->parts[i]), p.cluster - 1);
         s->dead = s->issued[0] = s->issued[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&weights);
@@ -303,18 +312,20 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
     }
     const int H = p.H, I = p.I, K = DOWN ? I : H, P = p.T * p.k;
     const int KB = (K + KS - 1) / KS;                // stages of a unit
-    const int G = gridDim.x;
+    // this CTA's units, and its stages of them
+    const int part = JOINT ? blockIdx.x % p.cluster : 0, parts = JOINT ? p.cluster : 1;
+    const int U0 = blockIdx.x / parts, G = gridDim.x / parts, K0 = KB * part / parts, K1 = KB * (part + 1) / parts;
 
     // The weights: stages up to number `until`, from where the last call ended.
     struct {
         int u, kb, i, st, parity;
         bool ok;
-    } feed{static_cast<int>(blockIdx.x), 0, 0, 0, 1, true};
+    } feed{U0, K0, 0, 0, 1, true};
     auto load_weights = [&](int M, int units, int until) {
         for (; feed.u < units; feed.u += G) {
             const int tile = feed.u / M, expert = unpack_entry(entries[feed.u - tile * M]).expert;
             const int c1a = tile * ROWS, c1b = DOWN ? c1a + kMoeRows : I + c1a;
-            for (; feed.kb < KB; ++feed.kb, ++feed.i) {
+            for (; feed.kb < K1; ++feed.kb, ++feed.i) {
                 if (feed.i == until) return;
                 if (feed.i >= S) feed.ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p, smem_addr(&s->empty[feed.st]), feed.parity));
                 if (!feed.ok) return;
@@ -337,7 +348,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     feed.parity ^= 1;
                 }
             }
-            feed.kb = 0;
+            feed.kb = K0;
         }
     };
 
@@ -361,6 +372,8 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
     if (P <= 32) M = s->scan[0];
     const uint32_t tmem = s->tmem;
     const int units = M * tiles;
+    if (JOINT) cluster_arrive();
+    bool met = false;                                // this thread has seen the cluster's arrivals
 
     if (warp == 0) {
         load_weights(M, units, INT_MAX);
@@ -373,7 +386,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
         }
         bool ok = true;
         int i = 0, st = 0, parity = 1;
-        for (int u = blockIdx.x; ok && u < units; u += G) {
+        for (int u = U0; ok && u < units; u += G) {
             const Entry en = unpack_entry(entries[u % M]);
             int v[4];
 #pragma unroll
@@ -385,7 +398,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             const int4 r2 = DOWN ? make_int4(v[0] + P, v[1] + P, v[2] + P, v[3] + P) : r;     // lower parts
             const int gathers = (en.n + 3) >> 2;
             const uint32_t second = ring + 2 * kPanel + (STACKED ? (en.n + 15) & ~15 : NB) * 128;
-            for (int kb = 0; kb < KB; ++kb, ++i) {
+            for (int kb = K0; kb < K1; ++kb, ++i) {
                 if (i >= S) ok = role_wait(&s->dead, p, smem_addr(&s->empty[st]), parity);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -406,17 +419,17 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
     } else if (warp == 1) {           // the products
         bool ok = true;
         int st = 0, parity = 0, uses = 0;
-        for (int u = blockIdx.x; ok && u < units; u += G) {
+        for (int u = U0; ok && u < units; u += G) {
             const int n = (unpack_entry(entries[u % M]).n + 15) & ~15;
             const uint32_t desc = mma_desc(FP8, STACKED ? 2 * n : n);
-            for (int kb = 0; kb < KB; ++kb) {
+            for (int kb = K0; kb < K1; ++kb) {
                 // the stage is full, and (lane 1) the accumulator's values are in registers
-                const bool again = lane == 1 && (FP8 || kb == 0) && uses >= TURNS;
+                const bool again = lane == 1 && (FP8 || kb == K0) && uses >= TURNS;
                 ok = __all_sync(0xFFFFFFFFu, role_wait(&s->dead, p, again ? smem_addr(&s->taken[uses % TURNS]) : smem_addr(&s->full[st]),
                                                        again ? (uses / TURNS - 1) & 1 : parity));
                 if (!ok) break;
                 tcgen05_fence_after();
-                const bool last = FP8 || kb == KB - 1;
+                const bool last = FP8 || kb == K1 - 1;
                 if (elect_lane()) {
                     const uint32_t a = ring + st * STAGE, d = tmem + uses % TURNS * ACC;
                     const uint64_t da = operand_desc(a), db = operand_desc(a + 2 * kPanel);
@@ -425,7 +438,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint64_t from = da + half * (kPanel >> 4) + i * 2;
-                            const bool more = i > 0 || (!FP8 && kb > 0) || (GATES && half > 0);
+                            const bool more = i > 0 || (!FP8 && kb > K0) || (GATES && half > 0);
                             mma_issue<FP8>(d + (GATES ? 0 : half * COLS), from, db + (GATES ? half * (NB * 128 >> 4) : 0) + i * 2, desc, more);
                             if constexpr (DOWN && !FP8 && !STACKED)
                                 mma_issue<FP8>(d + half * COLS, from, db + (NB * 128 >> 4) + i * 2, desc, true);
@@ -452,7 +465,42 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + side * 8;
         int uses = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += G) {
+        // where this warp's values of a part lie, 16 of a thread for each group of columns
+        float* mine = p.parts + (static_cast<int64_t>(blockIdx.x) * kFinishWarps + (warp - 2)) * (NB / 16) * 512 + lane;
+        auto put_part = [&](int q, const float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                mine[q * 512 + j * 32] = a[j];
+                mine[q * 512 + 256 + j * 32] = b[j];
+            }
+        };
+        auto add_parts = [&](int q, float (&a)[8], float (&b)[8]) {
+            for (int r = 1; r < parts; ++r) {
+                const float* from = mine + static_cast<int64_t>(r) * kFinishWarps * (NB / 16) * 512 + q * 512;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    a[j] += __ldcg(from + j * 32);
+                    b[j] += __ldcg(from + 256 + j * 32);
+                }
+            }
+        };
+        // this part's sums are in the workspace
+        auto hand_over = [&] {
+            __threadfence();
+            cluster_wait();
+            met = true;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(smem_addr(&s->parts[warp - 2]), 0);
+        };
+        // whether the others' are, for all of the finishing warps
+        auto parts_there = [&] {
+            cluster_wait();
+            met = true;
+            const bool there = role_wait<true>(&s->dead, p, smem_addr(&s->parts[warp - 2]), 0);
+            __threadfence();
+            return finishers_well(there);
+        };
+        for (int u = U0; ok && u < units; u += G) {
             const int tile = u / M;
             const Entry en = unpack_entry(entries[u - tile * M]);
             const uint16_t* pairs = list + en.start;
@@ -493,15 +541,15 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                 auto load_scales = [&](int kb) {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i) {
-                        const int at = min(kb + i, KB - 1);
+                        const int at = min(kb + i, K1 - 1);
                         nw0[i] = __ldg(w0 + at);
                         nw1[i] = __ldg(w1 + at);
                         n0[i] = __ldcg(from[0] + at);
                         n1[i] = HALF > 32 ? __ldcg(from[1] + at) : 0.f;
                     }
                 };
-                load_scales(0);
-                for (int kb0 = 0; ok && kb0 < KB; kb0 += AHEAD) {
+                load_scales(K0);
+                for (int kb0 = K0; ok && kb0 < K1; kb0 += AHEAD) {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i) {
                         sw0[i] = nw0[i];
@@ -512,7 +560,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     load_scales(kb0 + AHEAD);
 #pragma unroll
                     for (int step = 0; step < AHEAD; ++step) {
-                        if (kb0 + step >= KB) break;
+                        if (kb0 + step >= K1) break;
                         __syncwarp();
                         if (lane < HALF) sx[lane] = f0[step];
                         if (HALF > 32) sx[lane + 32] = f1[step];
@@ -545,6 +593,20 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                 }
                 ok = finishers_well(ok);
                 if (!ok) break;
+                if (JOINT && part > 0) {
+#pragma unroll
+                    for (int q = 0; q < NB / 16; ++q)
+                        if (q < groups) put_part(q, d0[q], d1[q]);
+                    hand_over();
+                    continue;
+                }
+                if (JOINT) {
+                    ok = parts_there();
+                    if (!ok) break;
+#pragma unroll
+                    for (int q = 0; q < NB / 16; ++q)
+                        if (q < groups) add_parts(q, d0[q], d1[q]);
+                }
 #pragma unroll
                 for (int q = 0; q < NB / 16; ++q) {
                     const int c0 = q * 16 + side * 8;
@@ -577,6 +639,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             } else {
                 ok = role_wait(&s->dead, p, smem_addr(&s->done[uses % TURNS]), uses / TURNS & 1);
                 ok = finishers_well(ok);
+                if (JOINT && part == 0 && ok) ok = parts_there();
                 if (!ok) break;
                 tcgen05_fence_after();
                 const uint32_t acc = lanes + uses % TURNS * ACC;
@@ -604,6 +667,11 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                             v1[i] += __uint_as_float(b[i]);
                         }
                     }
+                    if (JOINT && part > 0) {
+                        put_part(q, v0, v1);
+                        continue;
+                    }
+                    if (JOINT) add_parts(q, v0, v1);
                     if constexpr (DOWN) {
                         to_y(c0, v0, v1);
                     } else {
@@ -634,6 +702,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&s->taken[uses % TURNS]));
                 ++uses;
+                if (JOINT && part > 0) hand_over();
             }
         }
     }
@@ -651,6 +720,11 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
     if (warp == 1) {
         tcgen05_fence_after();
         tmem_free(tmem, tmem_columns<FP8, DOWN, NB>());
+    }
+    if (JOINT) {                      // nobody leaves while another may still arrive on its barriers
+        if (!met) cluster_wait();
+        cluster_arrive();
+        cluster_wait();
     }
 }
 
@@ -690,18 +764,21 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const MoeParams p)
 
 using Kernel = void (*)(const MoeParams, const CUtensorMap, const CUtensorMap);
 
-template <int NB>
-Kernel kernel_of(bool fp8, bool down) {
-    if (fp8) return down ? moe_layer_kernel<true, true, NB> : moe_layer_kernel<true, false, NB>;
-    return down ? moe_layer_kernel<false, true, NB> : moe_layer_kernel<false, false, NB>;
+template <bool FP8, int NB>
+Kernel kernel_of(bool down, bool joint) {
+    if (joint) return down ? moe_layer_kernel<FP8, true, NB, true> : moe_layer_kernel<FP8, false, NB, true>;
+    return down ? moe_layer_kernel<FP8, true, NB, false> : moe_layer_kernel<FP8, false, NB, false>;
 }
 
-Kernel kernel_for(const MoeLayerShape& s, bool down) {
+template <int NB>
+Kernel kernel_of(bool fp8, bool down, bool joint) { return fp8 ? kernel_of<true, NB>(down, joint) : kernel_of<false, NB>(down, joint); }
+
+Kernel kernel_for(const MoeLayerShape& s, bool down, bool joint) {
     switch (s.columns) {
-        case 16: return kernel_of<16>(s.fp8, down);
-        case 32: return kernel_of<32>(s.fp8, down);
-        case 64: return kernel_of<64>(s.fp8, down);
-        default: return kernel_of<128>(s.fp8, down);
+        case 16: return kernel_of<16>(s.fp8, down, joint);
+        case 32: return kernel_of<32>(s.fp8, down, joint);
+        case 64: return kernel_of<64>(s.fp8, down, joint);
+        default: return kernel_of<128>(s.fp8, down, joint);
     }
 }
 
@@ -735,6 +812,12 @@ int64_t align256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
 }  // namespace
 
+// Chunks of experts' pairs that there can be.
+static int most_entries(const MoeLayerShape& s) {
+    const int P = s.T * s.k;
+    return std::min(P, std::min(P, s.E) + P / s.columns);
+}
+
 void moe_layer_choose(MoeLayerShape& s, int sms) {
     const int64_t P = static_cast<int64_t>(s.T) * s.k;
     // columns for twice an expert's mean share of the pairs: fewer leave more of the ring
@@ -742,18 +825,17 @@ void moe_layer_choose(MoeLayerShape& s, int sms) {
     int64_t want = 2 * P / s.E + 8;
     if (want > s.T) want = s.T;
     s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
-    const int64_t entries = (P < s.E ? P : s.E) + P / s.columns;
-    s.entries = static_cast<int>((entries < P ? entries : P) + 3) & ~3;
+    s.entries = (most_entries(s) + 3) & ~3;
     const int behind = shared_bytes(s.columns) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
     const int stage = 2 * kPanel + s.columns * 128 * (s.fp8 ? 1 : 2);
     s.stages = (kMaxSmem - 1024 - behind) / stage;
     if (s.stages > kRingStages) s.stages = kRingStages;
     s.smem = 1024 + behind + s.stages * stage;
-    s.grid = sms;
     s.act = 0;
     s.act_sf = align256(P * s.I * (s.fp8 ? 1 : 4));
     s.y = s.act_sf + (s.fp8 ? align256(P * (s.I / 128) * 4) : 0);
-    s.bytes = s.y + align256(P * s.H * 4);
+    s.parts = s.y + align256(P * s.H * 4);
+    s.bytes = s.parts + static_cast<int64_t>(sms) * kFinishWarps * (s.columns / 16) * 512 * 4;
 }
 
 void* moe_layer_encoder() {
@@ -770,14 +852,50 @@ void* moe_layer_encoder() {
     return fn;
 }
 
-cudaError_t moe_layer_prepare(const MoeLayerShape& s) {
+static cudaError_t prepare(Kernel kernel) {
+    const void* k = reinterpret_cast<const void*>(kernel);
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, k);
+    // the attribute is per kernel, shared by every plan: always the most
+    return e == cudaSuccess ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) : e;
+}
+
+// Units are divided where a part saves at least `worth` stages (of 0.4 us; the launch in
+// clusters and the handing over cost 4 us) and the most units that there can be still
+// leave a third of the SMs idle: there the second launch loads ahead (one token of E4M3
+// experts, 4096 x 1024: 31.3 us as 64 units and 33.1 as 128 halves).  86 tokens of 8
+// experts of 5936 x 256 in E4M3: 47 -> 31 us; 2 of 304 x 1248: 15.0 -> 12.2.
+cudaError_t moe_layer_prepare(MoeLayerShape& s, int sms) {
+    constexpr int worth = 10;
     for (int down = 0; down < 2; ++down) {
-        const void* k = reinterpret_cast<const void*>(kernel_for(s, down != 0));
-        cudaFuncAttributes a;
-        cudaError_t e = cudaFuncGetAttributes(&a, k);
-        // the attribute is per kernel, shared by every plan: always the most
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-        if (e != cudaSuccess) return e;
+        const int rows = down ? 2 * kMoeRows : s.fp8 ? kMoeRows : kMoeRows / 2, step = s.fp8 ? 128 : down ? 64 : 128;
+        const int64_t units = static_cast<int64_t>(most_entries(s)) * (((down ? s.H : s.I) + rows - 1) / rows);
+        const int steps = ((down ? s.I : s.H) + step - 1) / step;
+        s.cluster[down] = 1;
+        s.grid[down] = sms;
+        cudaError_t e;
+        for (int c = 8; c > 1; c /= 2) {
+            if (units * c * 3 > sms * 2 || steps - steps / c < worth) continue;
+            const Kernel kernel = kernel_for(s, down != 0, true);
+            if ((e = prepare(kernel)) != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = static_cast<unsigned>(c);
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>(units * c), 1, 1);
+            cfg.blockDim = dim3(kMoeThreads, 1, 1);
+            cfg.dynamicSmemBytes = static_cast<size_t>(s.smem);
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+            if (n < units) continue;                  // they do not all find room at once
+            s.cluster[down] = c;
+            s.grid[down] = static_cast<int>(units) * c;
+            break;
+        }
+        if (s.cluster[down] == 1 && (e = prepare(kernel_for(s, down != 0, false))) != cudaSuccess) return e;
     }
     return preload(moe_sum_kernel);
 }
@@ -789,13 +907,16 @@ cudaError_t moe_layer_launch(const MoeLayerShape& s, const MoeParams& p, const v
     const uint64_t T = s.T, H = s.H, I = s.I, E = s.E, P = T * s.k * (s.fp8 ? 1 : 2);
     const uint32_t ke = s.fp8 ? 128 : 64;
     const uint64_t dx[] = {H, T}, d13[] = {H, 2 * I, E}, da[] = {I, P}, d2[] = {I, H, E};
-    const uint32_t row[] = {ke, 1}, box13[] = {ke, s.fp8 ? kMoeRows : kMoeRows / 2, 1}, box2[] = {ke, kMoeRows, 1};
+    const uint32_t row[] = {ke, 1}, box13[] = {ke, static_cast<uint32_t>(s.fp8 ? kMoeRows : kMoeRows / 2), 1}, box2[] = {ke, kMoeRows, 1};
     CUtensorMap mx, m13, ma, m2;
     if (!encode(enc, &mx, s.fp8, 2, x, dx, row) || !encode(enc, &m13, s.fp8, 3, w13, d13, box13) ||
         !encode(enc, &ma, s.fp8, 2, p.act, da, row) || !encode(enc, &m2, s.fp8, 3, w2, d2, box2))
         return cudaErrorInvalidValue;
-    cudaError_t e = layer_launch(kernel_for(s, false), s.grid, kMoeThreads, s.smem, 1, pdl, st, p, m13, mx);
-    if (e == cudaSuccess) e = layer_launch(kernel_for(s, true), s.grid, kMoeThreads, s.smem, 1, pdl, st, p, m2, ma);
+    MoeParams up = p, down = p;
+    up.cluster = s.cluster[0];
+    down.cluster = s.cluster[1];
+    cudaError_t e = layer_launch(kernel_for(s, false, up.cluster > 1), s.grid[0], kMoeThreads, s.smem, up.cluster, pdl, st, up, m13, mx);
+    if (e == cudaSuccess) e = layer_launch(kernel_for(s, true, down.cluster > 1), s.grid[1], kMoeThreads, s.smem, down.cluster, pdl, st, down, m2, ma);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((s.H + 4 * kSumThreads - 1) / (4 * kSumThreads), s.T, 1);

@@ -24,11 +24,13 @@ struct MoeLayerShape {
     int stages;       // of the ring
     int smem;
     int entries;      // most (expert, chunk of pairs) entries
-    int grid;
+    int cluster[2];   // CTAs of a cluster and of the grid, by launch
+    int grid[2];
     // workspace: byte offsets
     int64_t act;      // [pairs, I] E4M3, or [2, pairs, I] bf16: upper and lower parts
     int64_t act_sf;   // [pairs, I / 128] FP32 (E4M3)
     int64_t y;        // [pairs, H] FP32
+    int64_t parts;    // FP32 sums of units that are divided along K, a CTA's in a row
     int64_t bytes;
 };
 
@@ -41,6 +43,7 @@ struct MoeParams {
     uint8_t* act;
     float* act_sf;
     float* y;
+    float* parts;
     uint16_t* out;            // [T, H]
     int* status;
     int T;
@@ -50,13 +53,15 @@ struct MoeParams {
     int k;
     int entries;
     int stages;
+    int cluster;              // CTAs of a cluster of this launch
     int sentinel;
     long long wait_limit;     // cycles after which a wait gives up: kWaitCycles, or less to test that
 };
 
-// Fills the launch geometry and the workspace's layout from T .. fp8.
+// Fills the shared memory's and the workspace's layout from T .. fp8.
 void moe_layer_choose(MoeLayerShape& s, int sms);
-cudaError_t moe_layer_prepare(const MoeLayerShape& s);
+// Sets the kernels up and fills the launch geometry.
+cudaError_t moe_layer_prepare(MoeLayerShape& s, int sms);
 // The encoder of tensor maps that the driver has; NULL: it has none.
 void* moe_layer_encoder();
 cudaError_t moe_layer_launch(const MoeLayerShape& s, const MoeParams& p, const void* x, const void* w13, const void* w2,

@@ -149,7 +149,7 @@ int moe_small_layer_plan(moe_op_t* op, int64_t T, int64_t H, int64_t I, int E, i
     s.fp8 = e4m3;
     moe_layer_choose(s, p->sms);
     p->workspace = s.bytes;
-    return prepared(op, moe_layer_encoder() ? moe_layer_prepare(s) : cudaErrorNotSupported);
+    return prepared(op, moe_layer_encoder() ? moe_layer_prepare(s, p->sms) : cudaErrorNotSupported);
 }
 
 int moe_small_layer_set_wait_limit(moe_op_t op, int64_t limit_cycles) {
@@ -192,6 +192,7 @@ int moe_small_layer_run(moe_op_t op, const void* x, const float* x_sf, const int
     p.act = ws + s.act;
     p.act_sf = reinterpret_cast<float*>(ws + s.act_sf);
     p.y = reinterpret_cast<float*>(ws + s.y);
+    p.parts = reinterpret_cast<float*>(ws + s.parts);
     p.out = static_cast<uint16_t*>(out);
     p.status = op->status.words;
     p.T = s.T;

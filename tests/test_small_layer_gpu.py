@@ -85,6 +85,30 @@ def test_e4m3(T, H, I, E, k):
     layer.check(i)
 
 
+# few units of many steps along K: of the first product, of the second, of both; 16 to 128 columns
+LONG = [(1, 4104, 64, 1, 1), (5, 3088, 72, 2, 1), (3, 264, 2056, 2, 2), (20, 1808, 1000, 1, 1), (60, 2048, 704, 1, 1), (9, 1552, 136, 12, 1),
+        (120, 2048, 704, 1, 1), (300, 2608, 704, 2, 1)]
+LONG8 = [(1, 4112, 128, 1, 1), (5, 3088, 256, 2, 1), (3, 272, 2048, 2, 2), (20, 2064, 1536, 1, 1), (60, 1552, 1536, 1, 1),
+         (120, 2048, 1408, 1, 1), (300, 2608, 1408, 2, 1)]
+
+
+@pytest.mark.parametrize("T,H,I,E,k,fp8", [(*c, False) for c in LONG] + [(*c, True) for c in LONG8])
+def test_units_divided_along_k(T, H, I, E, k, fp8):
+    layer, i = Layer(T, H, I, E, k, fp8), inputs(T, H, I, E, k, fp8, seed=T)
+    layer.run(i)
+    layer.check(i)
+    first = layer.out.t.clone()
+    layer.plan.set_wait_limit(0)                      # each of a unit's CTAs gives up
+    layer.run(i)
+    torch.cuda.synchronize()
+    assert layer.plan.get_status() & mfr.STATUS_TIMEOUT
+    layer.plan.set_wait_limit(4_000_000_000)
+    for _ in range(20):
+        layer.run(i)
+    torch.cuda.synchronize()
+    assert layer.plan.get_status() == 0 and torch.equal(layer.out.t, first)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("T,E,k,share,skew", [(40, 16, 8, 0.4, 1.5), (5, 4, 2, 0.9, 0.0), (128, 4, 3, 0.2, 2.0)])
 def test_experts_elsewhere_and_popular_ones(T, E, k, share, skew, fp8):
