@@ -111,7 +111,7 @@ struct Shared {
     union {
         struct {                      // E4M3
             float sx[kFinishWarps][NB / 2];   // scales of a warp's columns
-            uint32_t top[2][4][8];            // largest magnitudes, by side, warp and column
+            uint32_t top[2][4][NB / 2];       // largest magnitudes, by side, warp and column
         };
         float up[2][8][64];           // bf16: the up rows' products, by side and column
     };
@@ -607,33 +607,48 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     for (int q = 0; q < NB / 16; ++q)
                         if (q < groups) add_parts(q, d0[q], d1[q]);
                 }
+                if constexpr (DOWN) {
 #pragma unroll
-                for (int q = 0; q < NB / 16; ++q) {
-                    const int c0 = q * 16 + side * 8;
-                    if (c0 >= en.n) break;
-                    if constexpr (DOWN) {
-                        to_y(c0, d0[q], d1[q]);
-                    } else {
-                        uint32_t(*top)[8] = s->top[side];
-                        const int i = tile * ROWS + row;
+                    for (int q = 0; q < NB / 16; ++q) {
+                        if (q >= groups) break;
+                        to_y(q * 16 + side * 8, d0[q], d1[q]);
+                    }
+                } else {
+                    uint32_t(*top)[HALF] = s->top[side];      // the last unit's were read before finishers_well
+                    const int i = tile * ROWS + row;
+#pragma unroll
+                    for (int q = 0; q < NB / 16; ++q) {
+                        if (q >= groups) break;
+                        uint32_t largest = 0;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             d0[q][j] = swiglu(d0[q][j], d1[q][j]);
                             const float m = fabsf(d0[q][j]);
                             const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, m == m ? __float_as_uint(m) : 0u);
-                            if (lane == j) top[quad][j] = t;
+                            if (lane == j) largest = t;
                         }
-                        group_sync(1 + side, 128);
+                        if (lane < 8) top[quad][q * 8 + lane] = largest;
+                    }
+                    group_sync(1 + side, 128);
+#pragma unroll
+                    for (int j = lane; j < HALF; j += 32) {
+                        const int col = (j >> 3) * 16 + side * 8 + (j & 7);
+                        if (col >= en.n) break;
+                        const uint32_t t = max(max(top[0][j], top[1][j]), max(top[2][j], top[3][j]));
+                        const float amax = fminf(fmaxf(__uint_as_float(t), kAmaxFloor), FLT_MAX);
+                        sx[j] = 448.f / amax;
+                        if (quad == 0) p.act_sf[static_cast<int64_t>(pairs[col]) * IB + tile] = amax / 448.f;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < NB / 16; ++q) {
+                        if (q >= groups) break;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            if (c0 + j >= en.n) break;
-                            const uint32_t t = max(max(top[0][j], top[1][j]), max(top[2][j], top[3][j]));
-                            const float amax = fminf(fmaxf(__uint_as_float(t), kAmaxFloor), FLT_MAX);
-                            const int pair = pairs[c0 + j];
-                            p.act[static_cast<int64_t>(pair) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[q][j] * (448.f / amax)));
-                            if (row == 0) p.act_sf[static_cast<int64_t>(pair) * IB + tile] = amax / 448.f;
+                            const int col = q * 16 + side * 8 + j;
+                            if (col >= en.n) break;
+                            p.act[static_cast<int64_t>(pairs[col]) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[q][j] * sx[q * 8 + j]));
                         }
-                        group_sync(1 + side, 128);
                     }
                 }
             } else {
