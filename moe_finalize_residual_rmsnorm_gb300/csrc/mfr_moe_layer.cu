@@ -52,6 +52,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <cmath>
 #include <mutex>
 
 #include "moe_step_ops.h"
@@ -835,9 +836,10 @@ static int most_entries(const MoeLayerShape& s) {
 
 void moe_layer_choose(MoeLayerShape& s, int sms) {
     const int64_t P = static_cast<int64_t>(s.T) * s.k;
-    // columns for twice an expert's mean share of the pairs: fewer leave more of the ring
-    // to the weights, and a popular expert's further chunks read its weights from L2
-    int64_t want = 2 * P / s.E + 8;
+    // columns for most experts' pairs, were they drawn evenly: fewer leave more of the ring to
+    // the weights, and a popular expert's further chunks read its weights from L2
+    const double mean = static_cast<double>(P) / s.E;
+    int64_t want = static_cast<int64_t>(mean + 3.0 * std::sqrt(mean) + 4.0);
     if (want > s.T) want = s.T;
     s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
     s.entries = (most_entries(s) + 3) & ~3;
