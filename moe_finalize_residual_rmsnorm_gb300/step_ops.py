@@ -96,8 +96,7 @@ class MoeLayerPlan(_OpPlan):
             self._stream(stream)), "moe_small_layer_run")
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+_HEADS = 24        # bytes of a moe_heads_t: address, token stride, head stride, 64 bits each
 
 
 class QkNormRopePlan(_OpPlan):
@@ -119,7 +118,7 @@ class QkNormRopePlan(_OpPlan):
                    debug_checks=debug_checks)
         self._need = self.workspace_bytes()
 
-    def _heads(self, name: str, t, heads: int):
+    def _heads(self, name: str, t, heads: int) -> tuple:
         shape = (self.T, heads, self.D)
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
@@ -131,7 +130,7 @@ class QkNormRopePlan(_OpPlan):
         if one != 1 or token < 0 or head < 0:
             raise ValueError(f"{name}: the elements of a head must lie together, got strides {t.stride()}")
         # the stride of a dimension of one is never taken
-        return ctypes.byref(_Heads(t.data_ptr(), token if self.T > 1 else 0, head if heads > 1 else 0))
+        return t.data_ptr(), token if self.T > 1 else 0, head if heads > 1 else 0
 
     def _shared(self, gamma_q, gamma_k, cos_sin, positions):
         dt, dev, D = self.dtype, self.device, (self.D,)
@@ -144,10 +143,12 @@ class QkNormRopePlan(_OpPlan):
         gammas [D], cos_sin FP32 [max_positions, rotary_dim] (cosines, then sines),
         positions int32 [T] -> q_out, k_out (may be q and k)."""
         gq, gk, table, pos = self._shared(gamma_q, gamma_k, cos_sin, positions)
-        _check(self._lib.moe_qk_norm_rope_run(
-            self._h, self._heads("q", q, self.heads_q), self._heads("k", k, self.heads_k), gq, gk, eps, table, pos,
-            self._heads("q_out", q_out, self.heads_q), self._heads("k_out", k_out, self.heads_k), self._stream(stream)),
-            "moe_qk_norm_rope_run")
+        hq, hk = self.heads_q, self.heads_k
+        heads = array("q", (*self._heads("q", q, hq), *self._heads("k", k, hk), *self._heads("q_out", q_out, hq),
+                            *self._heads("k_out", k_out, hk)))
+        at = heads.buffer_info()[0]
+        _check(self._lib.moe_qk_norm_rope_run(self._h, at, at + _HEADS, gq, gk, eps, table, pos, at + 2 * _HEADS,
+                                              at + 3 * _HEADS, self._stream(stream)), "moe_qk_norm_rope_run")
 
     def run_grad(self, d_q_out, d_k_out, q, k, gamma_q, gamma_k, eps: float, cos_sin, positions, d_q, d_k, d_gamma_q,
                  d_gamma_k, workspace, stream=None) -> None:
@@ -156,12 +157,14 @@ class QkNormRopePlan(_OpPlan):
         f32, dev = torch.float32, self.device
         gq, gk, table, pos = self._shared(gamma_q, gamma_k, cos_sin, positions)
         ws, ws_bytes = _workspace(workspace, self._need, dev)
+        hq, hk = self.heads_q, self.heads_k
+        heads = array("q", (*self._heads("d_q_out", d_q_out, hq), *self._heads("d_k_out", d_k_out, hk), *self._heads("q", q, hq),
+                            *self._heads("k", k, hk), *self._heads("d_q", d_q, hq), *self._heads("d_k", d_k, hk)))
+        at = heads.buffer_info()[0]
         _check(self._lib.moe_qk_norm_rope_grad_run(
-            self._h, self._heads("d_q_out", d_q_out, self.heads_q), self._heads("d_k_out", d_k_out, self.heads_k),
-            self._heads("q", q, self.heads_q), self._heads("k", k, self.heads_k), gq, gk, eps, table, pos,
-            self._heads("d_q", d_q, self.heads_q), self._heads("d_k", d_k, self.heads_k),
-            _tensor("d_gamma_q", d_gamma_q, f32, (self.D,), dev), _tensor("d_gamma_k", d_gamma_k, f32, (self.D,), dev), ws,
-            ws_bytes, self._stream(stream)), "moe_qk_norm_rope_grad_run")
+            self._h, at, at + _HEADS, at + 2 * _HEADS, at + 3 * _HEADS, gq, gk, eps, table, pos, at + 4 * _HEADS,
+            at + 5 * _HEADS, _tensor("d_gamma_q", d_gamma_q, f32, (self.D,), dev),
+            _tensor("d_gamma_k", d_gamma_k, f32, (self.D,), dev), ws, ws_bytes, self._stream(stream)), "moe_qk_norm_rope_grad_run")
 
 
 _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}

@@ -7,7 +7,6 @@ import torch
 
 import moe_finalize_residual_rmsnorm_gb300 as mfr
 import step_ref as ref
-from moe_finalize_residual_rmsnorm_gb300.step_ops import _Heads
 from test_layer_ops_gpu import B16, F32, I32, Guarded, randn
 
 pytestmark = pytest.mark.gpu
@@ -26,6 +25,10 @@ def _library():
 def table(most, rotary):
     a = torch.arange(most, dtype=torch.float64)[:, None] * 100.0 ** (-torch.arange(rotary // 2, dtype=torch.float64) / max(1, rotary))
     return torch.cat([torch.cos(a), torch.sin(a)], 1).float().cuda()
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class Case:
