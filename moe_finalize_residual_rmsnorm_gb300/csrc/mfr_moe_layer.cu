@@ -30,7 +30,7 @@
 // Measured on GB300 (4096 x 1024 weights an expert, bf16, copy rate 6782 GB/s): 16 tokens
 // of 128 experts 304 us (1.0 of the copy rate), 64 of 64 experts 244 us (0.97), one
 // token of 64 experts 38 us (0.78: two launches' starts, sorts and first loads, 8 us); 128
-// tokens of 64 experts of 8192 x 1024 in E4M3 274 us (0.87: 512 units are 3.4 turns of the
+// tokens of 64 experts of 8192 x 1024 in E4M3 268 us (0.89: 512 units are 3.4 turns of the
 // SMs).  With units for few SMs one SM takes 60-70 GB/s: a stage's eight products are
 // 330 cycles whatever their columns (the weights are read from shared memory for each), and
 // hand-overs 200 more.
@@ -39,7 +39,8 @@
 // trip: one token 54 us that way and 42 this, 37 tokens 85 and 51, 128 in E4M3 378 and
 // 289); adding the pairs in the second launch by the last CTA of a tile (128 tokens: 50
 // us at its end); two CTAs an SM, so that the launches overlap (half the ring each: one
-// token 52 us); fetching w2 to L2 at the first launch's end (no difference); units of 32
+// token 52 us); fetching w2 to L2 at the first launch's end (no difference) or further
+// ahead of the ring while waiting for it (8 to 64 stages: 2 to 4 % slower); units of 32
 // or 64 columns of h and 128 rows of D, in E4M3 with clusters that share a group's
 // largest magnitude (25 shapes 5 % slower: more copies, and in E4M3 more steps, a byte);
 // clusters of two for every call, which divide the last, partial turn (3 % slower).
