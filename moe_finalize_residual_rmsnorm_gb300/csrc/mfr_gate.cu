@@ -16,7 +16,7 @@
 // Bytes would bound both directions (32768 x 256: 5 us), but the choice's instructions
 // do: 22 us with a bias, 17 without (k = 8; taking the k experts one by one: 50).  The
 // gradient of renormalised softmax weights reads the chosen logits alone (16385 x 128:
-// 6.3 us, 2.6 of bytes, bound by its instructions as well).
+// 5.8 us, 2.6 of bytes, bound by its instructions as well).
 #include <cfloat>
 
 #include "moe_step_ops.h"
@@ -95,6 +95,13 @@ __device__ __forceinline__ float near_sigmoid(float l) {
 
 __device__ __forceinline__ float warp_max(float v) {
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+    return v;
+}
+
+// Sum over a token's slots, a lane each, for the lanes that may have one.
+__device__ __forceinline__ float slots_sum(float v) {
+#pragma unroll
+    for (int off = kMaxK / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     return v;
 }
 
@@ -334,11 +341,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, N <= 8 ? kGateCtas : 1) gate_
             if (p.renormalize) top = __shfl_sync(0xFFFFFFFFu, w, 0);   // the first chosen is the largest
             w = mine >= 0 ? expf(w - top) : 0.f;
         }
-        if (p.renormalize) {
-            denominator = w;                              // of the 16 lanes that may have one
-#pragma unroll
-            for (int off = kMaxK / 2; off > 0; off >>= 1) denominator += __shfl_xor_sync(0xFFFFFFFFu, denominator, off);
-        }
+        if (p.renormalize) denominator = slots_sum(w);
         if (lane < p.k) {
             p.ids[t * p.k + lane] = mine;
             p.w[t * p.k + lane] = w > 0.f ? p.scale * (w * reciprocal(denominator)) : 0.f;
@@ -383,18 +386,18 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GatePa
         if (p.renormalize) {
             const float m = warp_max(x);                  // all lanes, those without a slot too
             q = on ? shared_sigmoid(le, m) : 0.f;
-            const float total = warp_allreduce_sum(q);
-            q = total > 0.f ? q / total : 0.f;
-            d = g - warp_allreduce_sum(g * q);
+            const float total = slots_sum(q);
+            q = total > 0.f ? q * reciprocal(total) : 0.f;
+            d = g - slots_sum(g * q);
         }
         d = on ? d * q * sigmoid(-le) : 0.f;
     } else if (p.renormalize) {
         float m = warp_max(x);
         m = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
         float q = x > -INFINITY ? expf(le - m) : 0.f;
-        const float total = warp_allreduce_sum(q);
-        q = total > 0.f ? q / total : 0.f;
-        d = q * (g - warp_allreduce_sum(g * q));
+        const float total = slots_sum(q);
+        q = total > 0.f ? q * reciprocal(total) : 0.f;
+        d = q * (g - slots_sum(g * q));
     } else {
         float m = -INFINITY;
 #pragma unroll
@@ -407,24 +410,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const GatePa
             l[i] = l[i] > -INFINITY ? expf(fminf(l[i], FLT_MAX) - m) : 0.f;
             sum += l[i];
         }
-        const float inv = 1.f / fmaxf(warp_allreduce_sum(sum), FLT_MIN);
+        const float inv = reciprocal(fmaxf(warp_allreduce_sum(sum), FLT_MIN));
         const float q = x > -INFINITY ? expf(le - m) * inv : 0.f;
-        const float mean = warp_allreduce_sum(g * q);
+        const float mean = warp_allreduce_sum(g * q);      // every lane wants it
         all = -mean * inv;
         own = -mean * q;
         d = q * g;
     }
     // the same expert in several slots: the first of them has the sum
     float mine = d;
-    bool first = on;
-    for (int j = 0; j < p.k; ++j) {
-        const float v = __shfl_sync(0xFFFFFFFFu, d, j);
-        const int other = __shfl_sync(0xFFFFFFFFu, e, j);
-        if (other == e && j != lane) {
-            mine += v;
-            first = first && j > lane;
+    uint32_t same = 0;                                    // slots
+    for (int j = 0; j < p.k; ++j) same |= (__shfl_sync(0xFFFFFFFFu, e, j) == e ? 1u : 0u) << j;
+    const bool first = on && lane == __ffs(same) - 1;
+    if (__any_sync(0xFFFFFFFFu, on && (same & (same - 1)) != 0))
+        for (int j = 0; j < p.k; ++j) {
+            const float v = __shfl_sync(0xFFFFFFFFu, d, j);
+            if ((same >> j & 1u) && j != lane) mine += v;
         }
-    }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int from = (v * 32 + lane) * V;
