@@ -21,7 +21,7 @@
 // second launch adds their sums in a fixed order.
 // Measured on GB300, of the copy rate: 16384 x 40 heads x 128 out of a packed tensor 58.5
 // us (0.87; 61 without the prefetch to L2), its gradient at 8192 tokens 48.5 us (0.78); 4097
-// x 28 x 80 gradient 21 us (0.39: 2.5 units a warp, whose first loads nothing covers, 500
+// x 28 x 80 gradient 21 us (0.39: 2.5 units a warp, whose first loads nothing covers, 390
 // instructions a group of heads, and 3 us for the second launch).  Loads wait: 22 warps an
 // SM have 24 KB in flight in registers.  Three or four groups at a time (64, 67 us), more
 // warps of fewer registers (67), refilling a group's registers as soon as it is in use
