@@ -835,7 +835,7 @@ static int most_entries(const MoeLayerShape& s) {
     return std::min(P, std::min(P, s.E) + P / s.columns);
 }
 
-void moe_layer_choose(MoeLayerShape& s, int sms) {
+void moe_layer_choose(MoeLayerShape& s) {
     const int64_t P = static_cast<int64_t>(s.T) * s.k;
     // columns for most experts' pairs, were they drawn evenly: fewer leave more of the ring to
     // the weights, and a popular expert's further chunks read its weights from L2
@@ -853,7 +853,6 @@ void moe_layer_choose(MoeLayerShape& s, int sms) {
     s.act_sf = align256(P * s.I * (s.fp8 ? 1 : 4));
     s.y = s.act_sf + (s.fp8 ? align256(P * (s.I / 128) * 4) : 0);
     s.parts = s.y + align256(P * s.H * 4);
-    s.bytes = s.parts + static_cast<int64_t>(sms) * kFinishWarps * (s.columns / 16) * 512 * 4;
 }
 
 void* moe_layer_encoder() {
@@ -885,6 +884,7 @@ static cudaError_t prepare(Kernel kernel) {
 // experts of 5936 x 256 in E4M3: 47 -> 31 us; 2 of 304 x 1248: 15.0 -> 12.2.
 cudaError_t moe_layer_prepare(MoeLayerShape& s, int sms) {
     constexpr int worth = 10;
+    s.bytes = s.parts;
     for (int down = 0; down < 2; ++down) {
         const int rows = down ? 2 * kMoeRows : s.fp8 ? kMoeRows : kMoeRows / 2, step = s.fp8 ? 128 : down ? 64 : 128;
         const int64_t units = static_cast<int64_t>(most_entries(s)) * (((down ? s.H : s.I) + rows - 1) / rows);
@@ -911,6 +911,7 @@ cudaError_t moe_layer_prepare(MoeLayerShape& s, int sms) {
             if (n < units) continue;                  // they do not all find room at once
             s.cluster[down] = c;
             s.grid[down] = static_cast<int>(units) * c;
+            s.bytes = std::max(s.bytes, s.parts + int64_t(s.grid[down]) * kFinishWarps * (s.columns / 16) * 512 * 4);
             break;
         }
         if (s.cluster[down] == 1 && (e = prepare(kernel_for(s, down != 0, false))) != cudaSuccess) return e;

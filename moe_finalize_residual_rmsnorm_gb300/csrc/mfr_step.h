@@ -30,7 +30,7 @@ struct MoeLayerShape {
     int64_t act;      // [pairs, I] E4M3, or [2, pairs, I] bf16: upper and lower parts
     int64_t act_sf;   // [pairs, I / 128] FP32 (E4M3)
     int64_t y;        // [pairs, H] FP32
-    int64_t parts;    // FP32 sums of units that are divided along K, a CTA's in a row
+    int64_t parts;    // FP32 sums of units that are divided along K, a CTA's in a row; or nothing
     int64_t bytes;
 };
 
@@ -59,8 +59,8 @@ struct MoeParams {
 };
 
 // Fills the shared memory's and the workspace's layout from T .. fp8.
-void moe_layer_choose(MoeLayerShape& s, int sms);
-// Sets the kernels up and fills the launch geometry.
+void moe_layer_choose(MoeLayerShape& s);
+// Sets the kernels up and fills the launch geometry and the workspace's size.
 cudaError_t moe_layer_prepare(MoeLayerShape& s, int sms);
 // The encoder of tensor maps that the driver has; NULL: it has none.
 void* moe_layer_encoder();

@@ -147,9 +147,10 @@ int moe_small_layer_plan(moe_op_t* op, int64_t T, int64_t H, int64_t I, int E, i
     s.E = E;
     s.k = k;
     s.fp8 = e4m3;
-    moe_layer_choose(s, p->sms);
-    p->workspace = s.bytes;
-    return prepared(op, moe_layer_encoder() ? moe_layer_prepare(s, p->sms) : cudaErrorNotSupported);
+    moe_layer_choose(s);
+    rc = prepared(op, moe_layer_encoder() ? moe_layer_prepare(s, p->sms) : cudaErrorNotSupported);
+    if (rc == MFR_OK) p->workspace = s.bytes;
+    return rc;
 }
 
 int moe_small_layer_set_wait_limit(moe_op_t op, int64_t limit_cycles) {
