@@ -226,6 +226,25 @@ def test_captured_replayed_and_on_another_stream(pdl):
     layer.check(a)
 
 
+@pytest.mark.parametrize("pdl", [True, False])
+@pytest.mark.parametrize("T,H,I,E,k,fp8", [(5, 3088, 72, 2, 1, False), (3, 264, 2056, 2, 2, False), (20, 2064, 1536, 1, 1, True)])
+def test_divided_units_captured_and_beside_others(T, H, I, E, k, fp8, pdl):
+    layer, other = Layer(T, H, I, E, k, fp8, enable_pdl=pdl), Layer(16, 1024, 512, 16, 4)
+    i, j = inputs(T, H, I, E, k, fp8, seed=1), inputs(16, 1024, 512, 16, 4, seed=2)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        for _ in range(5):
+            layer.run(i)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            g.replay()
+        other.run(j)
+    other.check(j)
+    layer.check(i)
+
+
 def test_two_plans_at_once():
     """Calls on two streams, each with its own workspace, sharing the SMs and tensor memory."""
     shapes = [(16, 1024, 512, 16, 4), (100, 512, 256, 8, 8)]
