@@ -102,7 +102,7 @@ constexpr uint32_t tmem_columns() {
 }
 
 // Behind the ring.
-template <int NB>
+template <bool FP8, int NB>
 struct Shared {
     uint64_t full[kRingStages], empty[kRingStages];
     uint64_t done[kMaxTurns], taken[kMaxTurns];       // an accumulator is complete; its values are in registers
@@ -117,7 +117,9 @@ struct Shared {
             float sx[kFinishWarps][NB / 2];   // scales of a warp's columns
             uint32_t top[2][4][NB / 2];       // largest magnitudes, by side, warp and column
         };
-        float up[2][8][64];           // bf16: the up rows' products, by side and column
+        // bf16: products that gate and up rows' lanes exchange, by side, turn and column;
+        // two turns, so that one barrier does, where there are several
+        float other[2][!FP8 && NB > 16 ? 2 : 1][8][FP8 ? 1 : 64];
     };
 };
 
@@ -172,8 +174,8 @@ __device__ __forceinline__ bool valid_expert(int id, int E) { return static_cast
 // the pairs, `entries` the chunks of at most NB of them; returns their number.
 // `hist`: [kWarps + 1][E], and behind it the pairs' ids and their places among their
 // warp's pairs of the same expert.  All threads call it.
-template <int NB>
-__device__ int sort_pairs(const MoeParams& p, Shared<NB>* s, uint16_t* list, uint32_t* entries, int* hist, bool report) {
+template <bool FP8, int NB>
+__device__ int sort_pairs(const MoeParams& p, Shared<FP8, NB>* s, uint16_t* list, uint32_t* entries, int* hist, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.T * p.k, E = p.E;
     const int seg = ((P + kWarps - 1) / kWarps + 31) & ~31, first = warp * seg, last = min(P, first + seg);
@@ -283,8 +285,8 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
     const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
     const int S = p.stages;
     unsigned char* behind = raw + (ring - smem_addr(raw)) + S * STAGE;
-    Shared<NB>* s = reinterpret_cast<Shared<NB>*>(behind);
-    uint32_t* entries = reinterpret_cast<uint32_t*>(behind + sizeof(Shared<NB>));
+    Shared<FP8, NB>* s = reinterpret_cast<Shared<FP8, NB>*>(behind);
+    uint32_t* entries = reinterpret_cast<uint32_t*>(behind + sizeof(Shared<FP8, NB>));
     uint16_t* list = reinterpret_cast<uint16_t*>(entries + p.entries);
     int* hist = reinterpret_cast<int*>(raw + (ring - smem_addr(raw)));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -367,7 +369,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             load_weights(M, M * tiles, S);
         }
     } else {
-        M = sort_pairs<NB>(p, s, list, entries, hist, report);
+        M = sort_pairs<FP8, NB>(p, s, list, entries, hist, report);
         shared_proxy_fence();         // the ring's memory held the counts
     }
     tcgen05_fence_before();
@@ -694,27 +696,28 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     if constexpr (DOWN) {
                         to_y(c0, v0, v1);
                     } else {
-                        // lanes 64 .. 127 hold the up rows
-                        float(*up)[64] = s->up[side];
-                        if (row >= 64)
+                        // lanes 0 .. 63 hold gate rows and finish columns 0 .. 3, lanes 64 .. 127 hold up
+                        // rows and finish 4 .. 7
+                        float(*other)[64] = s->other[side][NB > 16 ? q & 1 : 0];
+                        const bool gates = row < 64;
+                        const int r = row & 63, i = tile * ROWS + r;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) up[j][row - 64] = v0[j];
+                        for (int j = 0; j < 4; ++j) other[gates ? 4 + j : j][r] = gates ? v0[4 + j] : v0[j];
                         group_sync(1 + side, 128);
-                        const int i = tile * ROWS + row;
-                        if (row < 64 && i < I) {
+                        if (i < I) {
                             __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(p.act);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                if (c0 + j >= en.n) break;
-                                const float h = swiglu(v0[j], up[j][row]);
-                                const int64_t pair = pairs[c0 + j];
+                            for (int j = 0; j < 4; ++j) {
+                                const int col = c0 + (gates ? j : 4 + j);
+                                if (col >= en.n) break;
+                                const float h = gates ? swiglu(v0[j], other[j][r]) : swiglu(other[4 + j][r], v0[4 + j]);
+                                const int64_t pair = pairs[col];
                                 const __nv_bfloat16 high = __float2bfloat16_rn(h);
                                 act[pair * I + i] = high;
                                 // an infinity is whole in its upper part
                                 act[(pair + P) * I + i] = __float2bfloat16_rn(fabsf(h) < INFINITY ? h - __bfloat162float(high) : 0.f);
                             }
                         }
-                        group_sync(1 + side, 128);
                     }
                 }
                 tcgen05_fence_before();
@@ -803,9 +806,10 @@ Kernel kernel_for(const MoeLayerShape& s, bool down, bool joint) {
 
 constexpr int kMaxSmem = 227 * 1024;
 
+template <bool FP8>
 int shared_bytes(int columns) {
-    return static_cast<int>(columns == 16 ? sizeof(Shared<16>) : columns == 32 ? sizeof(Shared<32>)
-                            : columns == 64 ? sizeof(Shared<64>) : sizeof(Shared<128>));
+    return static_cast<int>(columns == 16 ? sizeof(Shared<FP8, 16>) : columns == 32 ? sizeof(Shared<FP8, 32>)
+                            : columns == 64 ? sizeof(Shared<FP8, 64>) : sizeof(Shared<FP8, 128>));
 }
 
 bool encode(void* encoder, CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint32_t* box) {
@@ -846,7 +850,7 @@ void moe_layer_choose(MoeLayerShape& s) {
     if (want > s.T) want = s.T;
     s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
     s.entries = (most_entries(s) + 3) & ~3;
-    const int behind = shared_bytes(s.columns) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
+    const int behind = (s.fp8 ? shared_bytes<true>(s.columns) : shared_bytes<false>(s.columns)) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
     const int stage = 2 * kPanel + s.columns * 128 * (s.fp8 ? 1 : 2);
     s.stages = (kMaxSmem - 1024 - behind) / stage;
     if (s.stages > kRingStages) s.stages = kRingStages;
