@@ -11,7 +11,8 @@
 // expert those bytes bound the layer, so the weights are the streamed operand:
 // they are the 128 rows of the product's A, and the expert's pairs its 16 .. 128
 // columns (B).  One warp keeps a ring of stages of 32 KB of weights filled by
-// tensor-map copies, one gathers the pairs' rows next to them, four a copy, one
+// tensor-map copies, one loads the pairs' rows next to them (x by gathers of four, h,
+// which the first launch leaves in the sorted order, 16 a copy), one
 // thread issues tcgen05 products into tensor memory, and eight warps finish one
 // unit while the next one is multiplied.
 //
@@ -394,26 +395,33 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
         int i = 0, st = 0, parity = 1;
         for (int u = U0; ok && u < units; u += G) {
             const Entry en = unpack_entry(entries[u % M]);
-            int v[4];
+            // x by tokens, four rows a copy (lane n: 4 n and on); h lies in the list's order, 16 a copy
+            int4 r = make_int4(0, 0, 0, 0);
+            if constexpr (!DOWN) {
+                int v[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int pair = list[en.start + min(4 * lane + n, en.n - 1)];
-                v[n] = DOWN ? pair : pair / p.k;
+                for (int n = 0; n < 4; ++n) v[n] = list[en.start + min(4 * lane + n, en.n - 1)] / p.k;
+                r = make_int4(v[0], v[1], v[2], v[3]);
             }
-            const int4 r = make_int4(v[0], v[1], v[2], v[3]);
-            const int4 r2 = DOWN ? make_int4(v[0] + P, v[1] + P, v[2] + P, v[3] + P) : r;     // lower parts
-            const int gathers = (en.n + 3) >> 2;
+            const int copies = DOWN ? (en.n + 15) >> 4 : (en.n + 3) >> 2;
+            constexpr int COPY = DOWN ? 2048 : 512;
             const uint32_t second = ring + 2 * kPanel + (STACKED ? (en.n + 15) & ~15 : NB) * 128;
             for (int kb = K0; kb < K1; ++kb, ++i) {
                 if (i >= S) ok = role_wait(&s->dead, p, smem_addr(&s->empty[st]), parity);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const uint32_t bar = smem_addr(&s->full[st]), b = ring + st * STAGE + 2 * kPanel;
-                if (lane == 0) mbar_arrive_expect_tx(bar, gathers * (FP8 ? 512 : 1024));
+                if (lane == 0) mbar_arrive_expect_tx(bar, copies * COPY * (FP8 ? 1 : 2));
                 __syncwarp();
-                if (lane < gathers) {
-                    map_gather4(b + lane * 512, &rows, kb * KS, r, bar);
-                    if constexpr (!FP8) map_gather4(second + st * STAGE + lane * 512, &rows, kb * KS + (GATES ? KE : 0), r2, bar);
+                if (lane < copies) {
+                    const uint32_t b2 = second + st * STAGE + lane * COPY;
+                    if constexpr (DOWN) {
+                        map_load2(b + lane * COPY, &rows, kb * KS, en.start + lane * 16, bar);
+                        if constexpr (!FP8) map_load2(b2, &rows, kb * KS, P + en.start + lane * 16, bar);      // the lower parts
+                    } else {
+                        map_gather4(b + lane * COPY, &rows, kb * KS, r, bar);
+                        if constexpr (!FP8) map_gather4(b2, &rows, kb * KS + KE, r, bar);
+                    }
                 }
                 if (++st == S) {
                     st = 0;
@@ -531,8 +539,8 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int j = (lane + 32 * i) & (HALF - 1);
-                    const int pair = pairs[min((j >> 3) * 16 + side * 8 + (j & 7), en.n - 1)];
-                    from[i] = DOWN ? p.act_sf + static_cast<int64_t>(pair) * KB : p.x_sf + static_cast<int64_t>(pair / p.k) * KB;
+                    const int at = min((j >> 3) * 16 + side * 8 + (j & 7), en.n - 1);
+                    from[i] = DOWN ? p.act_sf + static_cast<int64_t>(en.start + at) * KB : p.x_sf + static_cast<int64_t>(pairs[at] / p.k) * KB;
                 }
                 const float* w0 = DOWN ? p.w2_sf + (static_cast<int64_t>(en.expert) * HB + 2 * tile) * IB
                                        : p.w13_sf + (static_cast<int64_t>(en.expert) * 2 * IB + tile) * HB;
@@ -643,7 +651,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         const uint32_t t = max(max(top[0][j], top[1][j]), max(top[2][j], top[3][j]));
                         const float amax = fminf(fmaxf(__uint_as_float(t), kAmaxFloor), FLT_MAX);
                         sx[j] = 448.f / amax;
-                        if (quad == 0) p.act_sf[static_cast<int64_t>(pairs[col]) * IB + tile] = amax / 448.f;
+                        if (quad == 0) p.act_sf[static_cast<int64_t>(en.start + col) * IB + tile] = amax / 448.f;
                     }
                     __syncwarp();
 #pragma unroll
@@ -653,7 +661,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         for (int j = 0; j < 8; ++j) {
                             const int col = q * 16 + side * 8 + j;
                             if (col >= en.n) break;
-                            p.act[static_cast<int64_t>(pairs[col]) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[q][j] * sx[q * 8 + j]));
+                            p.act[static_cast<int64_t>(en.start + col) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[q][j] * sx[q * 8 + j]));
                         }
                     }
                 }
@@ -711,11 +719,11 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                                 const int col = c0 + (gates ? j : 4 + j);
                                 if (col >= en.n) break;
                                 const float h = gates ? swiglu(v0[j], other[j][r]) : swiglu(other[4 + j][r], v0[4 + j]);
-                                const int64_t pair = pairs[col];
+                                const int64_t at = en.start + col;
                                 const __nv_bfloat16 high = __float2bfloat16_rn(h);
-                                act[pair * I + i] = high;
+                                act[at * I + i] = high;
                                 // an infinity is whole in its upper part
-                                act[(pair + P) * I + i] = __float2bfloat16_rn(fabsf(h) < INFINITY ? h - __bfloat162float(high) : 0.f);
+                                act[(at + P) * I + i] = __float2bfloat16_rn(fabsf(h) < INFINITY ? h - __bfloat162float(high) : 0.f);
                             }
                         }
                     }
@@ -933,9 +941,10 @@ cudaError_t moe_layer_launch(const MoeLayerShape& s, const MoeParams& p, const v
     const uint32_t ke = s.fp8 ? 128 : 64;
     const uint64_t dx[] = {H, T}, d13[] = {H, 2 * I, E}, da[] = {I, P}, d2[] = {I, H, E};
     const uint32_t row[] = {ke, 1}, box13[] = {ke, static_cast<uint32_t>(s.fp8 ? kMoeRows : kMoeRows / 2), 1}, box2[] = {ke, kMoeRows, 1};
+    const uint32_t rows16[] = {ke, 16};
     CUtensorMap mx, m13, ma, m2;
     if (!encode(enc, &mx, s.fp8, 2, x, dx, row) || !encode(enc, &m13, s.fp8, 3, w13, d13, box13) ||
-        !encode(enc, &ma, s.fp8, 2, p.act, da, row) || !encode(enc, &m2, s.fp8, 3, w2, d2, box2))
+        !encode(enc, &ma, s.fp8, 2, p.act, da, rows16) || !encode(enc, &m2, s.fp8, 3, w2, d2, box2))
         return cudaErrorInvalidValue;
     MoeParams up = p, down = p;
     up.cluster = s.cluster[0];

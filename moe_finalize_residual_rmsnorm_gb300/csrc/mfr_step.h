@@ -27,7 +27,7 @@ struct MoeLayerShape {
     int cluster[2];   // CTAs of a cluster and of the grid, by launch
     int grid[2];
     // workspace: byte offsets
-    int64_t act;      // [pairs, I] E4M3, or [2, pairs, I] bf16: upper and lower parts
+    int64_t act;      // [pairs, I] E4M3, or [2, pairs, I] bf16: upper and lower parts; pairs sorted by expert
     int64_t act_sf;   // [pairs, I / 128] FP32 (E4M3)
     int64_t y;        // [pairs, H] FP32
     int64_t parts;    // FP32 sums of units that are divided along K, a CTA's in a row; or nothing
