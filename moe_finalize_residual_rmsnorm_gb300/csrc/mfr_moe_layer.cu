@@ -11,10 +11,10 @@
 // expert those bytes bound the layer, so the weights are the streamed operand:
 // they are the 128 rows of the product's A, and the expert's pairs its 16 .. 128
 // columns (B).  One warp keeps a ring of stages of 32 KB of weights filled by
-// tensor-map copies, one loads the pairs' rows next to them (x by gathers of four, h,
-// which the first launch leaves in the sorted order, 16 a copy), one
-// thread issues tcgen05 products into tensor memory, and eight warps finish one
-// unit while the next one is multiplied.
+// tensor-map copies, one loads the pairs' rows next to them (x by gathers of four; h,
+// which the first launch leaves in the sorted order, 16 a copy), one thread issues tcgen05
+// products into tensor memory, and eight warps finish one unit while the next one is
+// multiplied.
 //
 // Each CTA sorts the pairs by expert itself (at most 4096, from L2), so that no
 // launch before it is needed; up to 32 of them are one warp's, which asks for its first
@@ -27,7 +27,8 @@
 //                  before it waits for the first launch
 //   then the pairs of every token are added in slot order, by a small third launch:
 //                  no atomics, the same bits in every call
-// Where units are few and long, the CTAs of a cluster take a part of K each.
+// bf16 calls with many pairs an expert have a launch before these, which copies their rows
+// of x in the sorted order.  Where units are few and long, the CTAs of a cluster take a part of K each.
 // Measured on GB300 (4096 x 1024 weights an expert, bf16, copy rate 6782 GB/s): 16 tokens
 // of 128 experts 304 us (1.0 of the copy rate), 64 of 64 experts 244 us (0.97), one
 // token of 64 experts 38 us (0.78: two launches' starts, sorts and first loads, 8 us); 128
@@ -267,12 +268,47 @@ __device__ __forceinline__ int sort_few(const MoeParams& p, uint16_t* list, uint
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
+// bf16 with many pairs an expert: their rows of x are put in the sorted order by a launch
+// of their own, because gathers of four rows take 23 ns each, 128 rows of a stage 1.5 us
+// (256 tokens of 16 experts of 4096 x 1024: 269 us with gathers and 140 so, of 8 of 1024 x
+// 1024: 63 and 41; with 64 columns between 5 % faster and 4 % slower, and slower in E4M3,
+// whose stages take half the gathers).
+constexpr bool copied(bool fp8, int columns) { return !fp8 && columns == 128; }
+
+__global__ void __launch_bounds__(kMoeThreads, 1) moe_rows_kernel(const MoeParams p, const uint8_t* x) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    Shared<false, 128>* s = reinterpret_cast<Shared<false, 128>*>(raw);
+    uint32_t* entries = reinterpret_cast<uint32_t*>(raw + sizeof(Shared<false, 128>));
+    int* hist = reinterpret_cast<int*>(entries + p.entries);
+    uint16_t* list = reinterpret_cast<uint16_t*>(hist + (kWarps + 1) * p.E) + 3 * p.T * p.k;       // behind the ids and places
+    pdl_wait();
+    pdl_launch_dependents();
+    const int M = sort_pairs<false, 128>(p, s, list, entries, hist, false);
+    __syncthreads();
+    if (M == 0) return;
+    const Entry last = unpack_entry(entries[M - 1]);
+    const int lane = threadIdx.x & 31, pairs = last.start + last.n, bytes = p.H * 2;
+    for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < pairs; i += gridDim.x * kWarps) {
+        const uint8_t* from = x + static_cast<int64_t>(list[i] / p.k) * bytes;
+        uint8_t* to = p.rows + static_cast<int64_t>(i) * bytes;
+        for (int b = lane * 16; b < bytes; b += 4 * 512) {
+            uint4 v[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] = ld_stream_u4_if(from + b + n * 512, b + n * 512 < bytes);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if (b + n * 512 < bytes) *reinterpret_cast<uint4*>(to + b + n * 512) = v[n];
+        }
+    }
+}
+
 // One launch of products.  DOWN: the second one.  JOINT: the CTAs of a cluster have one
 // unit, a part of K each, and the first adds the others' sums to its own.
 template <bool FP8, bool DOWN, int NB, bool JOINT>
 __global__ void __launch_bounds__(kMoeThreads, 1)
 moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights, const __grid_constant__ CUtensorMap rows) {
     constexpr bool GATES = !FP8 && !DOWN;            // gate and up rows in one accumulator, two steps of K a stage
+    constexpr bool LATER = DOWN || copied(FP8, NB);     // a launch before it writes its rows, in the list's order
     constexpr int KE = FP8 ? 128 : 64;               // elements of 128 bytes of K
     constexpr int KS = GATES ? 2 * KE : KE;          // of a stage
     constexpr int HALF = NB / 2;                     // columns that one finishing warp holds at most
@@ -310,10 +346,10 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
         prefetch_map(&rows);
     }
     if (warp == 1) tmem_alloc(smem_addr(&s->tmem), tmem_columns<FP8, DOWN, NB>());
-    // The second launch starts when every CTA of the first has waited for what lay
-    // before it, so only what the first one writes is still to come: the ids, the
-    // weights and their scales are there.
-    if (!DOWN) {
+    // A later launch starts when every CTA of the one before has waited for what lay
+    // before it, so only what that one writes is still to come: the ids, the weights
+    // and their scales are there.
+    if (!LATER) {
         pdl_wait();
         pdl_launch_dependents();
     }
@@ -386,7 +422,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
         load_weights(M, units, INT_MAX);
         if (lane == 0) s->issued[0] = feed.i;
     } else if (warp == kWarps - 1) {  // the pairs' rows
-        if (DOWN) {
+        if (LATER) {
             pdl_wait();
             pdl_launch_dependents();
             proxy_fence();
@@ -395,16 +431,16 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
         int i = 0, st = 0, parity = 1;
         for (int u = U0; ok && u < units; u += G) {
             const Entry en = unpack_entry(entries[u % M]);
-            // x by tokens, four rows a copy (lane n: 4 n and on); h lies in the list's order, 16 a copy
+            // x by tokens, four rows a copy (lane n: 4 n and on); in the list's order 16 a copy
             int4 r = make_int4(0, 0, 0, 0);
-            if constexpr (!DOWN) {
+            if constexpr (!LATER) {
                 int v[4];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) v[n] = list[en.start + min(4 * lane + n, en.n - 1)] / p.k;
                 r = make_int4(v[0], v[1], v[2], v[3]);
             }
-            const int copies = DOWN ? (en.n + 15) >> 4 : (en.n + 3) >> 2;
-            constexpr int COPY = DOWN ? 2048 : 512;
+            const int copies = LATER ? (en.n + 15) >> 4 : (en.n + 3) >> 2;
+            constexpr int COPY = LATER ? 2048 : 512;
             const uint32_t second = ring + 2 * kPanel + (STACKED ? (en.n + 15) & ~15 : NB) * 128;
             for (int kb = K0; kb < K1; ++kb, ++i) {
                 if (i >= S) ok = role_wait(&s->dead, p, smem_addr(&s->empty[st]), parity);
@@ -415,9 +451,10 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                 __syncwarp();
                 if (lane < copies) {
                     const uint32_t b2 = second + st * STAGE + lane * COPY;
-                    if constexpr (DOWN) {
+                    if constexpr (LATER) {
                         map_load2(b + lane * COPY, &rows, kb * KS, en.start + lane * 16, bar);
-                        if constexpr (!FP8) map_load2(b2, &rows, kb * KS, P + en.start + lane * 16, bar);      // the lower parts
+                        // the other step of K, or the lower parts of h
+                        if constexpr (!FP8) map_load2(b2, &rows, kb * KS + (GATES ? KE : 0), (DOWN ? P : 0) + en.start + lane * 16, bar);
                     } else {
                         map_gather4(b + lane * COPY, &rows, kb * KS, r, bar);
                         if constexpr (!FP8) map_gather4(b2, &rows, kb * KS + KE, r, bar);
@@ -474,7 +511,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             mbar_wait(smem_addr(&s->drain), 0);
         }
     } else {                          // the ends of the units
-        if (DOWN) pdl_wait();
+        if (LATER) pdl_wait();
         const int quad = warp & 3, side = (warp - 2) >> 2, row = quad * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + side * 8;
         int uses = 0;
@@ -819,6 +856,7 @@ int shared_bytes(int columns) {
     return static_cast<int>(columns == 16 ? sizeof(Shared<FP8, 16>) : columns == 32 ? sizeof(Shared<FP8, 32>)
                             : columns == 64 ? sizeof(Shared<FP8, 64>) : sizeof(Shared<FP8, 128>));
 }
+int shared_bytes(const MoeLayerShape& s) { return s.fp8 ? shared_bytes<true>(s.columns) : shared_bytes<false>(s.columns); }
 
 bool encode(void* encoder, CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint32_t* box) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -858,7 +896,7 @@ void moe_layer_choose(MoeLayerShape& s) {
     if (want > s.T) want = s.T;
     s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
     s.entries = (most_entries(s) + 3) & ~3;
-    const int behind = (s.fp8 ? shared_bytes<true>(s.columns) : shared_bytes<false>(s.columns)) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
+    const int behind = shared_bytes(s) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
     const int stage = 2 * kPanel + s.columns * 128 * (s.fp8 ? 1 : 2);
     s.stages = (kMaxSmem - 1024 - behind) / stage;
     if (s.stages > kRingStages) s.stages = kRingStages;
@@ -866,7 +904,8 @@ void moe_layer_choose(MoeLayerShape& s) {
     s.act = 0;
     s.act_sf = align256(P * s.I * (s.fp8 ? 1 : 4));
     s.y = s.act_sf + (s.fp8 ? align256(P * (s.I / 128) * 4) : 0);
-    s.parts = s.y + align256(P * s.H * 4);
+    s.rows = s.y + align256(P * s.H * 4);
+    s.parts = s.rows + (copied(s.fp8, s.columns) ? align256(P * s.H * 2) : 0);
 }
 
 void* moe_layer_encoder() {
@@ -883,7 +922,8 @@ void* moe_layer_encoder() {
     return fn;
 }
 
-static cudaError_t prepare(Kernel kernel) {
+template <typename F>
+static cudaError_t prepare(F* kernel) {
     const void* k = reinterpret_cast<const void*>(kernel);
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, k);
@@ -930,6 +970,10 @@ cudaError_t moe_layer_prepare(MoeLayerShape& s, int sms) {
         }
         if (s.cluster[down] == 1 && (e = prepare(kernel_for(s, down != 0, false))) != cudaSuccess) return e;
     }
+    if (copied(s.fp8, s.columns)) {
+        const cudaError_t e = prepare(moe_rows_kernel);
+        if (e != cudaSuccess) return e;
+    }
     return preload(moe_sum_kernel);
 }
 
@@ -943,13 +987,21 @@ cudaError_t moe_layer_launch(const MoeLayerShape& s, const MoeParams& p, const v
     const uint32_t row[] = {ke, 1}, box13[] = {ke, static_cast<uint32_t>(s.fp8 ? kMoeRows : kMoeRows / 2), 1}, box2[] = {ke, kMoeRows, 1};
     const uint32_t rows16[] = {ke, 16};
     CUtensorMap mx, m13, ma, m2;
-    if (!encode(enc, &mx, s.fp8, 2, x, dx, row) || !encode(enc, &m13, s.fp8, 3, w13, d13, box13) ||
+    const bool copy = copied(s.fp8, s.columns);
+    const uint64_t dr[] = {H, static_cast<uint64_t>(s.T) * s.k};
+    if (!encode(enc, &mx, s.fp8, 2, copy ? p.rows : x, copy ? dr : dx, copy ? rows16 : row) || !encode(enc, &m13, s.fp8, 3, w13, d13, box13) ||
         !encode(enc, &ma, s.fp8, 2, p.act, da, rows16) || !encode(enc, &m2, s.fp8, 3, w2, d2, box2))
         return cudaErrorInvalidValue;
     MoeParams up = p, down = p;
     up.cluster = s.cluster[0];
     down.cluster = s.cluster[1];
-    cudaError_t e = layer_launch(kernel_for(s, false, up.cluster > 1), s.grid[0], kMoeThreads, s.smem, up.cluster, pdl, st, up, m13, mx);
+    cudaError_t e = cudaSuccess;
+    if (copy) {
+        const int pairs = s.T * s.k, smem = shared_bytes(s) + s.entries * 4 + (kWarps + 1) * s.E * 4 + pairs * 8;
+        e = layer_launch(moe_rows_kernel, std::min(s.grid[0], (pairs + kWarps - 1) / kWarps),
+                         kMoeThreads, smem, 1, pdl, st, p, static_cast<const uint8_t*>(x));
+    }
+    if (e == cudaSuccess) e = layer_launch(kernel_for(s, false, up.cluster > 1), s.grid[0], kMoeThreads, s.smem, up.cluster, pdl, st, up, m13, mx);
     if (e == cudaSuccess) e = layer_launch(kernel_for(s, true, down.cluster > 1), s.grid[1], kMoeThreads, s.smem, down.cluster, pdl, st, down, m2, ma);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};

@@ -30,6 +30,7 @@ struct MoeLayerShape {
     int64_t act;      // [pairs, I] E4M3, or [2, pairs, I] bf16: upper and lower parts; pairs sorted by expert
     int64_t act_sf;   // [pairs, I / 128] FP32 (E4M3)
     int64_t y;        // [pairs, H] FP32
+    int64_t rows;     // [pairs, H] bf16: x in the sorted order, where that is a launch of its own; or nothing
     int64_t parts;    // FP32 sums of units that are divided along K, a CTA's in a row; or nothing
     int64_t bytes;
 };
@@ -43,6 +44,7 @@ struct MoeParams {
     uint8_t* act;
     float* act_sf;
     float* y;
+    uint8_t* rows;
     float* parts;
     uint16_t* out;            // [T, H]
     int* status;

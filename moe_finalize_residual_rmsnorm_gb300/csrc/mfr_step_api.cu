@@ -193,6 +193,7 @@ int moe_small_layer_run(moe_op_t op, const void* x, const float* x_sf, const int
     p.act = ws + s.act;
     p.act_sf = reinterpret_cast<float*>(ws + s.act_sf);
     p.y = reinterpret_cast<float*>(ws + s.y);
+    p.rows = ws + s.rows;
     p.parts = reinterpret_cast<float*>(ws + s.parts);
     p.out = static_cast<uint16_t*>(out);
     p.status = op->status.words;
