@@ -245,6 +245,25 @@ def test_divided_units_captured_and_beside_others(T, H, I, E, k, fp8, pdl):
     layer.check(i)
 
 
+@pytest.mark.parametrize("pdl", [True, False])
+@pytest.mark.parametrize("share", [0.0, 0.5])
+def test_many_pairs_an_expert_captured_with_other_tokens_each_time(share, pdl):
+    T, H, I, E, k = 150, 1032, 136, 4, 2
+    layer = Layer(T, H, I, E, k, enable_pdl=pdl)
+    a, b = inputs(T, H, I, E, k, seed=1, share=share), inputs(T, H, I, E, k, seed=9, skew=1.5)
+    i = {n: t.clone() for n, t in a.items()}
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        layer.run(i)
+        layer.run(i)
+    for src in (a, b, a):
+        for n in i:
+            i[n].copy_(src[n])
+        g.replay()
+        layer.check(src)
+
+
 def test_two_plans_at_once():
     """Calls on two streams, each with its own workspace, sharing the SMs and tensor memory."""
     shapes = [(16, 1024, 512, 16, 4), (100, 512, 256, 8, 8)]
