@@ -116,7 +116,7 @@ struct Shared {
     int scan[kWarps];
     union {
         struct {                      // E4M3
-            float sx[kFinishWarps][NB / 2];   // scales of a warp's columns
+            alignas(16) float sx[kFinishWarps][2][NB / 2];   // factors of a warp's columns, for both accumulators
             uint32_t top[2][4][NB / 2];       // largest magnitudes, by side, warp and column
         };
         // bf16: products that gate and up rows' lanes exchange, by side, turn and column;
@@ -571,7 +571,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
             if constexpr (FP8) {
                 const int HB = (H + 127) / 128, IB = I / 128;        // scale blocks
                 float d0[NB / 16][8], d1[NB / 16][8];
-                float* sx = s->sx[warp - 2];
+                float(*sx)[HALF] = s->sx[warp - 2];
                 const float* from[2]; // this lane's columns' rows of scales
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -613,10 +613,15 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     for (int step = 0; step < AHEAD; ++step) {
                         if (kb0 + step >= K1) break;
                         __syncwarp();
-                        if (lane < HALF) sx[lane] = f0[step];
-                        if (HALF > 32) sx[lane + 32] = f1[step];
+                        if (lane < HALF) {
+                            sx[0][lane] = f0[step] * sw0[step];
+                            sx[1][lane] = f0[step] * sw1[step];
+                        }
+                        if constexpr (HALF > 32) {
+                            sx[0][lane + 32] = f1[step] * sw0[step];
+                            sx[1][lane + 32] = f1[step] * sw1[step];
+                        }
                         __syncwarp();
-                        const float a0 = sw0[step], a1 = sw1[step];
                         ok = role_wait(&s->dead, p, smem_addr(&s->done[uses % TURNS]), uses / TURNS & 1);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
@@ -631,9 +636,8 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                             tmem_wait_load(a, b);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float f = sx[q * 8 + i];
-                                d0[q][i] = fmaf(__uint_as_float(a[i]), f * a0, d0[q][i]);
-                                d1[q][i] = fmaf(__uint_as_float(b[i]), f * a1, d1[q][i]);
+                                d0[q][i] = fmaf(__uint_as_float(a[i]), sx[0][q * 8 + i], d0[q][i]);
+                                d1[q][i] = fmaf(__uint_as_float(b[i]), sx[1][q * 8 + i], d1[q][i]);
                             }
                         }
                         tcgen05_fence_before();
@@ -687,7 +691,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         if (col >= en.n) break;
                         const uint32_t t = max(max(top[0][j], top[1][j]), max(top[2][j], top[3][j]));
                         const float amax = fminf(fmaxf(__uint_as_float(t), kAmaxFloor), FLT_MAX);
-                        sx[j] = 448.f / amax;
+                        sx[0][j] = 448.f / amax;
                         if (quad == 0) p.act_sf[static_cast<int64_t>(en.start + col) * IB + tile] = amax / 448.f;
                     }
                     __syncwarp();
@@ -698,7 +702,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         for (int j = 0; j < 8; ++j) {
                             const int col = q * 16 + side * 8 + j;
                             if (col >= en.n) break;
-                            p.act[static_cast<int64_t>(en.start + col) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[q][j] * sx[q * 8 + j]));
+                            p.act[static_cast<int64_t>(en.start + col) * I + i] = static_cast<uint8_t>(e4m3_rn_sat(d0[q][j] * sx[0][q * 8 + j]));
                         }
                     }
                 }
