@@ -88,11 +88,11 @@ constexpr int accumulators() { return FP8 || DOWN ? 2 : 1; }
 template <bool FP8, bool DOWN, int NB>
 constexpr bool stacked() { return DOWN && !FP8 && NB <= 64; }
 
-// Accumulators in turn: two units', in E4M3 four steps' where tensor memory holds them
-// (128 tokens of 64 experts 287 -> 278 us).
+// Accumulators in turn: two units', in E4M3 four steps' (128 tokens of 64 experts 287 ->
+// 278 us).
 constexpr int kMaxTurns = 4;
 template <bool FP8, int NB>
-constexpr int turns() { return FP8 && NB <= 64 ? 4 : 2; }
+constexpr int turns() { return FP8 ? 4 : 2; }
 
 // Columns of an accumulator, and of all.
 template <bool FP8, bool DOWN, int NB>
@@ -572,13 +572,10 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                 const int HB = (H + 127) / 128, IB = I / 128;        // scale blocks
                 float d0[NB / 16][8], d1[NB / 16][8];
                 float(*sx)[HALF] = s->sx[warp - 2];
-                const float* from[2]; // this lane's columns' rows of scales
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = (lane + 32 * i) & (HALF - 1);
-                    const int at = min((j >> 3) * 16 + side * 8 + (j & 7), en.n - 1);
-                    from[i] = DOWN ? p.act_sf + static_cast<int64_t>(en.start + at) * KB : p.x_sf + static_cast<int64_t>(pairs[at] / p.k) * KB;
-                }
+                // this lane's column's row of scales
+                const int own = lane & (HALF - 1), at_own = min((own >> 3) * 16 + side * 8 + (own & 7), en.n - 1);
+                const float* from = DOWN ? p.act_sf + static_cast<int64_t>(en.start + at_own) * KB
+                                         : p.x_sf + static_cast<int64_t>(pairs[at_own] / p.k) * KB;
                 const float* w0 = DOWN ? p.w2_sf + (static_cast<int64_t>(en.expert) * HB + 2 * tile) * IB
                                        : p.w13_sf + (static_cast<int64_t>(en.expert) * 2 * IB + tile) * HB;
                 const float* w1 = DOWN ? w0 + (2 * tile + 1 < HB ? IB : 0) : w0 + static_cast<int64_t>(IB) * HB;
@@ -588,15 +585,14 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     for (int i = 0; i < 8; ++i) d0[q][i] = d1[q][i] = 0.f;
                 // the scales of four steps, and the next four on their way
                 constexpr int AHEAD = 4;
-                float sw0[AHEAD], sw1[AHEAD], f0[AHEAD], f1[AHEAD], nw0[AHEAD], nw1[AHEAD], n0[AHEAD], n1[AHEAD];
+                float sw0[AHEAD], sw1[AHEAD], f[AHEAD], nw0[AHEAD], nw1[AHEAD], nf[AHEAD];
                 auto load_scales = [&](int kb) {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i) {
                         const int at = min(kb + i, K1 - 1);
                         nw0[i] = __ldg(w0 + at);
                         nw1[i] = __ldg(w1 + at);
-                        n0[i] = __ldcg(from[0] + at);
-                        n1[i] = HALF > 32 ? __ldcg(from[1] + at) : 0.f;
+                        nf[i] = __ldcg(from + at);
                     }
                 };
                 load_scales(K0);
@@ -605,8 +601,7 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                     for (int i = 0; i < AHEAD; ++i) {
                         sw0[i] = nw0[i];
                         sw1[i] = nw1[i];
-                        f0[i] = n0[i];
-                        f1[i] = n1[i];
+                        f[i] = nf[i];
                     }
                     load_scales(kb0 + AHEAD);
 #pragma unroll
@@ -614,12 +609,8 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         if (kb0 + step >= K1) break;
                         __syncwarp();
                         if (lane < HALF) {
-                            sx[0][lane] = f0[step] * sw0[step];
-                            sx[1][lane] = f0[step] * sw1[step];
-                        }
-                        if constexpr (HALF > 32) {
-                            sx[0][lane + 32] = f1[step] * sw0[step];
-                            sx[1][lane + 32] = f1[step] * sw1[step];
+                            sx[0][lane] = f[step] * sw0[step];
+                            sx[1][lane] = f[step] * sw1[step];
                         }
                         __syncwarp();
                         ok = role_wait(&s->dead, p, smem_addr(&s->done[uses % TURNS]), uses / TURNS & 1);
@@ -627,17 +618,25 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         if (!ok) break;
                         tcgen05_fence_after();
                         const uint32_t acc = lanes + uses % TURNS * ACC;
+                        constexpr int TWO = NB > 16 ? 2 : 1;           // groups on their way at once
 #pragma unroll
-                        for (int q = 0; q < NB / 16; ++q) {
-                            if (q >= groups) break;
-                            uint32_t a[8], b[8];
-                            tmem_load8(acc + q * 16, a);
-                            tmem_load8(acc + COLS + q * 16, b);
-                            tmem_wait_load(a, b);
+                        for (int q0 = 0; q0 < NB / 16; q0 += TWO) {
+                            if (q0 >= groups) break;
+                            uint32_t a[TWO][8], b[TWO][8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                d0[q][i] = fmaf(__uint_as_float(a[i]), sx[0][q * 8 + i], d0[q][i]);
-                                d1[q][i] = fmaf(__uint_as_float(b[i]), sx[1][q * 8 + i], d1[q][i]);
+                            for (int n = 0; n < TWO; ++n) {            // one behind the last: columns that nothing uses
+                                tmem_load8(acc + (q0 + n) * 16, a[n]);
+                                tmem_load8(acc + COLS + (q0 + n) * 16, b[n]);
+                            }
+#pragma unroll
+                            for (int n = 0; n < TWO; ++n) {
+                                const int q = q0 + n;
+                                tmem_wait_load(a[n], b[n]);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    d0[q][i] = fmaf(__uint_as_float(a[n][i]), sx[0][q * 8 + i], d0[q][i]);
+                                    d1[q][i] = fmaf(__uint_as_float(b[n][i]), sx[1][q * 8 + i], d1[q][i]);
+                                }
                             }
                         }
                         tcgen05_fence_before();
@@ -685,13 +684,10 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                         if (lane < 8) top[quad][q * 8 + lane] = largest;
                     }
                     group_sync(1 + side, 128);
-#pragma unroll
-                    for (int j = lane; j < HALF; j += 32) {
-                        const int col = (j >> 3) * 16 + side * 8 + (j & 7);
-                        if (col >= en.n) break;
-                        const uint32_t t = max(max(top[0][j], top[1][j]), max(top[2][j], top[3][j]));
+                    if (const int col = (lane >> 3) * 16 + side * 8 + (lane & 7); lane < HALF && col < en.n) {
+                        const uint32_t t = max(max(top[0][lane], top[1][lane]), max(top[2][lane], top[3][lane]));
                         const float amax = fminf(fmaxf(__uint_as_float(t), kAmaxFloor), FLT_MAX);
-                        sx[0][j] = 448.f / amax;
+                        sx[0][lane] = 448.f / amax;
                         if (quad == 0) p.act_sf[static_cast<int64_t>(en.start + col) * IB + tile] = amax / 448.f;
                     }
                     __syncwarp();
@@ -849,7 +845,7 @@ Kernel kernel_for(const MoeLayerShape& s, bool down, bool joint) {
         case 16: return kernel_of<16>(s.fp8, down, joint);
         case 32: return kernel_of<32>(s.fp8, down, joint);
         case 64: return kernel_of<64>(s.fp8, down, joint);
-        default: return kernel_of<128>(s.fp8, down, joint);
+        default: return kernel_of<false, 128>(down, joint);
     }
 }
 
@@ -898,7 +894,9 @@ void moe_layer_choose(MoeLayerShape& s) {
     const double mean = static_cast<double>(P) / s.E;
     int64_t want = static_cast<int64_t>(mean + 3.0 * std::sqrt(mean) + 4.0);
     if (want > s.T) want = s.T;
-    s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
+    // E4M3: 64 at most, whose accumulators and sums a finishing warp holds in registers
+    // (256 tokens of 16 experts of 4096 x 1024: 215 us with 128, 98 with 64)
+    s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 || s.fp8 ? 64 : 128;
     s.entries = (most_entries(s) + 3) & ~3;
     const int behind = shared_bytes(s) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
     const int stage = 2 * kPanel + s.columns * 128 * (s.fp8 ? 1 : 2);
