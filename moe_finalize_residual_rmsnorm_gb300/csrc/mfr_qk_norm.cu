@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 if (g + i >= g1) break;
+                const bool here = good && i * heads_a_warp < heads;      // this lane's head counts
                 f2 x[8], square = 0;
                 widen<F16>(xa[i], x);
                 widen<F16>(xb[i], x + 4);
@@ -302,7 +303,8 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         x[e] = mul2(x[e], inv2);                      // unit
-                        if (good) sum[e] = fma2(d[e], x[e], sum[e]);
+                        // zeros of a lane without a head are NaN here when eps is 0
+                        if (here) sum[e] = fma2(d[e], x[e], sum[e]);
                         d[e] = mul2(d[e], gamma[e]);
                         dot2 = fma2(d[e], x[e], dot2);
                     }
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(32 * kQkWarps, GRAD ? kQkGradCtas : kQkCtas) q
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = mul2(inv2, fma2(x[e], less, d[e]));
                 }
-                if (good && i * heads_a_warp < heads) {
+                if (here) {
                     if (has_a) st_stream_u4(os + i * o_step + pl.a, narrow<F16>(x));
                     if (has_b) st_stream_u4(os + i * o_step + pl.b, narrow<F16>(x + 4));
                 }
