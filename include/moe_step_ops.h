@@ -109,8 +109,10 @@ int moe_small_layer_run(moe_op_t op, const void* x, const float* x_sf, const int
  * sin = cos_sin[p, rotary / 2 + i] at p = positions[t].
  *  q, k, q_out, k_out  bf16 (fp16 = 1: fp16) [T, heads, D] with strides in elements
  *                      (moe_heads_t), multiples of 8; the D elements of a head lie
- *                      together.  Parts of one packed tensor are fine.  q_out may be
- *                      q and k_out k, with the same strides; other overlaps are refused
+ *                      together.  Parts of one packed tensor are fine: [T, heads_q +
+ *                      heads_k + .., D], or [T, heads, 3, D] with a head's parts side by
+ *                      side.  q_out may be q and k_out k, with the same strides; other
+ *                      overlaps are refused
  *  gamma_q, gamma_k    [D], of the same type
  *  cos_sin             FP32 [max_positions, rotary]
  *  positions           int32 [T].  A token whose position lies outside [0,

@@ -2,6 +2,7 @@
 // launch geometry.
 #include <algorithm>
 #include <cstdlib>
+#include <numeric>
 
 #include "moe_step_ops.h"
 #include "mfr_op.h"
@@ -26,15 +27,31 @@ bool same_heads(const moe_heads_t* a, const moe_heads_t* b) {
     return a->data == b->data && a->token_stride == b->token_stride && a->head_stride == b->head_stride;
 }
 
-// Whether two may share a byte.  Parts of one packed tensor, of the same token
-// stride, are told apart by their places within a token.
+// The heads' first elements lie a multiple of this apart; 0: there is one head.
+int64_t head_pitch(const Heads& a, int64_t T) {
+    return std::gcd(T > 1 ? a.h->token_stride : 0, a.heads > 1 ? a.h->head_stride : 0);
+}
+
+// Where b lies within a's period of `pitch` bytes.
+int64_t offset_within(const Heads& a, const Heads& b, int64_t pitch) {
+    const int64_t d = (reinterpret_cast<intptr_t>(b.h->data) - reinterpret_cast<intptr_t>(a.h->data)) % pitch;
+    return d < 0 ? d + pitch : d;
+}
+
+// Whether two may share a byte.  Parts of one packed tensor are told apart by their
+// places within a token (a's heads, then b's), or where heads of both lie between each
+// other, by their places within the pitch that all of them keep.
 bool heads_meet(const Heads& a, const Heads& b, int64_t T, int D) {
     if (!meet({a.h->data, extent_bytes(a, T, D)}, {b.h->data, extent_bytes(b, T, D)})) return false;
-    const int64_t pitch = a.h->token_stride * 2, ra = row_extent(a, D) * 2, rb = row_extent(b, D) * 2;
-    if (T == 1 || a.h->token_stride != b.h->token_stride || ra > pitch || rb > pitch) return true;
-    int64_t d = (reinterpret_cast<intptr_t>(b.h->data) - reinterpret_cast<intptr_t>(a.h->data)) % pitch;
-    if (d < 0) d += pitch;                  // where b's token begins within a's
-    return d < ra || d + rb > pitch;
+    const int64_t token = a.h->token_stride * 2, ra = row_extent(a, D) * 2, rb = row_extent(b, D) * 2, head = int64_t(2) * D;
+    if (T > 1 && a.h->token_stride == b.h->token_stride && ra <= token && rb <= token) {
+        const int64_t d = offset_within(a, b, token);
+        if (d >= ra && d + rb <= token) return false;
+    }
+    const int64_t pitch = std::gcd(head_pitch(a, T), head_pitch(b, T)) * 2;
+    if (pitch == 0) return true;
+    const int64_t d = offset_within(a, b, pitch);
+    return d < head || d + head > pitch;
 }
 
 // `output`: no two heads may share a byte.
