@@ -7,8 +7,9 @@
 // leaves a sum of squares a CTA, the second adds those in a fixed order, each CTA
 // for itself, and scales the pieces from the last to the first, so that what the
 // first launch read last still lies in L2.
-// A thread adds up to 128 squares of a piece in FP32 in four chains; its pieces'
-// sums and everything above are 64 bits.  No atomics: the same bits in every call.
+// A thread adds up to 130 squares of a piece in FP32 in four chains, and where their
+// sum leaves FP32 adds them once more at a smaller scale; its pieces' sums and
+// everything above are 64 bits.  No atomics: the same bits in every call.
 // Measured on GB300: 60 tensors of 700 M elements, 1.85 GB, in place, 859 us: the first
 // launch 252 us (7.3 TB/s), the second 557 (6.65 TB/s, of a copy rate of 6.78).
 #include "moe_step_ops.h"
@@ -132,6 +133,24 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
     return sum;
 }
 
+// This thread's squares of a piece once more, where their FP32 sum is infinite though each
+// of them may be finite: at 2^-8, which 130 of them at most do not leave.
+__device__ __forceinline__ double wide_sum(const void* in, int64_t n, int type, const Piece& q) {
+    const int per = type == MFR_GRAD_F32 ? 4 : 8;
+    float a = 0.f;
+    const auto add = [&](int64_t i) {
+        const float f = element(in, i, type);
+        a = fmaf(f * f, 0x1p-8f, a);
+    };
+#pragma unroll 1
+    for (int64_t at = q.v0 + threadIdx.x; at < q.v1; at += kClipThreads)
+#pragma unroll 1
+        for (int e = 0; e < per; ++e) add(q.head + at * per + e);
+    if (q.first && threadIdx.x < q.head) add(threadIdx.x);
+    if (q.last && q.tail + threadIdx.x < n) add(q.tail + threadIdx.x);
+    return 256.0 * static_cast<double>(a);
+}
+
 template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipCtas) squares_kernel(const __grid_constant__ ClipList<N> l, const ClipParams p) {
     __shared__ double s[kClipThreads / 32];
@@ -173,7 +192,8 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) squares_kernel(const 
             const float f = element(in, q.tail + tid, type);
             a[2] = fmaf(f, f, a[2]);
         }
-        sum += static_cast<double>((a[0] + a[1]) + (a[2] + a[3]));
+        const float chains = (a[0] + a[1]) + (a[2] + a[3]);
+        sum += chains < INFINITY || chains != chains ? static_cast<double>(chains) : wide_sum(in, n, type, q);
     }
     sum = block_sum(sum, s);
     if (tid == 0) p.partial[p.partial_at + blockIdx.x] = sum;
