@@ -73,6 +73,7 @@ constexpr int kFinishWarps = 8;
 constexpr int kPanel = kMoeRows * 128;             // 128 weight rows of 128 bytes of K; a stage has two
 constexpr int kRingStages = 6;
 constexpr float kAmaxFloor = 0x1p-100f;
+constexpr float kBf16Max = 0x1.FEp127f;            // the largest finite bf16 value
 
 // Rows of pairs in a stage.  bf16: two panels, of the two steps of K in a stage of the
 // first launch, or of the two parts of h in the second.
@@ -757,10 +758,11 @@ moe_layer_kernel(const MoeParams p, const __grid_constant__ CUtensorMap weights,
                                 if (col >= en.n) break;
                                 const float h = gates ? swiglu(v0[j], other[j][r]) : swiglu(other[4 + j][r], v0[4 + j]);
                                 const int64_t at = en.start + col;
-                                const __nv_bfloat16 high = __float2bfloat16_rn(h);
+                                const bool finite = fabsf(h) < INFINITY;
+                                // an infinity is whole in its upper part, and no other h is made one
+                                const __nv_bfloat16 high = __float2bfloat16_rn(finite ? fminf(fmaxf(h, -kBf16Max), kBf16Max) : h);
                                 act[at * I + i] = high;
-                                // an infinity is whole in its upper part
-                                act[(at + P) * I + i] = __float2bfloat16_rn(fabsf(h) < INFINITY ? h - __bfloat162float(high) : 0.f);
+                                act[(at + P) * I + i] = __float2bfloat16_rn(finite ? h - __bfloat162float(high) : 0.f);
                             }
                         }
                     }
