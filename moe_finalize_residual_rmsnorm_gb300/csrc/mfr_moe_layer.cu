@@ -30,10 +30,10 @@
 // bf16 calls with many pairs an expert have a launch before these, which copies their rows
 // of x in the sorted order.  Where units are few and long, the CTAs of a cluster take a part of K each.
 // Measured on GB300 (4096 x 1024 weights an expert, bf16, copy rate 6782 GB/s): 16 tokens
-// of 128 experts 304 us (1.0 of the copy rate), 64 of 64 experts 244 us (0.97), one
-// token of 64 experts 38 us (0.78: two launches' starts, sorts and first loads, 8 us); 128
-// tokens of 64 experts of 8192 x 1024 in E4M3 268 us (0.89: 512 units are 3.4 turns of the
-// SMs).  With units for few SMs one SM takes 60-70 GB/s: a stage's eight products are
+// of 128 experts 293 to 320 us (78 to 82 of them chosen; 0.95 to 1.0 of the copy rate), 64 of
+// 64 experts 247 us (0.96), one token of 64 experts 38.5 us (0.77: two launches' starts, sorts
+// and first loads, 8 us); 128 tokens of 64 experts of 8192 x 1024 in E4M3 270 us (0.88: 512
+// units are 3.4 turns of the SMs).  With units for few SMs one SM takes 60-70 GB/s: a stage's eight products are
 // 330 cycles whatever their columns (the weights are read from shared memory for each), and
 // hand-overs 200 more.
 // Not taken: dividing the steps along K evenly over the CTAs, with partial sums put
@@ -51,7 +51,9 @@
 //
 // bf16: h is kept as the sum of two bf16 values (16 bits of it), two products of the
 // same weights, which cost nothing where bytes bound it; rounded once it alone would
-// put the output 1.4 times as far from the exact one as its own rounding does.
+// put the output 1.4 times as far from the exact one as its own rounding does.  So held
+// the output is as far from it as with all 24 bits (0.00166 of its rms), and one in 200
+// is the neighbouring bf16 value of the one that 24 bits give.
 // E4M3: products of 128 columns of K are one accumulation in tensor memory, which
 // the finishing warps scale and add in FP32 registers.
 #include <algorithm>
@@ -267,6 +269,8 @@ __device__ __forceinline__ int sort_few(const MoeParams& p, uint16_t* list, uint
     return __popc(leaders);
 }
 
+// __expf is off by 2 + 1.2 |g| units of 2^-23 at most, which nothing after it shows: h is held to
+// 2^-16, in E4M3 to 2^-4.
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
 // bf16 with many pairs an expert: their rows of x are put in the sorted order by a launch
@@ -897,7 +901,8 @@ void moe_layer_choose(MoeLayerShape& s) {
     int64_t want = static_cast<int64_t>(mean + 3.0 * std::sqrt(mean) + 4.0);
     if (want > s.T) want = s.T;
     // E4M3: 64 at most, whose accumulators and sums a finishing warp holds in registers
-    // (256 tokens of 16 experts of 4096 x 1024: 215 us with 128, 98 with 64)
+    // (256 tokens of 16 experts of 4096 x 1024: 215 us with 128, 98 with 64, 126 where more than
+    // 38 chunks are a third turn of the SMs)
     s.columns = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 || s.fp8 ? 64 : 128;
     s.entries = (most_entries(s) + 3) & ~3;
     const int behind = shared_bytes(s) + s.entries * 4 + static_cast<int>((P * 2 + 15) & ~15);
